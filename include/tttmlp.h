@@ -420,6 +420,234 @@ TTT_API ttt_status ttt_linear_forward_host(const ttt_mlp_desc* desc, const void*
                                            void* workspace, size_t workspace_bytes, ttt_stream_t stream);
 
 /*
+ * ------------------------------------------------------------------------
+ * Sequence operators beside the layer: rotary positions, attention with a
+ * sliding window and a few first tokens that stay visible (training, prefill
+ * and single-token form), and the gated linear recurrence.
+ *
+ * Packed sequences.  Where a call takes `cu`, rows [cu[s], cu[s+1]) of its
+ * arrays are sequence s (0 <= s < n_seq): n_seq + 1 ints in DEVICE memory,
+ * cu[0] = 0, not falling, cu[n_seq] at most the number of rows.  Sequences may
+ * be empty.  Rows from cu[n_seq] on are neither read nor written (they may
+ * hold anything, NaN included).  cu = NULL is one sequence of every row
+ * (n_seq must be 1).  The host cannot see the values: offsets that fall or
+ * leave the array are cut to it, never followed out of bounds, the outputs are
+ * then undefined, and ttt_mlp_status(workspace, stream) returns
+ * TTT_ERR_INVALID_ARG.
+ *
+ * All pointers are device pointers, 16-byte aligned, row strides (ld) count
+ * elements and are multiples of 8.  The calls are asynchronous on `stream`,
+ * allocate nothing, use no streams of their own and can be captured into a
+ * CUDA graph; a workspace serves one call at a time (two graphs or streams
+ * that may overlap need one each).  The same inputs give the same bits.
+ * ------------------------------------------------------------------------
+ */
+
+/*
+ * Rotary positions.  For row t (position p_t), head h and pair i < rot / 2 of
+ * the head's first `rot` columns,
+ *   (y0, y1) = amplitude * (x0 cos u - x1 sin u, x0 sin u + x1 cos u),
+ *   u = p_t * freq_i,  freq_i = base^(-2 i / rot),
+ * where (0, 1) are columns (i, i + rot / 2) for TTT_ROPE_HALF and
+ * (2 i, 2 i + 1) for TTT_ROPE_INTERLEAVED.  Columns from rot on are copied.
+ * The angle is reduced in 64 bits (positions up to 2^31 keep their turns), the
+ * rotation runs in fp32 and is rounded once.
+ *
+ *   scaling   TTT_ROPE_SCALE_NONE.
+ *             TTT_ROPE_SCALE_LINEAR: freq_i / factor.
+ *             TTT_ROPE_SCALE_BASE: base * factor^(rot / (rot - 2)), which
+ *               divides the slowest frequency by `factor` (rot > 2).
+ *             TTT_ROPE_SCALE_RAMP: with r_i = length * freq_i / (2 pi) turns
+ *               over the original length, keep = clamp((r_i - low) /
+ *               (high - low), 0, 1): freq_i * (keep + (1 - keep) / factor).
+ *   inverse   turns by -u with the same amplitude: the transpose, that is the
+ *             gradient with respect to X given the gradient in X's place.
+ *   X, Y      element (t, h, j) at t * ld + h * d + j, dtype x_dtype.  d a
+ *             multiple of 8 up to 256, rot even, 2 <= rot <= d.  Y may be X
+ *             with the same ld (in place).  H heads of a wider array are
+ *             H * d consecutive columns, so the queries and keys of one fused
+ *             projection turn in one call.
+ *   positions int [T] in device memory, or NULL: row t has position pos0 + t
+ *             (computed without 32-bit overflow).
+ */
+typedef enum { TTT_ROPE_HALF = 0, TTT_ROPE_INTERLEAVED = 1 } ttt_rope_layout;
+typedef enum {
+    TTT_ROPE_SCALE_NONE = 0,
+    TTT_ROPE_SCALE_LINEAR = 1,
+    TTT_ROPE_SCALE_BASE = 2,
+    TTT_ROPE_SCALE_RAMP = 3
+} ttt_rope_scaling;
+
+typedef struct {
+    int T, H, d, rot;      /* T >= 0 */
+    ttt_rope_layout layout;
+    ttt_dtype x_dtype;
+    ttt_rope_scaling scaling;
+    double base;           /* > 1 */
+    double factor;         /* >= 1; used unless scaling is NONE */
+    double length, low, high;  /* RAMP: length > 0, 0 <= low < high */
+    double amplitude;      /* finite */
+} ttt_rope_desc;
+
+TTT_API ttt_status ttt_rope(const ttt_rope_desc* desc, const void* X, int ld_x, void* Y, int ld_y,
+                            const int* positions, int pos0, int inverse, ttt_stream_t stream);
+
+/*
+ * Attention with a sliding window and sinks, over packed sequences.  Query i
+ * of a sequence with nq queries and nk keys has position p = nk - nq + i (the
+ * queries are the sequence's last tokens: nq < nk is a prefill behind cached
+ * tokens) and sees key u, 0 <= u < nk, where
+ *   u <= p + right   and   (u >= p - left   or   u < sinks).
+ * right = 0 is causal, left = right a window to both sides (the bidirectional
+ * backbone's); INT_MAX leaves a side open.  Query head h reads key and value
+ * head h / (Hq / Hk).
+ *   Out[i, h] = Xres[i, h] + sum_u softmax_u(scale * q_i . k_u) v_u
+ *   Lse[h, i] = log sum_u exp(scale * q_i . k_u)
+ * A row that sees no key gets Out = Xres (or 0) and Lse = -infinity.
+ * Arithmetic as in ttt_seg_attention: bf16 operands, products accumulated in
+ * fp32, softmax statistics in fp32, the weights rounded to bf16 for the
+ * product with V, one rounding of the result.
+ * A non-finite key, value or query makes the rows that see it (its own row)
+ * NaN and is reported by the status; rows that do not see it are not affected.
+ *
+ *   desc      Tq, Tk rows of the query and key arrays (Tq, Tk >= 0), d = 64,
+ *             Hq a multiple of Hk, left, right, sinks >= 0, scale > 0.
+ *   cu_q, cu_k  packed sequences as above (both or neither).
+ *   Q, K, V   bf16; head h of row t at t * ld + h * 64.  ld_q >= Hq * 64,
+ *             ld_k, ld_v >= Hk * 64.
+ *   Xres      bf16 [Tq, ld_out] residual or NULL; may be Out.
+ *   Out       bf16 [Tq, ld_out], must not overlap Q, K or V.
+ *   Lse       fp32 [Hq, Tq] or NULL (needed for the backward pass).
+ *   workspace ttt_window_attention_workspace_size(desc) bytes, 256-byte
+ *             aligned: the status word, cleared by the call.
+ * TTT_ERR_UNSUPPORTED for d != 64.
+ */
+typedef struct {
+    int Tq, Tk, n_seq, Hq, Hk, d;
+    int left, right, sinks;
+    float scale;
+} ttt_window_desc;
+
+TTT_API size_t ttt_window_attention_workspace_size(const ttt_window_desc* desc);
+TTT_API ttt_status ttt_window_attention(const ttt_window_desc* desc, const int* cu_q, const int* cu_k, const void* Q,
+                                        int ld_q, const void* K, int ld_k, const void* V, int ld_v, const void* Xres,
+                                        void* Out, int ld_out, float* Lse, void* workspace, size_t workspace_bytes,
+                                        ttt_stream_t stream);
+
+/*
+ * Its backward pass: dQ, dK, dV of a scalar loss from dOut (bf16).
+ *   Out       the forward pass's output WITHOUT a residual (Xres = NULL),
+ *             Lse its log-sum-exp (the gradient of a residual is dOut itself).
+ *   dQ [Tq, ld_dq], dK [Tk, ld_dk], dV [Tk, ld_dv]  bf16, overwritten for every
+ *             row of a sequence; keys that no query sees get zeros.  They must
+ *             not overlap the inputs.
+ * P and dS enter their products as bf16; every sum is fp32 in a fixed order
+ * (no atomics; a key head's gradient sums its query heads one after the other).
+ *   workspace ttt_window_attention_backward_workspace_size(desc) bytes.
+ */
+TTT_API size_t ttt_window_attention_backward_workspace_size(const ttt_window_desc* desc);
+TTT_API ttt_status ttt_window_attention_backward(const ttt_window_desc* desc, const int* cu_q, const int* cu_k,
+                                                 const void* Q, int ld_q, const void* K, int ld_k, const void* V,
+                                                 int ld_v, const void* Out, int ld_out, const float* Lse,
+                                                 const void* dOut, int ld_do, void* dQ, int ld_dq, void* dK,
+                                                 int ld_dk, void* dV, int ld_dv, void* workspace,
+                                                 size_t workspace_bytes, ttt_stream_t stream);
+
+/*
+ * Its single-token form, for serving: one query per request on a cache of
+ * `slots` slots per request whose first `sinks` slots hold the first tokens
+ * and whose other slots are a ring.  Position u lives in slot
+ *   u                                     where u < slots,
+ *   sinks + (u - sinks) mod (slots - sinks)  else,
+ * so a cache with slots = sinks + left + 1 serves a sequence of any length and
+ * one with a slot per token never wraps.  The query of request r is the token
+ * at position lens[r] - 1; it sees the keys ttt_window_attention would show it
+ * (right = 0) that are still in the cache.
+ *
+ *   K_new, V_new  bf16 [B, ld_new] or both NULL: the key and value of that
+ *             token; the call stores them in the cache (in their slot) and
+ *             attends to them.  NULL: they are in the cache already.
+ *   K_cache, V_cache  bf16; slot c of request r, head h at
+ *             r * ld_request + c * ld_slot + h * ld_head (64-bit offsets,
+ *             multiples of 8), both caches alike.  Slots that hold no token of
+ *             the sequence are not read (they may hold anything).
+ *   lens      int [B] in device memory, the tokens so far, this one included.
+ *             0: an idle request: Out = 0, nothing is stored.  Negative
+ *             lengths count as 0 and set the status (TTT_ERR_INVALID_ARG).
+ *   Q, Out    bf16 [B, ld].  No two requests may share cache slots.
+ *   workspace ttt_window_attention_decode_workspace_size(desc) bytes, 256-byte
+ *             aligned.  The caller zeroes it once after allocating it; the
+ *             call does not clear the status word (one launch less), which
+ *             collects until ttt_mlp_status reads and clears it.
+ * A cache with slots <= sinks has no ring: it serves lengths up to `slots`,
+ * longer ones count as 0 and set the status.  d = 64.
+ */
+typedef struct {
+    int B, Hq, Hk, d, slots, left, sinks;
+    float scale;
+    long long ld_request, ld_slot, ld_head;
+} ttt_window_decode_desc;
+
+TTT_API size_t ttt_window_attention_decode_workspace_size(const ttt_window_decode_desc* desc);
+TTT_API ttt_status ttt_window_attention_decode(const ttt_window_decode_desc* desc, const void* Q, int ld_q,
+                                               const void* K_new, const void* V_new, int ld_new, void* K_cache,
+                                               void* V_cache, const int* lens, void* Out, int ld_out,
+                                               void* workspace, size_t workspace_bytes, ttt_stream_t stream);
+
+/*
+ * Gated linear recurrence, per channel and packed sequence, in walking order
+ * (TTT_FWD: rising rows, TTT_REV: falling rows):
+ *   a_t = sigmoid(f_t),   h_t = a_t h_{t-1} + s(a_t) x_t,   Y_t = h_t,
+ *   s = 1 (TTT_GATE_SUM), 1 - a (TTT_GATE_CONVEX) or sqrt(1 - a^2)
+ *   (TTT_GATE_UNIT),   h before a sequence's first row = H_0 (or 0).
+ * 1 - a is computed as sigmoid(-f), so long memories keep their input's scale.
+ * Gates and states are fp32 whatever x_dtype; Y is rounded once.
+ *
+ *   F, X, Y   [T, ld], D columns, dtype x_dtype; D a multiple of 8.  Y must not
+ *             overlap F or X.
+ *   H_0, H_T  fp32 [n_seq, D], each may be NULL; H_T receives the state after
+ *             each sequence's last row (H_0, or 0, for an empty sequence).
+ *   chunk_states  NULL, or ttt_gated_scan_chunk_states_size(desc) bytes: what
+ *             the backward pass needs besides the inputs.
+ *   workspace ttt_gated_scan_workspace_size(desc) bytes, 256-byte aligned;
+ *             ttt_mlp_status reports non-finite outputs, bad offsets and
+ *             expired waits.
+ * dir is TTT_FWD or TTT_REV.
+ *
+ * Backward: from dY (x_dtype, [T, ld_dy]) and optionally dH_T (fp32
+ * [n_seq, D]), dF and dX (x_dtype) and optionally dH_0 (fp32 [n_seq, D]):
+ *   l_t = dY_t + a_{t+1} l_{t+1}  (dH_T joins at the last row),
+ *   dF_t = l_t (h_{t-1} a (1 - a) + x_t ds/df),  dX_t = l_t s(a_t),
+ *   dH_0 = a l at the first row,
+ * with h recomputed in fp32 from the chunk states.  The same workspace size.
+ *
+ * Step, for serving: one token of each of B rows: H_out = a H + s(a) x (fp32
+ * [B, D] dense; H_out may be H), Y (may be NULL) = H_out rounded.
+ */
+typedef enum { TTT_GATE_SUM = 0, TTT_GATE_CONVEX = 1, TTT_GATE_UNIT = 2 } ttt_gate_form;
+
+typedef struct {
+    int T, D, n_seq;       /* T >= 0 */
+    ttt_gate_form form;
+    ttt_direction dir;
+    ttt_dtype x_dtype;
+} ttt_gated_scan_desc;
+
+TTT_API size_t ttt_gated_scan_workspace_size(const ttt_gated_scan_desc* desc);
+TTT_API size_t ttt_gated_scan_chunk_states_size(const ttt_gated_scan_desc* desc);
+TTT_API ttt_status ttt_gated_scan(const ttt_gated_scan_desc* desc, const int* cu, const void* F, int ld_f,
+                                  const void* X, int ld_x, const float* H_0, void* Y, int ld_y, float* H_T,
+                                  void* chunk_states, void* workspace, size_t workspace_bytes, ttt_stream_t stream);
+TTT_API ttt_status ttt_gated_scan_backward(const ttt_gated_scan_desc* desc, const int* cu, const void* F, int ld_f,
+                                           const void* X, int ld_x, const float* H_0, const void* chunk_states,
+                                           const void* dY, int ld_dy, const float* dH_T, void* dF, int ld_df,
+                                           void* dX, int ld_dx, float* dH_0, void* workspace,
+                                           size_t workspace_bytes, ttt_stream_t stream);
+TTT_API ttt_status ttt_gated_scan_step(int B, int D, ttt_gate_form form, ttt_dtype x_dtype, const void* F, int ld_f,
+                                       const void* X, int ld_x, const float* H, float* H_out, void* Y, int ld_y,
+                                       ttt_stream_t stream);
+
+/*
  * Fault injection for tests (process-wide).  While enabled, the two-CTA
  * tensor-core scan kernel (the default for bf16 inputs) first waits on an
  * mbarrier that nothing arrives on, with a 1 ms limit; the wait expires, the

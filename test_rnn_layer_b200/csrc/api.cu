@@ -1116,6 +1116,8 @@ ttt_status ttt_mlp_status(void* workspace, ttt_stream_t stream_) {
     CUDA_TRY(cudaMemcpy(&word, workspace, sizeof(int), cudaMemcpyDeviceToHost));
     CUDA_TRY(cudaMemset(workspace, 0, sizeof(int)));
     if (word & kStatusTimeout) return fail(TTT_ERR_TIMEOUT, "a bounded wait inside a scan kernel expired");
+    if (word & kStatusBadOffsets)
+        return fail(TTT_ERR_INVALID_ARG, "sequence offsets or lengths in device memory fall or leave the arrays");
     if (word & kStatusNonFinite)
         return fail(TTT_ERR_NONFINITE, "non-finite values in the inputs, projections or outputs");
     return TTT_OK;

@@ -10,7 +10,7 @@
 namespace ttt {
 
 // Status bits a kernel may set in the workspace status word.
-enum : int { kStatusNonFinite = 1, kStatusTimeout = 2 };
+enum : int { kStatusNonFinite = 1, kStatusTimeout = 2, kStatusBadOffsets = 4 };
 
 // Token-stream and gate arguments of one direction's scan.  Element (h, t, j)
 // of a [H, T, d]-style stream lives at base + h * hs + t * ts + j; the same
@@ -167,6 +167,79 @@ cudaError_t launch_gate_backward(const float* g, const float* z, const float* al
 cudaError_t launch_grad_gemm(float* C, long long ldc, long long cbs, const void* A, int a_bf16, long long a_rs,
                              long long a_cs, long long a_bs, const void* B, int b_bf16, long long b_rs, long long b_cs,
                              long long b_bs, int batch, int M, int N, long long K, int accumulate, cudaStream_t s);
+
+// Rotary positions of H heads of width d (turns[i]: turns per position of pair i, 64 bits).
+constexpr int kRopeMaxPairs = 128;
+struct RopeArgs {
+    const void* X;
+    void* Y;
+    long long ld_x, ld_y;
+    const int* positions;
+    long long pos0;
+    int T, H, d, rot, half, bf16, inverse;
+    float amplitude;
+    double turns[kRopeMaxPairs];
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+
+// Window attention with sinks over packed sequences (d = 64, bf16).
+struct WindowArgs {
+    int Tq, Tk, n_seq, Hq, Hk, left, right, sinks;
+    float scale;
+    const int *cu_q, *cu_k;   // device, or null: one sequence of every row
+    const __nv_bfloat16 *Q, *K, *V;
+    long long ld_q, ld_k, ld_v;
+    const __nv_bfloat16* Xres;   // forward: residual (ld_out)
+    __nv_bfloat16* Out;          // forward output; the backward pass reads it
+    long long ld_out;
+    float* Lse;
+    int* status;
+    // backward
+    const __nv_bfloat16* dOut;
+    __nv_bfloat16 *dQ, *dK, *dV;
+    long long ld_do, ld_dq, ld_dk, ld_dv;
+    float* delta;                // [Hq, Tq] scratch: rowsum(dOut * Out)
+};
+cudaError_t launch_window_attention(const WindowArgs& a, cudaStream_t s);
+cudaError_t launch_window_attention_backward(const WindowArgs& a, cudaStream_t s);
+
+struct WindowDecodeArgs {
+    int B, Hq, Hk, slots, left, sinks;
+    float scale;
+    long long ld_request, ld_slot, ld_head;
+    const __nv_bfloat16 *Q, *K_new, *V_new;
+    long long ld_q, ld_new, ld_out;
+    __nv_bfloat16 *K_cache, *V_cache, *Out;
+    const int* lens;
+    int* status;
+};
+cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t s);
+
+// Gated linear recurrence (forward, backward, one token).
+struct GatedScanArgs {
+    int T, D, n_seq, form, reverse, bf16;
+    const int* cu;
+    const void *F, *X;
+    long long ld_f, ld_x;
+    const float* H_0;
+    void* Y;                  // forward
+    long long ld_y;
+    float* H_T;
+    float* chunk_states;
+    const void* dY;           // backward
+    long long ld_dy, ld_df, ld_dx;
+    const float* dH_T;
+    void *dF, *dX;
+    float* dH_0;
+    int* status;              // the workspace: status word first
+};
+long long gated_scan_workspace_bytes(int T, int D);      // after the status word
+long long gated_scan_chunk_state_floats(int T, int D);
+cudaError_t launch_gated_scan(const GatedScanArgs& a, cudaStream_t s);
+cudaError_t launch_gated_scan_backward(const GatedScanArgs& a, cudaStream_t s);
+cudaError_t launch_gated_scan_step(int B, int D, int form, int bf16, const void* F, long long ld_f, const void* X,
+                                   long long ld_x, const float* H, float* H_out, void* Y, long long ld_y,
+                                   cudaStream_t s);
 
 // Records a message for ttt_last_error() on this thread and returns `code`.
 ttt_status set_error(ttt_status code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));

@@ -30,13 +30,47 @@ EXPORTED = ["ttt_mlp_workspace_size", "ttt_mlp_forward", "ttt_mlp_status", "ttt_
             "ttt_mlp_backward_workspace_size", "ttt_mlp_backward", "ttt_mlp_heads_workspace_size",
             "ttt_mlp_forward_heads", "ttt_seg_attention_workspace_size", "ttt_seg_attention",
             "ttt_block_workspace_size", "ttt_block_forward", "ttt_debug_set_block_front",
-            "ttt_linear_host_io_workspace_size", "ttt_linear_forward_host", "ttt_debug_set_backward_ctas"]
+            "ttt_linear_host_io_workspace_size", "ttt_linear_forward_host", "ttt_debug_set_backward_ctas",
+            "ttt_rope", "ttt_window_attention_workspace_size", "ttt_window_attention",
+            "ttt_window_attention_backward_workspace_size", "ttt_window_attention_backward",
+            "ttt_window_attention_decode_workspace_size", "ttt_window_attention_decode",
+            "ttt_gated_scan_workspace_size", "ttt_gated_scan_chunk_states_size", "ttt_gated_scan",
+            "ttt_gated_scan_backward", "ttt_gated_scan_step"]
 
 
 class TTTError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}: {ttt_last_error()}")
+
+
+TTT_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+TTT_ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
+TTT_GATE_FORMS = {"sum": 0, "convex": 1, "unit": 2}
+
+
+class ttt_rope_desc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("H", ctypes.c_int), ("d", ctypes.c_int), ("rot", ctypes.c_int),
+                ("layout", ctypes.c_int), ("x_dtype", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double), ("length", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class ttt_window_desc(ctypes.Structure):
+    _fields_ = [("Tq", ctypes.c_int), ("Tk", ctypes.c_int), ("n_seq", ctypes.c_int), ("Hq", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("d", ctypes.c_int), ("left", ctypes.c_int), ("right", ctypes.c_int),
+                ("sinks", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class ttt_window_decode_desc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int), ("d", ctypes.c_int),
+                ("slots", ctypes.c_int), ("left", ctypes.c_int), ("sinks", ctypes.c_int), ("scale", ctypes.c_float),
+                ("ld_request", ctypes.c_longlong), ("ld_slot", ctypes.c_longlong), ("ld_head", ctypes.c_longlong)]
+
+
+class ttt_gated_scan_desc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("D", ctypes.c_int), ("n_seq", ctypes.c_int), ("form", ctypes.c_int),
+                ("dir", ctypes.c_int), ("x_dtype", ctypes.c_int)]
 
 
 class ttt_mlp_desc(ctypes.Structure):
@@ -102,6 +136,24 @@ def lib():
         L.ttt_linear_forward_host.argtypes = [dp, vp, vp, vp, vp, vp, f, i, i, vp, vp, vp, vp, sz, vp]
         L.ttt_linear_forward.restype = i
         L.ttt_linear_forward.argtypes = [dp, vp, vp, vp, vp, vp, f, i, i, vp, vp, vp, vp, vp, vp, sz, vp]
+        rp, wp, ep, gp = (ctypes.POINTER(c) for c in (ttt_rope_desc, ttt_window_desc, ttt_window_decode_desc,
+                                                      ttt_gated_scan_desc))
+        for name, res, args in (
+                ("ttt_rope", i, [rp, vp, i, vp, i, vp, i, i, vp]),
+                ("ttt_window_attention_workspace_size", sz, [wp]),
+                ("ttt_window_attention", i, [wp, vp, vp, vp, i, vp, i, vp, i, vp, vp, i, vp, vp, sz, vp]),
+                ("ttt_window_attention_backward_workspace_size", sz, [wp]),
+                ("ttt_window_attention_backward", i, [wp, vp, vp, vp, i, vp, i, vp, i, vp, i, vp, vp, i, vp, i, vp, i,
+                                                      vp, i, vp, sz, vp]),
+                ("ttt_window_attention_decode_workspace_size", sz, [ep]),
+                ("ttt_window_attention_decode", i, [ep, vp, i, vp, vp, i, vp, vp, vp, vp, i, vp, sz, vp]),
+                ("ttt_gated_scan_workspace_size", sz, [gp]),
+                ("ttt_gated_scan_chunk_states_size", sz, [gp]),
+                ("ttt_gated_scan", i, [gp, vp, vp, i, vp, i, vp, vp, i, vp, vp, vp, sz, vp]),
+                ("ttt_gated_scan_backward", i, [gp, vp, vp, i, vp, i, vp, vp, vp, i, vp, vp, i, vp, i, vp, vp, sz, vp]),
+                ("ttt_gated_scan_step", i, [i, i, i, i, vp, i, vp, i, vp, vp, vp, i, vp])):
+            fn = getattr(L, name)
+            fn.restype, fn.argtypes = res, args
         L.ttt_mlp_status.restype = i
         L.ttt_mlp_status.argtypes = [vp, vp]
         L.ttt_mlp_select_kernels.restype = i
@@ -408,3 +460,359 @@ def linear_layer_forward(X, theta_q, theta_k, theta_v, W_0, eta: float, b: int, 
         out["status"] = st
         check(st, "ttt_mlp_status")
     return out
+
+
+# ------------------------------------------------------------------ sequence operators
+# The C entry points of the same names (pointers as tensors or integers), then
+# tensor-level functions that take row strides from the tensors' own, allocate
+# what is not given and run on the tensors' device.
+def ttt_rope(desc, X, ld_x, Y, ld_y, positions, pos0, inverse, stream=None) -> int:
+    return int(lib().ttt_rope(ctypes.byref(desc), _p(X), ld_x, _p(Y), ld_y, _p(positions), pos0, int(inverse),
+                              _stream(stream)))
+
+
+def ttt_window_attention_workspace_size(desc) -> int:
+    return int(lib().ttt_window_attention_workspace_size(ctypes.byref(desc)))
+
+
+def ttt_window_attention(desc, cu_q, cu_k, Q, ld_q, K, ld_k, V, ld_v, Xres, Out, ld_out, Lse, workspace,
+                         workspace_bytes, stream=None) -> int:
+    return int(lib().ttt_window_attention(ctypes.byref(desc), _p(cu_q), _p(cu_k), _p(Q), ld_q, _p(K), ld_k, _p(V),
+                                          ld_v, _p(Xres), _p(Out), ld_out, _p(Lse), _p(workspace), workspace_bytes,
+                                          _stream(stream)))
+
+
+def ttt_window_attention_backward_workspace_size(desc) -> int:
+    return int(lib().ttt_window_attention_backward_workspace_size(ctypes.byref(desc)))
+
+
+def ttt_window_attention_backward(desc, cu_q, cu_k, Q, ld_q, K, ld_k, V, ld_v, Out, ld_out, Lse, dOut, ld_do, dQ,
+                                  ld_dq, dK, ld_dk, dV, ld_dv, workspace, workspace_bytes, stream=None) -> int:
+    return int(lib().ttt_window_attention_backward(ctypes.byref(desc), _p(cu_q), _p(cu_k), _p(Q), ld_q, _p(K), ld_k,
+                                                   _p(V), ld_v, _p(Out), ld_out, _p(Lse), _p(dOut), ld_do, _p(dQ),
+                                                   ld_dq, _p(dK), ld_dk, _p(dV), ld_dv, _p(workspace),
+                                                   workspace_bytes, _stream(stream)))
+
+
+def ttt_window_attention_decode_workspace_size(desc) -> int:
+    return int(lib().ttt_window_attention_decode_workspace_size(ctypes.byref(desc)))
+
+
+def ttt_window_attention_decode(desc, Q, ld_q, K_new, V_new, ld_new, K_cache, V_cache, lens, Out, ld_out, workspace,
+                                workspace_bytes, stream=None) -> int:
+    return int(lib().ttt_window_attention_decode(ctypes.byref(desc), _p(Q), ld_q, _p(K_new), _p(V_new), ld_new,
+                                                 _p(K_cache), _p(V_cache), _p(lens), _p(Out), ld_out, _p(workspace),
+                                                 workspace_bytes, _stream(stream)))
+
+
+def ttt_gated_scan_workspace_size(desc) -> int:
+    return int(lib().ttt_gated_scan_workspace_size(ctypes.byref(desc)))
+
+
+def ttt_gated_scan_chunk_states_size(desc) -> int:
+    return int(lib().ttt_gated_scan_chunk_states_size(ctypes.byref(desc)))
+
+
+def ttt_gated_scan(desc, cu, F, ld_f, X, ld_x, H_0, Y, ld_y, H_T, chunk_states, workspace, workspace_bytes,
+                   stream=None) -> int:
+    return int(lib().ttt_gated_scan(ctypes.byref(desc), _p(cu), _p(F), ld_f, _p(X), ld_x, _p(H_0), _p(Y), ld_y,
+                                    _p(H_T), _p(chunk_states), _p(workspace), workspace_bytes, _stream(stream)))
+
+
+def ttt_gated_scan_backward(desc, cu, F, ld_f, X, ld_x, H_0, chunk_states, dY, ld_dy, dH_T, dF, ld_df, dX, ld_dx,
+                            dH_0, workspace, workspace_bytes, stream=None) -> int:
+    return int(lib().ttt_gated_scan_backward(ctypes.byref(desc), _p(cu), _p(F), ld_f, _p(X), ld_x, _p(H_0),
+                                             _p(chunk_states), _p(dY), ld_dy, _p(dH_T), _p(dF), ld_df, _p(dX), ld_dx,
+                                             _p(dH_0), _p(workspace), workspace_bytes, _stream(stream)))
+
+
+def ttt_gated_scan_step(B, D, form, x_dtype, F, ld_f, X, ld_x, H, H_out, Y, ld_y, stream=None) -> int:
+    return int(lib().ttt_gated_scan_step(B, D, form, x_dtype, _p(F), ld_f, _p(X), ld_x, _p(H), _p(H_out), _p(Y), ld_y,
+                                         _stream(stream)))
+
+
+class _Place:
+    """Runs a call with the tensors' device current and, if one is given, on `stream`
+    (new tensors then belong to that stream)."""
+
+    def __init__(self, tensor, stream):
+        self.index, self.stream = tensor.device.index, stream
+        self.stack = []
+
+    def __enter__(self):
+        if self.index != torch.cuda.current_device():
+            self.stack.append(torch.cuda.device(self.index))
+        if isinstance(self.stream, torch.cuda.Stream):
+            self.stack.append(torch.cuda.stream(self.stream))
+        for c in self.stack:
+            c.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.stack):
+            c.__exit__(*exc)
+        return False
+
+
+def _ask(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(x, shape, dtype, device, name) -> int:
+    """Row stride of a tensor of `shape` whose rows are dense (checked with its type and device)."""
+    _ask(x.dtype == dtype and x.device == device, f"{name}: {x.dtype} on {x.device}, wanted {dtype} on {device}")
+    _ask(tuple(x.shape) == tuple(shape), f"{name}: shape {tuple(x.shape)}, wanted {tuple(shape)}")
+    width, strides = 1, x.stride()
+    for k in range(len(shape) - 1, 0, -1):
+        _ask(shape[k] <= 1 or strides[k] == width, f"{name}: the columns of a row must be dense, strides {strides}")
+        width *= shape[k]
+    ld = strides[0] if shape[0] > 1 else -(-width // 8) * 8
+    _ask(ld < 2 ** 31, f"{name}: row stride {ld}")
+    return ld
+
+
+def _offsets(cu, device, name):
+    if cu is None:
+        return 1
+    _ask(cu.dtype == torch.int32 and cu.device == device and cu.dim() == 1 and cu.numel() >= 2 and cu.is_contiguous(),
+         f"{name}: a dense int32 vector of n_seq + 1 offsets on {device} is wanted")
+    return cu.numel() - 1
+
+
+def _dense(x, shape, dtype, device, name):
+    _ask(x.dtype == dtype and x.device == device and tuple(x.shape) == tuple(shape) and x.is_contiguous(),
+         f"{name}: a dense {dtype} tensor of shape {tuple(shape)} on {device} is wanted")
+    return x
+
+
+def _space(workspace, n, device):
+    if n == 0:
+        raise TTTError(TTT_ERR_INVALID_ARG, "workspace size")
+    if workspace is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    _ask(workspace.device == device, f"workspace on {workspace.device}, wanted {device}")
+    return workspace
+
+
+def _dtype_code(x, name) -> int:
+    _ask(x.is_cuda and x.dtype in (torch.float32, torch.bfloat16), f"{name}: float32 or bfloat16 on a GPU is wanted")
+    return TTT_BF16 if x.dtype == torch.bfloat16 else TTT_F32
+
+
+def rope(x, positions=None, *, pos0: int = 0, rot: int | None = None, layout: str = "half", base: float = 10000.0,
+         scaling: dict | None = None, inverse: bool = False, out=None, stream=None):
+    """Rotary positions of x [T, H, d] (ttt_rope).  `scaling`: {"kind": "linear" | "base", "factor": f} or
+    {"kind": "ramp", "factor": f, "length": n, "low": l, "high": h}, with "amplitude" optional.  `out` may be x."""
+    code = _dtype_code(x, "x")
+    T, H, d = x.shape
+    sc = scaling or {}
+    known = {"kind", "factor", "length", "low", "high", "amplitude"}
+    _ask(set(sc) <= known and sc.get("kind", "none") in TTT_ROPE_SCALINGS, f"scaling {scaling}")
+    desc = ttt_rope_desc(T, H, d, d if rot is None else rot, TTT_ROPE_LAYOUTS[layout], code,
+                         TTT_ROPE_SCALINGS[sc.get("kind", "none")], base, sc.get("factor", 1.0), sc.get("length", 0.0),
+                         sc.get("low", 0.0), sc.get("high", 0.0), sc.get("amplitude", 1.0))
+    if positions is not None:
+        _dense(positions, (T,), torch.int32, x.device, "positions")
+    with _Place(x, stream):
+        if out is None:
+            out = torch.empty((T, H, d), dtype=x.dtype, device=x.device)
+        check(ttt_rope(desc, x, _rows(x, x.shape, x.dtype, x.device, "x"), out,
+                       _rows(out, x.shape, x.dtype, x.device, "out"), positions, pos0, inverse, stream), "ttt_rope")
+    return out
+
+
+def _window_desc(q, k, n_seq, left, right, sinks, scale):
+    _ask(q.is_cuda and q.dim() == 3 and k.dim() == 3, "q and k: [T, H, 64] on a GPU")
+    return ttt_window_desc(q.shape[0], k.shape[0], n_seq, q.shape[1], k.shape[1], q.shape[2], left, right, sinks,
+                           q.shape[2] ** -0.5 if scale is None else scale)
+
+
+def window_attention_workspace(q, k, n_seq: int = 1, backward: bool = False) -> torch.Tensor:
+    """A workspace that window_attention (and, with backward, window_attention_backward) can use."""
+    desc = _window_desc(q, k, n_seq, 0, 0, 0, None)
+    n = (ttt_window_attention_backward_workspace_size if backward else ttt_window_attention_workspace_size)(desc)
+    return _space(None, n, q.device)
+
+
+def window_attention(q, k, v, *, left: int, right: int = 0, sinks: int = 0, cu_q=None, cu_k=None, scale=None,
+                     residual=None, out=None, lse=None, want_lse: bool = False, workspace=None,
+                     check_status: bool = True, stream=None) -> dict:
+    """Window attention of q [Tq, Hq, 64] on k, v [Tk, Hk, 64] (ttt_window_attention)."""
+    dev, bf = q.device, torch.bfloat16
+    n_seq = _offsets(cu_q, dev, "cu_q")
+    _ask((cu_q is None) == (cu_k is None) and _offsets(cu_k, dev, "cu_k") == n_seq,
+         "cu_q and cu_k: both or neither, of the same length")
+    desc = _window_desc(q, k, n_seq, left, right, sinks, scale)
+    lds = [_rows(q, q.shape, bf, dev, "q"), _rows(k, k.shape, bf, dev, "k"), _rows(v, k.shape, bf, dev, "v")]
+    with _Place(q, stream):
+        ws = _space(workspace, ttt_window_attention_workspace_size(desc), dev)
+        if out is None:   # rows outside the sequences are not written: they start as zeros
+            out = (torch.empty if cu_q is None else torch.zeros)(q.shape, dtype=bf, device=dev)
+        if lse is None and want_lse:
+            lse = (torch.empty if cu_q is None else torch.zeros)((q.shape[1], q.shape[0]), device=dev)
+        if lse is not None:
+            _dense(lse, (q.shape[1], q.shape[0]), torch.float32, dev, "lse")
+        ld_out = _rows(out, q.shape, bf, dev, "out")
+        if residual is not None:
+            _ask(_rows(residual, q.shape, bf, dev, "residual") == ld_out, "residual and out need the same row stride")
+        check(ttt_window_attention(desc, cu_q, cu_k, q, lds[0], k, lds[1], v, lds[2], residual, out, ld_out, lse, ws,
+                                   ws.numel(), stream), "ttt_window_attention")
+        if check_status:
+            check(ttt_mlp_status(ws, stream), "ttt_mlp_status")
+    return {"out": out, "lse": lse, "workspace": ws}
+
+
+def window_attention_backward(q, k, v, out, lse, dout, *, left: int, right: int = 0, sinks: int = 0, cu_q=None,
+                              cu_k=None, scale=None, dq=None, dk=None, dv=None, workspace=None,
+                              check_status: bool = True, stream=None) -> dict:
+    """Gradients of window_attention (without a residual) from its out and lse (ttt_window_attention_backward)."""
+    dev, bf = q.device, torch.bfloat16
+    n_seq = _offsets(cu_q, dev, "cu_q")
+    _ask((cu_q is None) == (cu_k is None) and _offsets(cu_k, dev, "cu_k") == n_seq,
+         "cu_q and cu_k: both or neither, of the same length")
+    desc = _window_desc(q, k, n_seq, left, right, sinks, scale)
+    _dense(lse, (q.shape[1], q.shape[0]), torch.float32, dev, "lse")
+    with _Place(q, stream):
+        ws = _space(workspace, ttt_window_attention_backward_workspace_size(desc), dev)
+        new = torch.empty if cu_q is None else torch.zeros
+        dq = new(q.shape, dtype=bf, device=dev) if dq is None else dq
+        dk = new(k.shape, dtype=bf, device=dev) if dk is None else dk
+        dv = new(k.shape, dtype=bf, device=dev) if dv is None else dv
+        ld = {n: _rows(t, (q if n in ("q", "out", "dout", "dq") else k).shape, bf, dev, n)
+              for n, t in dict(q=q, k=k, v=v, out=out, dout=dout, dq=dq, dk=dk, dv=dv).items()}
+        check(ttt_window_attention_backward(desc, cu_q, cu_k, q, ld["q"], k, ld["k"], v, ld["v"], out, ld["out"], lse,
+                                            dout, ld["dout"], dq, ld["dq"], dk, ld["dk"], dv, ld["dv"], ws,
+                                            ws.numel(), stream), "ttt_window_attention_backward")
+        if check_status:
+            check(ttt_mlp_status(ws, stream), "ttt_mlp_status")
+    return {"dq": dq, "dk": dk, "dv": dv, "workspace": ws}
+
+
+def _decode_desc(q, cache, left, sinks, scale):
+    _ask(q.is_cuda and q.dim() == 3 and cache.dim() == 4 and cache.shape[0] == q.shape[0] and
+         cache.shape[3] == q.shape[2], "q [B, Hq, 64] and a cache [B, slots, Hk, 64] on a GPU")
+    _ask(cache.stride(3) == 1, "the cache's last axis must be dense")
+    B, slots, Hk, d = cache.shape
+    return ttt_window_decode_desc(B, q.shape[1], Hk, d, slots, left, sinks, d ** -0.5 if scale is None else scale,
+                                  cache.stride(0), cache.stride(1) if slots > 1 else d, cache.stride(2))
+
+
+def window_attention_decode_workspace(q, cache) -> torch.Tensor:
+    """A zeroed workspace for window_attention_decode."""
+    n = ttt_window_attention_decode_workspace_size(_decode_desc(q, cache, 0, 0, None))
+    return _space(None, n, q.device).zero_()
+
+
+def window_attention_decode(q, cache_k, cache_v, lens, *, left: int, sinks: int = 0, scale=None, k_new=None,
+                            v_new=None, out=None, workspace=None, check_status: bool = True, stream=None) -> dict:
+    """One token of each request on its cache (ttt_window_attention_decode): q [B, Hq, 64], caches
+    [B, slots, Hk, 64] with any strides, lens int32 [B]; k_new, v_new [B, Hk, 64] are stored first.
+    A given workspace must have been zeroed once (window_attention_decode_workspace)."""
+    dev, bf = q.device, torch.bfloat16
+    desc = _decode_desc(q, cache_k, left, sinks, scale)
+    _ask(cache_k.dtype == bf and cache_v.dtype == bf and cache_k.device == dev and cache_v.device == dev and
+         cache_k.shape == cache_v.shape and cache_k.stride() == cache_v.stride(),
+         f"the caches: bfloat16 on {dev}, of the same shape and strides")
+    _dense(lens, (q.shape[0],), torch.int32, dev, "lens")
+    ld_q = _rows(q, q.shape, bf, dev, "q")
+    ld_new = 0
+    if k_new is not None or v_new is not None:
+        _ask(k_new is not None and v_new is not None, "k_new and v_new: both or neither")
+        shape = (q.shape[0], cache_k.shape[2], q.shape[2])
+        ld_new = _rows(k_new, shape, bf, dev, "k_new")
+        _ask(_rows(v_new, shape, bf, dev, "v_new") == ld_new, "k_new and v_new need the same row stride")
+    with _Place(q, stream):
+        if workspace is None:
+            workspace = _space(None, ttt_window_attention_decode_workspace_size(desc), dev).zero_()
+        if out is None:
+            out = torch.empty(q.shape, dtype=bf, device=dev)
+        check(ttt_window_attention_decode(desc, q, ld_q, k_new, v_new, ld_new, cache_k, cache_v, lens, out,
+                                          _rows(out, q.shape, bf, dev, "out"), workspace, workspace.numel(), stream),
+              "ttt_window_attention_decode")
+        if check_status:
+            check(ttt_mlp_status(workspace, stream), "ttt_mlp_status")
+    return {"out": out, "workspace": workspace}
+
+
+def _gated_desc(x, n_seq, form, dirs):
+    _ask(x.dim() == 2, "x: [T, D]")
+    return ttt_gated_scan_desc(x.shape[0], x.shape[1], n_seq, TTT_GATE_FORMS[form], DIRS[dirs], _dtype_code(x, "x"))
+
+
+def gated_scan_workspace(x, n_seq: int = 1) -> torch.Tensor:
+    """A workspace for gated_scan and gated_scan_backward on tensors of x's shape and type."""
+    return _space(None, ttt_gated_scan_workspace_size(_gated_desc(x, n_seq, "sum", "fwd")), x.device)
+
+
+def gated_scan(f, x, *, form: str = "convex", dirs: str = "fwd", cu=None, h0=None, y=None, h_T=None,
+               want_state: bool = False, want_chunk_states: bool = False, chunk_states=None, workspace=None,
+               check_status: bool = True, stream=None) -> dict:
+    """Gated linear recurrence of the gate logits f and inputs x [T, D] (ttt_gated_scan)."""
+    dev, n_seq = x.device, _offsets(cu, x.device, "cu")
+    desc = _gated_desc(x, n_seq, form, dirs)
+    ld_f, ld_x = _rows(f, x.shape, x.dtype, dev, "f"), _rows(x, x.shape, x.dtype, dev, "x")
+    state = (n_seq, x.shape[1])
+    if h0 is not None:
+        _dense(h0, state, torch.float32, dev, "h0")
+    with _Place(x, stream):
+        ws = _space(workspace, ttt_gated_scan_workspace_size(desc), dev)
+        if y is None:
+            y = (torch.empty if cu is None else torch.zeros)(x.shape, dtype=x.dtype, device=dev)
+        if h_T is None and want_state:
+            h_T = torch.empty(state, device=dev)
+        if h_T is not None:
+            _dense(h_T, state, torch.float32, dev, "h_T")
+        n = ttt_gated_scan_chunk_states_size(desc)
+        if chunk_states is None and want_chunk_states:
+            chunk_states = torch.empty(n // 4, device=dev)
+        if chunk_states is not None:
+            _dense(chunk_states, (n // 4,), torch.float32, dev, "chunk_states")
+        check(ttt_gated_scan(desc, cu, f, ld_f, x, ld_x, h0, y, _rows(y, x.shape, x.dtype, dev, "y"), h_T,
+                             chunk_states, ws, ws.numel(), stream), "ttt_gated_scan")
+        if check_status:
+            check(ttt_mlp_status(ws, stream), "ttt_mlp_status")
+    return {"y": y, "h_T": h_T, "chunk_states": chunk_states, "workspace": ws}
+
+
+def gated_scan_backward(f, x, dy, chunk_states, *, form: str = "convex", dirs: str = "fwd", cu=None, h0=None,
+                        dh_T=None, df=None, dx=None, dh0=None, want_dh0: bool = False, workspace=None,
+                        check_status: bool = True, stream=None) -> dict:
+    """Gradients of gated_scan from its inputs and chunk states (ttt_gated_scan_backward)."""
+    dev, n_seq = x.device, _offsets(cu, x.device, "cu")
+    desc = _gated_desc(x, n_seq, form, dirs)
+    state = (n_seq, x.shape[1])
+    _dense(chunk_states, (ttt_gated_scan_chunk_states_size(desc) // 4,), torch.float32, dev, "chunk_states")
+    for t, name in ((h0, "h0"), (dh_T, "dh_T")):
+        if t is not None:
+            _dense(t, state, torch.float32, dev, name)
+    with _Place(x, stream):
+        ws = _space(workspace, ttt_gated_scan_workspace_size(desc), dev)
+        new = torch.empty if cu is None else torch.zeros
+        df = new(x.shape, dtype=x.dtype, device=dev) if df is None else df
+        dx = new(x.shape, dtype=x.dtype, device=dev) if dx is None else dx
+        if dh0 is None and want_dh0:
+            dh0 = torch.empty(state, device=dev)
+        if dh0 is not None:
+            _dense(dh0, state, torch.float32, dev, "dh0")
+        ld = {n: _rows(t, x.shape, x.dtype, dev, n) for n, t in dict(f=f, x=x, dy=dy, df=df, dx=dx).items()}
+        check(ttt_gated_scan_backward(desc, cu, f, ld["f"], x, ld["x"], h0, chunk_states, dy, ld["dy"], dh_T, df,
+                                      ld["df"], dx, ld["dx"], dh0, ws, ws.numel(), stream),
+              "ttt_gated_scan_backward")
+        if check_status:
+            check(ttt_mlp_status(ws, stream), "ttt_mlp_status")
+    return {"df": df, "dx": dx, "dh0": dh0, "workspace": ws}
+
+
+def gated_scan_step(f, x, h, *, form: str = "convex", y=None, h_out=None, stream=None):
+    """One token of each row: returns (y, h_out) for f, x [B, D] and the state h fp32 [B, D] (h_out may be h)."""
+    dev, code = x.device, _dtype_code(x, "x")
+    B, D = x.shape
+    _dense(h, (B, D), torch.float32, dev, "h")
+    with _Place(x, stream):
+        y = torch.empty((B, D), dtype=x.dtype, device=dev) if y is None else y
+        h_out = torch.empty_like(h) if h_out is None else _dense(h_out, (B, D), torch.float32, dev, "h_out")
+        check(ttt_gated_scan_step(B, D, TTT_GATE_FORMS[form], code, f, _rows(f, x.shape, x.dtype, dev, "f"), x,
+                                  _rows(x, x.shape, x.dtype, dev, "x"), h, h_out, y,
+                                  _rows(y, x.shape, x.dtype, dev, "y"), stream), "ttt_gated_scan_step")
+    return y, h_out
