@@ -510,7 +510,7 @@ TTT_API ttt_status ttt_rope(const ttt_rope_desc* desc, const void* X, int ld_x, 
  * A non-finite key, value or query makes the rows that see it (its own row)
  * NaN and is reported by the status; rows that do not see it are not affected.
  *
- *   desc      Tq, Tk rows of the query and key arrays (Tq, Tk >= 0), d = 64,
+ *   desc      Tq, Tk rows of the query and key arrays (0 to 2^28), d = 64,
  *             Hq a multiple of Hk, left, right, sinks >= 0, scale > 0.
  *   cu_q, cu_k  packed sequences as above (both or neither).
  *   Q, K, V   bf16; head h of row t at t * ld + h * 64.  ld_q >= Hq * 64,

@@ -199,9 +199,12 @@ struct WindowArgs {
     __nv_bfloat16 *dQ, *dK, *dV;
     long long ld_do, ld_dq, ld_dk, ld_dv;
     float* delta;                // [Hq, Tq] scratch: rowsum(dOut * Out)
+    float* partial;              // scratch: partial sums of the sinks' dK and dV
 };
 cudaError_t launch_window_attention(const WindowArgs& a, cudaStream_t s);
 cudaError_t launch_window_attention_backward(const WindowArgs& a, cudaStream_t s);
+cudaError_t launch_window_dkv(const WindowArgs& a, int sms, cudaStream_t s);
+long long window_partial_floats(const WindowArgs& a);   // of Tq, n_seq, Hq and Hk alone
 
 struct WindowDecodeArgs {
     int B, Hq, Hk, slots, left, sinks;

@@ -12,7 +12,8 @@ using namespace ttt;
 namespace {
 
 constexpr size_t kAlign = 256;
-constexpr int kMaxRows = 1 << 30;   // row counts and their sums stay inside an int
+constexpr int kMaxRows = 1 << 30;
+constexpr int kMaxWindowRows = 1 << 28;   // positions plus a window of any width stay inside an int
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 #define SEQ_TRY(expr)                                                                                       \
@@ -74,8 +75,8 @@ ttt_status check_sequences(int n_seq, const int* cu) {
 // ---------------------------------------------------------------- window attention
 ttt_status check_window(const ttt_window_desc* q) {
     if (!q) return set_error(TTT_ERR_INVALID_ARG, "desc is NULL");
-    if (q->Tq < 0 || q->Tk < 0 || q->Tq > kMaxRows || q->Tk > kMaxRows)
-        return set_error(TTT_ERR_INVALID_ARG, "Tq=%d, Tk=%d must lie in [0, 2^30]", q->Tq, q->Tk);
+    if (q->Tq < 0 || q->Tk < 0 || q->Tq > kMaxWindowRows || q->Tk > kMaxWindowRows)
+        return set_error(TTT_ERR_INVALID_ARG, "Tq=%d, Tk=%d must lie in [0, 2^28]", q->Tq, q->Tk);
     if (q->Hq < 1 || q->Hk < 1 || q->Hq % q->Hk || q->Hq > 65535)
         return set_error(TTT_ERR_INVALID_ARG, "Hq=%d must be a multiple of Hk=%d, both at least 1", q->Hq, q->Hk);
     if (q->d != 64) return set_error(TTT_ERR_UNSUPPORTED, "head dim %d: the window attention has 64", q->d);
@@ -169,7 +170,9 @@ extern "C" TTT_API size_t ttt_window_attention_workspace_size(const ttt_window_d
 
 extern "C" TTT_API size_t ttt_window_attention_backward_workspace_size(const ttt_window_desc* desc) {
     if (check_window(desc) != TTT_OK) return 0;
-    return kAlign + align_up((size_t)desc->Hq * desc->Tq * sizeof(float));
+    WindowArgs a{};
+    a.Tq = desc->Tq; a.n_seq = desc->n_seq; a.Hq = desc->Hq; a.Hk = desc->Hk;
+    return kAlign + align_up((size_t)desc->Hq * desc->Tq * sizeof(float)) + (size_t)window_partial_floats(a) * sizeof(float);
 }
 
 extern "C" TTT_API ttt_status ttt_window_attention(const ttt_window_desc* desc, const int* cu_q, const int* cu_k, const void* Q,
@@ -241,6 +244,7 @@ extern "C" TTT_API ttt_status ttt_window_attention_backward(const ttt_window_des
     a.dV = static_cast<__nv_bfloat16*>(dV); a.ld_dv = ld_dv;
     a.status = static_cast<int*>(workspace);
     a.delta = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign);
+    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign + align_up((size_t)q.Hq * q.Tq * sizeof(float)));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     SEQ_TRY(cudaMemsetAsync(workspace, 0, 16, s));
     if (q.Tq || q.Tk) SEQ_TRY(launch_window_attention_backward(a, s));

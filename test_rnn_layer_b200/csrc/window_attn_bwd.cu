@@ -1,100 +1,409 @@
-// Window attention with sinks, backward: one warp per query row (dQ), one per key row (dK, dV).
-#include "common.cuh"
-#include "window_mask.cuh"
+// Window attention, backward: delta = rowsum(dO Out), and dQ on the tcgen05 tensor cores (dK and dV have a
+// kernel of their own: each sum has one owner and one order, at the price of computing the scores twice).
+//   dQ_i = scale sum_u dS_iu k_u,  dS = P (dO.v - delta),  P = exp(scale q.k - lse)
+//
+// Work: an item is 256 query rows of a sequence (tiles A and B of 128) of one head, walking the forward pass's
+// key tiles in steps of 64 keys: S_X = Q_X K^T and dP_X = dO_X V^T into tensor memory, dS_X back to it as bf16,
+// dQ_X += dS_X K.  A thread holds the 64 scores and products of its query row; lse and delta are two registers.
+// Roles (384 threads): warps 0-3 tile A, 4-7 tile B, warp 8 the TMA producer, warps 9 and 10 the MMA issuers,
+// warp 11 the screen for key rows that are not finite.
+// Tensor memory, tile X: S 256 X, dP 256 X + 64, dQ 256 X + 128, dS 256 X + 192.
+// Every wait is bounded, as in the forward kernel.
+#include "window_bwd.cuh"
 
 namespace ttt {
 namespace {
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
+using namespace winb;
 
-struct Pair {
-    float x, y;
+constexpr int ROWS = 2 * BT, NST = 4;
+constexpr int OFF_Q = 0;                          // Q_A, Q_B, dO_A, dO_B
+constexpr int OFF_KV = 4 * TILE;                  // stage s: K at OFF_KV + 2 s TILE, V after it
+constexpr int OFF_BAR = OFF_KV + NST * 2 * TILE;
+constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
+constexpr uint32_t TM_X = 256, TM_S = 0, TM_DP = 64, TM_DQ = 128, TM_DS = 192;
+
+enum : int {
+    B_QF = 0,              // Q and dO landed
+    B_QE = 1,              // the item's S and dP products are done (2 arrivals)
+    B_KF = 2,              // [NST] K and V landed
+    B_SC = 2 + NST,        // [NST] K screened
+    B_KVE = 2 + 2 * NST,   // [NST] both tiles are done with the stage (2 arrivals)
+    B_SF = 2 + 3 * NST,    // [2] S_X and dP_X in tensor memory
+    B_SR = B_SF + 2,       // [2] the group has read them (4 warps)
+    B_PF = B_SR + 2,       // [2] dS_X written (4 warps)
+    B_PV = B_PF + 2,       // [2] its product is done
+    B_SLOT = B_PV + 2,
+    B_BAD = 32             // [NST] 16 bytes: bits of the stage's key rows that are not finite
 };
-__device__ __forceinline__ Pair load2(const __nv_bfloat16* base, long long ld, int row, int h, int lane) {
-    const __nv_bfloat16* q = base + row * ld + h * 64 + 2 * lane;
-    return {__bfloat162float(q[0]), __bfloat162float(q[1])};
-}
-__device__ __forceinline__ void store2(__nv_bfloat16* base, long long ld, int row, int h, int lane, Pair v) {
-    __nv_bfloat16* q = base + row * ld + h * 64 + 2 * lane;
-    q[0] = __float2bfloat16_rn(v.x);
-    q[1] = __float2bfloat16_rn(v.y);
+static_assert(B_SLOT < B_BAD && B_BAD * 8 + NST * 16 <= 512, "barrier area");
+static_assert(SMEM_BYTES <= 232448, "shared memory");
+
+struct QArgs {
+    CUtensorMap mapQ, mapK, mapV, mapDO;
+    WindowArgs w;
+    long long n_items;
+    float c;
+};
+
+struct Item {
+    int q_lo, rows, pos0, k0, nk, h, hk;
+    int ns, nt;
+    win::KeyRange r;
+
+    __device__ __forceinline__ bool load(const WindowArgs& p, long long w) {
+        const SeqOffsets cq{p.cu_q, p.n_seq, p.Tq}, ck{p.cu_k, p.n_seq, p.Tk};
+        h = (int)(w % p.Hq);
+        hk = h / (p.Hq / p.Hk);
+        const int s = win::block_of<ROWS>(cq, (int)(w / p.Hq), q_lo, rows);
+        if (s < 0) return false;
+        const int q0 = cq.begin(s), nq = cq.begin(s + 1) - q0;
+        k0 = ck.begin(s);
+        nk = max(ck.begin(s + 1) - k0, 0);
+        pos0 = nk - nq + (q_lo - q0);
+        r = win::keys_of(pos0, rows, nk, p.left, p.right, p.sinks);
+        ns = (r.sk + BT - 1) / BT;
+        nt = ns + (r.hi - r.lo + BT - 1) / BT;
+        return true;
+    }
+    __device__ __forceinline__ int start(int j) const { return j < ns ? BT * j : r.lo + BT * (j - ns); }
+    // the window keys [a, b) of tile X's rows (sinks that reach into the window begin it)
+    __device__ __forceinline__ void range(const WindowArgs& p, int X, int& a, int& b) const {
+        const int n = min(rows - BT * X, BT), q = pos0 + BT * X;
+        a = p.sinks > r.lo ? r.lo : max(q - p.left, r.lo);
+        b = n > 0 ? max(min(q + n + p.right, r.hi), a) : a;
+    }
+    // whether tile X meets keys of half hh of key tile j
+    __device__ __forceinline__ bool sees(int X, int j, int hh, int a, int b) const {
+        const int t0 = start(j) + HALF * hh;
+        return j < ns ? rows > BT * X && t0 < r.sk : t0 < b && t0 + HALF > a;
+    }
+};
+
+__global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_constant__ QArgs p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_SLOT);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    uint4* bad_rows = reinterpret_cast<uint4*>(bars + B_BAD);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        tc::mbar_init(bars + B_QF, 1);
+        tc::mbar_init(bars + B_QE, 2);
+        for (int s = 0; s < NST; ++s) {
+            tc::mbar_init(bars + B_KF + s, 1);
+            tc::mbar_init(bars + B_SC + s, 1);
+            tc::mbar_init(bars + B_KVE + s, 2);
+        }
+        for (int x = 0; x < 2; ++x) {
+            tc::mbar_init(bars + B_SF + x, 1);
+            tc::mbar_init(bars + B_SR + x, 4);
+            tc::mbar_init(bars + B_PF + x, 4);
+            tc::mbar_init(bars + B_PV + x, 1);
+        }
+        *abort_flag = 0;
+        tc::fence_mbar_init();
+        tc::tma_prefetch_desc(&p.mapQ);
+        tc::tma_prefetch_desc(&p.mapK);
+        tc::tma_prefetch_desc(&p.mapV);
+        tc::tma_prefetch_desc(&p.mapDO);
+    }
+    if (warp == 9) {
+        tc::tmem_alloc(tmem_slot, 512);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tm = *tmem_slot;
+
+    auto give_up = [&]() {
+        *abort_flag = 1;
+        atomicOr(p.w.status, kStatusTimeout);
+    };
+    // waits of a whole warp, so that every branch after it is uniform
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        const bool got = tc::mbar_wait(bar, parity, abort_flag);
+        return __all_sync(0xffffffffu, got);
+    };
+    Item it;
+
+    if (warp == 8) {
+        // ---------------- TMA producer
+        if (tc::elect_one()) {
+            int g = 0, n = 0;
+            bool ok = true;
+            for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
+                if (!it.load(p.w, w)) continue;
+                if (n > 0 && !tc::mbar_wait(bars + B_QE, (n - 1) & 1, abort_flag)) { ok = false; break; }
+                ++n;
+                const int xq = it.h * DH, xk = it.hk * DH;
+                // tile B past the last row: tile A's rows again (its results are never stored)
+                const int q_b = it.rows > BT ? it.q_lo + BT : it.q_lo;
+                tc::mbar_arrive_expect_tx(bars + B_QF, 4 * TILE);
+                tc::tma_load_2d(sm + OFF_Q, &p.mapQ, xq, it.q_lo, bars + B_QF);
+                tc::tma_load_2d(sm + OFF_Q + TILE, &p.mapQ, xq, q_b, bars + B_QF);
+                tc::tma_load_2d(sm + OFF_Q + 2 * TILE, &p.mapDO, xq, it.q_lo, bars + B_QF);
+                tc::tma_load_2d(sm + OFF_Q + 3 * TILE, &p.mapDO, xq, q_b, bars + B_QF);
+                for (int j = 0; j < it.nt; ++j, ++g) {
+                    const int s = g % NST, use = g / NST, row = it.k0 + it.start(j);
+                    if (use > 0 && !tc::mbar_wait(bars + B_KVE + s, (use - 1) & 1, abort_flag)) { ok = false; break; }
+                    uint8_t* kt = sm + OFF_KV + s * 2 * TILE;
+                    tc::mbar_arrive_expect_tx(bars + B_KF + s, 2 * TILE);
+                    tc::tma_load_2d(kt, &p.mapK, xk, row, bars + B_KF + s);
+                    tc::tma_load_2d(kt + TILE, &p.mapV, xk, row, bars + B_KF + s);
+                }
+            }
+            if (!ok) give_up();
+        }
+    } else if (warp == 11) {
+        // ---------------- screen of the keys
+        int g = 0;
+        bool ok = true;
+        for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
+            if (!it.load(p.w, w)) continue;
+            for (int j = 0; j < it.nt; ++j, ++g) {
+                const int s = g % NST, use = g / NST;
+                if (!wait_all(bars + B_KF + s, use & 1)) { ok = false; break; }
+                uint32_t a[4];
+                screen_tile(sm + OFF_KV + s * 2 * TILE, lane, a);
+                if (lane == 0) bad_rows[s] = make_uint4(a[0], a[1], a[2], a[3]);
+                if (a[0] | a[1] | a[2] | a[3]) tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bars + B_SC + s);
+            }
+        }
+        if (!ok && lane == 0) give_up();
+    } else if (warp >= 9) {
+        // ---------------- MMA issuers, one per tile: S_X and dP_X of a step, then the product of the step before
+        const int X = warp - 9;
+        if (tc::elect_one()) {
+            constexpr uint32_t ID_S = tc::instr_desc(1, BT, HALF, 0, 0);   // both K-major
+            constexpr uint32_t ID_Q = tc::instr_desc(1, BT, DH, 0, 1);     // A in tensor memory, B MN-major
+            const uint64_t dQ = kmajor_desc(sm + OFF_Q + X * TILE), dO = kmajor_desc(sm + OFF_Q + (2 + X) * TILE);
+            const uint32_t tX = tm + TM_X * X;
+            int g = 0, gs = 0, n = 0;
+            bool ok = true;
+            // the product of step gs - 1: half hh of stage s, and the stage's release after X's last half in it
+            auto product = [&](int s, int hh, bool accumulate, bool release) {
+                if (!tc::mbar_wait(bars + B_PF + X, (gs - 1) & 1, abort_flag)) return false;
+                tc::tc_fence_after();
+                const uint64_t mK = mnmajor_desc(sm + OFF_KV + s * 2 * TILE + hh * (TILE / 2));
+#pragma unroll
+                for (int kk = 0; kk < HALF / 16; ++kk)
+                    tc::mma_f16_ts(tX + TM_DQ, tX + TM_DS + 8 * kk, mK + (uint64_t)(kk * 128), ID_Q,
+                                   (accumulate || kk > 0) ? 1u : 0u);
+                tc::mma_commit(bars + B_PV + X);
+                if (release) tc::mma_commit(bars + B_KVE + s);
+                return true;
+            };
+            for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
+                if (!it.load(p.w, w)) continue;
+                int a, b;
+                it.range(p.w, X, a, b);
+                if (!tc::mbar_wait(bars + B_QF, n & 1, abort_flag)) { ok = false; break; }
+                ++n;
+                tc::tc_fence_after();
+                int done = 0, ps = -1, ph = 0;
+                bool prel = false;
+                for (int j = 0; j < it.nt && ok; ++j, ++g) {
+                    const int s = g % NST, use = g / NST;
+                    if (!tc::mbar_wait(bars + B_KF + s, use & 1, abort_flag)) { ok = false; break; }
+                    const bool first = it.sees(X, j, 0, a, b), second = it.sees(X, j, 1, a, b);
+                    if (!first && !second) {
+                        tc::mbar_arrive(bars + B_KVE + s);
+                        continue;
+                    }
+                    for (int hh = 0; hh < 2; ++hh) {
+                        if (!(hh ? second : first)) continue;
+                        if (gs > 0 && !tc::mbar_wait(bars + B_SR + X, (gs - 1) & 1, abort_flag)) { ok = false; break; }
+                        tc::tc_fence_after();
+                        const uint8_t* kt = sm + OFF_KV + s * 2 * TILE + hh * (TILE / 2);
+                        const uint64_t dK = kmajor_desc(kt), dV = kmajor_desc(kt + TILE);
+#pragma unroll
+                        for (int kk = 0; kk < DH / 16; ++kk)
+                            tc::mma_f16_ss(tX + TM_S, dQ + 2 * kk, dK + 2 * kk, ID_S, kk > 0);
+#pragma unroll
+                        for (int kk = 0; kk < DH / 16; ++kk)
+                            tc::mma_f16_ss(tX + TM_DP, dO + 2 * kk, dV + 2 * kk, ID_S, kk > 0);
+                        tc::mma_commit(bars + B_SF + X);
+                        if (ps >= 0 && !product(ps, ph, done > 1, prel)) { ok = false; break; }
+                        ++gs;
+                        ++done;
+                        ps = s;
+                        ph = hh;
+                        prel = hh == 1 || !second;
+                    }
+                }
+                if (ok) tc::mma_commit(bars + B_QE);
+                if (ok && ps >= 0 && !product(ps, ph, done > 1, prel)) ok = false;
+            }
+            if (!ok) give_up();
+        }
+    } else {
+        // ---------------- softmax groups: thread = query row r of tile X
+        const int X = warp >> 2, qd = warp & 3, r = 32 * qd + lane;
+        const uint32_t tX = tm + TM_X * X + ((uint32_t)(32 * qd) << 16);
+        const float c = p.c;
+        int g = 0, gs = 0, nonfinite = 0;
+        bool ok = true;
+        for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
+            if (!it.load(p.w, w)) continue;
+            int a, b;
+            it.range(p.w, X, a, b);
+            const int pos = it.pos0 + BT * X + r;
+            const bool mine = BT * X + r < it.rows;
+            const long long at = (long long)it.h * p.w.Tq + it.q_lo + BT * X + r;
+            const float nl = mine ? -kLog2e * p.w.Lse[at] : 0.f, nd = mine ? -p.w.delta[at] : 0.f;
+            const uint64_t nl2 = f2(nl, nl), nd2 = f2(nd, nd);
+            bool any = false;
+            for (int j = 0; j < it.nt && ok; ++j, ++g) {
+                const int s = g % NST, use = g / NST;
+                for (int hh = 0; hh < 2; ++hh) {
+                    if (!it.sees(X, j, hh, a, b)) continue;
+                    const int t0 = it.start(j) + HALF * hh;
+                    int lo = 0, hi = it.r.sk - t0, sk = 0;
+                    if (j >= it.ns) {
+                        lo = pos - p.w.left - t0;
+                        hi = min(pos + p.w.right + 1, it.nk) - t0;
+                        sk = p.w.sinks - t0;
+                    }
+                    const bool whole = __all_sync(0xffffffffu, hi >= HALF && lo <= 0);
+                    uint32_t vis[2], bad[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        vis[i] = win::low_bits(hi - 32 * i) & (~win::low_bits(lo - 32 * i) | win::low_bits(sk - 32 * i));
+                    if (!wait_all(bars + B_SC + s, use & 1) || !wait_all(bars + B_SF + X, gs & 1)) { ok = false; break; }
+                    tc::tc_fence_after();
+                    const uint32_t* bw = reinterpret_cast<const uint32_t*>(bad_rows + s) + 2 * hh;
+                    bad[0] = bw[0] & vis[0];
+                    bad[1] = bw[1] & vis[1];
+                    uint32_t sc[HALF], dp[HALF];
+                    tc::tmem_ld_32x32b_x32(tX + TM_S, *reinterpret_cast<uint32_t(*)[32]>(sc));
+                    tc::tmem_ld_32x32b_x32(tX + TM_S + 32, *reinterpret_cast<uint32_t(*)[32]>(sc + 32));
+                    tc::tmem_ld_32x32b_x32(tX + TM_DP, *reinterpret_cast<uint32_t(*)[32]>(dp));
+                    tc::tmem_ld_32x32b_x32(tX + TM_DP + 32, *reinterpret_cast<uint32_t(*)[32]>(dp + 32));
+                    tc::tmem_wait_ld();
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(bars + B_SR + X);
+                    grad_scores(sc, dp, c, whole, vis, bad, [&](int, uint64_t& l, uint64_t& d) {
+                        l = nl2;
+                        d = nd2;
+                    });
+                    if (gs > 0) {
+                        if (!wait_all(bars + B_PV + X, (gs - 1) & 1)) { ok = false; break; }
+                        tc::tc_fence_after();
+                    }
+                    tc::tmem_st_32x32b_x32(tX + TM_DS, *reinterpret_cast<uint32_t(*)[32]>(dp));
+                    tc::tmem_wait_st();
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(bars + B_PF + X);
+                    ++gs;
+                    any = true;
+                }
+            }
+            if (!ok) break;
+            // ---- epilogue
+            if (any) {
+                if (!wait_all(bars + B_PV + X, (gs - 1) & 1)) { ok = false; break; }
+                tc::tc_fence_after();
+            }
+            uint32_t o[DH];
+            tc::tmem_ld_32x32b_x32(tX + TM_DQ, *reinterpret_cast<uint32_t(*)[32]>(o));
+            tc::tmem_ld_32x32b_x32(tX + TM_DQ + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
+            tc::tmem_wait_ld();
+            if (!any) {   // rows that see nothing
+#pragma unroll
+                for (int e = 0; e < DH; ++e) o[e] = 0;
+            }
+            if (mine) {
+                const long long t = it.q_lo + BT * X + r;
+                nonfinite |= store_row(p.w.dQ + t * p.w.ld_dq + it.h * DH, o, p.w.scale);
+            }
+        }
+        if (!ok && lane == 0) give_up();
+        if (__any_sync(0xffffffffu, nonfinite) && lane == 0) atomicOr(p.w.status, kStatusNonFinite);
+    }
+
+    if (*abort_flag) {
+        // let copies and products already in flight land before the CTA's memory goes away
+        const uint64_t t0 = tc::globaltimer_ns();
+        while (tc::globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tm, 512);
+    }
 }
 
-__global__ void window_dq_kernel(const WindowArgs p) {
-    const SeqOffsets cq{p.cu_q, p.n_seq, p.Tq}, ck{p.cu_k, p.n_seq, p.Tk};
-    const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (blockIdx.x == 0)
+// delta[h, t] = sum of dO Out over the head's columns: eight lanes a row of 64, 16 bytes each; a warp takes four
+// consecutive rows of one head.  Also looks over the offsets.
+__global__ void __launch_bounds__(256) window_delta_kernel(const WindowArgs p) {
+    if (blockIdx.x == 0) {
+        const SeqOffsets cq{p.cu_q, p.n_seq, p.Tq}, ck{p.cu_k, p.n_seq, p.Tk};
         for (int s = threadIdx.x; s <= p.n_seq; s += blockDim.x)
             if (cq.bad(s) || ck.bad(s)) atomicOr(p.status, kStatusBadOffsets);
-    if (w >= (long long)p.Tq * p.Hq) return;
-    const int t = (int)(w / p.Hq), h = (int)(w % p.Hq), hk = h / (p.Hq / p.Hk);
-    const int s = cq.find(t);
-    if (t < cq.begin(s) || t >= cq.begin(s + 1)) return;
-    const int k0 = ck.begin(s), nk = max(ck.begin(s + 1) - k0, 0);
-    const int pos = nk - (cq.begin(s + 1) - cq.begin(s)) + t - cq.begin(s);
-    const Pair q = load2(p.Q, p.ld_q, t, h, lane), g = load2(p.dOut, p.ld_do, t, h, lane), o = load2(p.Out, p.ld_out, t, h, lane);
-    const float lse = p.Lse[(long long)h * p.Tq + t], delta = warp_sum(g.x * o.x + g.y * o.y);
-    if (lane == 0) p.delta[(long long)h * p.Tq + t] = delta;
-    Pair d = {0.f, 0.f};
-    const int lo = max(pos - p.left, 0), hi = min(pos + p.right, nk - 1);
-    for (int u = p.sinks > 0 ? 0 : lo; u <= hi; ++u) {
-        if (!window_sees(pos, u, p.left, p.right, p.sinks)) continue;
-        const Pair k = load2(p.K, p.ld_k, k0 + u, hk, lane), v = load2(p.V, p.ld_v, k0 + u, hk, lane);
-        const float x = p.scale * warp_sum(q.x * k.x + q.y * k.y), dp = warp_sum(g.x * v.x + g.y * v.y);
-        const float ds = p.scale * expf(x - lse) * (dp - delta);
-        d.x += ds * k.x;
-        d.y += ds * k.y;
     }
-    if (!(isfinite(d.x) && isfinite(d.y))) atomicOr(p.status, kStatusNonFinite);
-    store2(p.dQ, p.ld_dq, t, h, lane, d);
+    const int lane = threadIdx.x & 31;
+    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int h = (int)(w % p.Hq);
+    const long long t = w / p.Hq * 4 + (lane >> 3);
+    float sum = 0.f;
+    if (t < p.Tq) {
+        const int col = h * 64 + (lane & 7) * 8;
+        const uint4 g = *reinterpret_cast<const uint4*>(p.dOut + t * p.ld_do + col);
+        const uint4 o = *reinterpret_cast<const uint4*>(p.Out + t * p.ld_out + col);
+        const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, ow[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&gw[e]), b = *reinterpret_cast<const __nv_bfloat162*>(&ow[e]);
+            sum = fmaf(__low2float(a), __low2float(b), sum);
+            sum = fmaf(__high2float(a), __high2float(b), sum);
+        }
+    }
+#pragma unroll
+    for (int m = 1; m < 8; m *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if (t < p.Tq && (lane & 7) == 0) p.delta[(long long)h * p.Tq + t] = sum;
 }
 
-__global__ void window_dkv_kernel(const WindowArgs p) {
-    const SeqOffsets cq{p.cu_q, p.n_seq, p.Tq}, ck{p.cu_k, p.n_seq, p.Tk};
-    const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    if (w >= (long long)p.Tk * p.Hk) return;
-    const int t = (int)(w / p.Hk), hk = (int)(w % p.Hk), G = p.Hq / p.Hk;
-    const int s = ck.find(t);
-    if (t < ck.begin(s) || t >= ck.begin(s + 1)) return;
-    const int u = t - ck.begin(s), q0 = cq.begin(s), nq = max(cq.begin(s + 1) - q0, 0);
-    const int shift = ck.begin(s + 1) - ck.begin(s) - nq;
-    const Pair k = load2(p.K, p.ld_k, t, hk, lane), v = load2(p.V, p.ld_v, t, hk, lane);
-    Pair dk = {0.f, 0.f}, dv = {0.f, 0.f};
-    for (int h = hk * G; h < hk * G + G; ++h)
-        for (int i = 0; i < nq; ++i) {
-            if (!window_sees(shift + i, u, p.left, p.right, p.sinks)) continue;
-            const Pair q = load2(p.Q, p.ld_q, q0 + i, h, lane), g = load2(p.dOut, p.ld_do, q0 + i, h, lane);
-            const float x = p.scale * warp_sum(q.x * k.x + q.y * k.y), dp = warp_sum(g.x * v.x + g.y * v.y);
-            const long long at = (long long)h * p.Tq + q0 + i;
-            const float e = expf(x - p.Lse[at]), ds = p.scale * e * (dp - p.delta[at]);
-            dv.x += e * g.x;
-            dv.y += e * g.y;
-            dk.x += ds * q.x;
-            dk.y += ds * q.y;
-        }
-    if (!(isfinite(dk.x) && isfinite(dk.y) && isfinite(dv.x) && isfinite(dv.y))) atomicOr(p.status, kStatusNonFinite);
-    store2(p.dK, p.ld_dk, t, hk, lane, dk);
-    store2(p.dV, p.ld_dv, t, hk, lane, dv);
+cudaError_t launch_dq(const WindowArgs& a, int sms, cudaStream_t s) {
+    QArgs p{};
+    p.w = a;
+    const bool k = a.Tk > 0;   // without keys the tiles are never loaded; any valid array serves the maps
+    if (!make_map(&p.mapQ, a.Q, a.Tq, a.Hq * DH, a.ld_q) || !make_map(&p.mapDO, a.dOut, a.Tq, a.Hq * DH, a.ld_do) ||
+        !make_map(&p.mapK, k ? a.K : a.Q, k ? a.Tk : a.Tq, (k ? a.Hk : a.Hq) * DH, k ? a.ld_k : a.ld_q) ||
+        !make_map(&p.mapV, k ? a.V : a.Q, k ? a.Tk : a.Tq, (k ? a.Hk : a.Hq) * DH, k ? a.ld_v : a.ld_q))
+        return cudaErrorInvalidValue;
+    p.c = a.scale * kLog2e;
+    p.n_items = win::block_numbers<ROWS>(a.Tq, a.n_seq) * a.Hq;
+    cudaError_t e = cudaFuncSetAttribute(window_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    LaunchScope scope("window_dq", s);
+    window_dq_kernel<<<(unsigned)(p.n_items < sms ? p.n_items : sms), THREADS, SMEM_BYTES, s>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_window_attention_backward(const WindowArgs& a, cudaStream_t s) {
-    if (a.Tq) {
-        LaunchScope scope("window_dq", s);
-        window_dq_kernel<<<(unsigned)(((long long)a.Tq * a.Hq + 7) / 8), 256, 0, s>>>(a);
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    {
+        LaunchScope scope("window_delta", s);
+        const long long warps = ((long long)a.Tq + 3) / 4 * a.Hq;
+        window_delta_kernel<<<(unsigned)((warps + 7) / 8 ? (warps + 7) / 8 : 1), 256, 0, s>>>(a);
     }
-    if (a.Tk) {
-        LaunchScope scope("window_dkv", s);
-        window_dkv_kernel<<<(unsigned)(((long long)a.Tk * a.Hk + 7) / 8), 256, 0, s>>>(a);
-    }
-    return cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && a.Tk) e = launch_window_dkv(a, sms, s);
+    if (e == cudaSuccess && a.Tq) e = launch_dq(a, sms, s);
+    return e;
 }
 
 }  // namespace ttt

@@ -1,0 +1,469 @@
+// Window attention, backward: dK and dV on the tcgen05 tensor cores (head dim 64, bf16, fp32 accumulation).
+//   P = exp(scale q.k - lse), dS = P (dO.v - delta), dV_u = sum_i P_iu dO_i, dK_u = scale sum_i dS_iu q_i
+// over the queries i that see key u, of every query head that shares the key head.
+//
+// Work: an item is 128 keys of a sequence of one key head; it walks the query tiles of 128 rows that see them,
+// head after head, so that each sum has one owner and one order (no atomics).  The transposed scores are
+// computed, S^T = K Q^T and dP^T = V dO^T with a key per tensor-memory lane, so that P^T and dS^T are the A
+// operands of dV += P^T dO and dK += dS^T Q straight from tensor memory.  Two softmax groups take 64 queries of
+// a tile each: a thread holds 64 scores and 64 products of its key.  The rows' lse and delta lie in shared
+// memory beside the tile.
+//
+// Roles (384 threads): warps 0-3 queries 0..63 of a tile, 4-7 queries 64..127, warp 8 the TMA producer, warp 9
+// the MMA issuer (one, so that the sums' order is fixed), warp 10 the screen for rows of Q and dO that are not
+// finite, warp 11 loads lse and delta.
+// Tensor memory (512 columns), group X: S 192 X, dP 192 X + 64, P 192 X + 128, dS 192 X + 160; dV 384, dK 448.
+// Per tile of 128 x 128 scores the tensor cores have 4 products of 2.1 MFLOP and the exponential unit 14,336
+// results (1,024 and 896 cycles): S and dP of the next tile are issued as soon as this one's are in registers.
+// Every wait is bounded, as in the forward kernel.
+#include "window_bwd.cuh"
+
+namespace ttt {
+namespace {
+
+using namespace winb;
+
+constexpr int NST = 4;
+constexpr int OFF_KV = 0;                             // item n: K at (n & 1) 2 TILE, V after it
+constexpr int OFF_Q = 4 * TILE;                       // stage s: Q at OFF_Q + 2 s TILE, dO after it
+constexpr int OFF_STAT = OFF_Q + NST * 2 * TILE;      // stage s: 128 x -lse2, 128 x -delta
+constexpr int OFF_BAR = OFF_STAT + NST * 1024;
+constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
+constexpr uint32_t TM_X = 192, TM_S = 0, TM_DP = 64, TM_P = 128, TM_DS = 160, TM_DV = 384, TM_DK = 448;
+
+enum : int {
+    B_KVF = 0,             // [2] the item's K and V landed
+    B_KVE = 2,             // [2] its S and dP products are done
+    B_QF = 4,              // [NST] Q and dO landed
+    B_ST = 4 + NST,        // [NST] lse and delta written
+    B_SC = 4 + 2 * NST,    // [NST] Q and dO screened
+    B_QE = 4 + 3 * NST,    // [NST] stage free (a commit and 8 warps)
+    B_SF = 4 + 4 * NST,    // [2] S_X and dP_X in tensor memory
+    B_SR = B_SF + 2,       // [2] the group has read them (4 warps)
+    B_PF = B_SR + 2,       // [2] P_X and dS_X written (4 warps)
+    B_PV = B_PF + 2,       // [2] their products are done
+    B_AF = B_PV + 2,       // the item's dV and dK are complete
+    B_AE = B_AF + 1,       // and read (8 warps)
+    B_SLOT = B_AE + 1,
+    B_BAD = 36             // [NST] 16 bytes: bits of the stage's query rows that are not finite
+};
+static_assert(B_SLOT < B_BAD && B_BAD * 8 + NST * 16 <= 512 && B_BAD % 2 == 0, "barrier area");
+static_assert(SMEM_BYTES <= 232448, "shared memory");
+
+struct KvArgs {
+    CUtensorMap mapQ, mapK, mapV, mapDO;
+    WindowArgs w;
+    long long n_window, n_items;   // window items, then chunks of the sinks' further queries
+    float c;
+    int cut;                       // whether sinks are cut up (partial sums in w.partial)
+};
+
+struct Item {
+    int k_lo, keys, u0, nk, hk;    // first key row, number of keys, its index in the sequence
+    int q0, nq, first;             // the sequence's first query row, number of queries, position of query 0
+    int i0, i1, h0, heads;         // query range, heads h0 .. h0 + heads - 1
+    long long slot;                // partial sums go here (-1: the item's sums are dK and dV)
+
+    __device__ __forceinline__ bool load(const KvArgs& a, long long w) {
+        const WindowArgs& p = a.w;
+        const SeqOffsets cq{p.cu_q, p.n_seq, p.Tq}, ck{p.cu_k, p.n_seq, p.Tk};
+        const int G = p.Hq / p.Hk;
+        const bool window = w < a.n_window;
+        int s, c0 = 0, c1 = 0;
+        if (window) {
+            hk = (int)(w % p.Hk);
+            h0 = hk * G;
+            heads = G;
+            s = win::block_of<BT>(ck, (int)(w / p.Hk), k_lo, keys);
+        } else {
+            const long long r = w - a.n_window;
+            h0 = (int)(r % p.Hq);
+            hk = h0 / G;
+            heads = 1;
+            const long long b = r / p.Hq;
+            s = win::block_of<CHUNK>(cq, (int)(b / SINK_BLOCKS), c0, c1);
+            u0 = (int)(b % SINK_BLOCKS) * BT;
+        }
+        if (s < 0) return false;
+        q0 = cq.begin(s);
+        nq = max(cq.begin(s + 1) - q0, 0);
+        const int kb = ck.begin(s);
+        nk = max(ck.begin(s + 1) - kb, 0);
+        first = nk - nq;
+        if (window) {
+            u0 = k_lo - kb;
+        } else {
+            if (u0 >= min(p.sinks, nk)) return false;
+            k_lo = kb + u0;
+            keys = min(BT, nk - u0);
+        }
+        const QueryRange r = queries_of(u0, u0 + keys, first, nq, p.left, p.right);
+        i0 = r.ia;
+        i1 = r.ib;
+        slot = -1;
+        if (u0 < p.sinks && i1 < nq) {
+            if (!a.cut) {
+                i1 = nq;
+            } else if (window) {
+                slot = chunk_slots(p) + ((long long)s * p.Hk + hk) * SINK_BLOCKS + u0 / BT;
+            }
+        }
+        if (!window) {
+            i0 = max(i1, c0 - q0);
+            i1 = min(nq, c0 - q0 + c1);
+            if (i1 <= i0) return false;
+            slot = w - a.n_window;
+        }
+        return true;
+    }
+    __device__ __forceinline__ int tiles() const { return (i1 - i0 + BT - 1) / BT; }
+};
+
+__global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_constant__ KvArgs p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_SLOT);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    uint4* bad_rows = reinterpret_cast<uint4*>(bars + B_BAD);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int x = 0; x < 2; ++x) {
+            tc::mbar_init(bars + B_KVF + x, 1);
+            tc::mbar_init(bars + B_KVE + x, 1);
+            tc::mbar_init(bars + B_SF + x, 1);
+            tc::mbar_init(bars + B_SR + x, 4);
+            tc::mbar_init(bars + B_PF + x, 4);
+            tc::mbar_init(bars + B_PV + x, 1);
+        }
+        for (int s = 0; s < NST; ++s) {
+            tc::mbar_init(bars + B_QF + s, 1);
+            tc::mbar_init(bars + B_ST + s, 1);
+            tc::mbar_init(bars + B_SC + s, 1);
+            tc::mbar_init(bars + B_QE + s, 9);
+        }
+        tc::mbar_init(bars + B_AF, 1);
+        tc::mbar_init(bars + B_AE, 8);
+        *abort_flag = 0;
+        tc::fence_mbar_init();
+        tc::tma_prefetch_desc(&p.mapQ);
+        tc::tma_prefetch_desc(&p.mapK);
+        tc::tma_prefetch_desc(&p.mapV);
+        tc::tma_prefetch_desc(&p.mapDO);
+    }
+    if (warp == 9) {
+        tc::tmem_alloc(tmem_slot, 512);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tm = *tmem_slot;
+
+    auto give_up = [&]() {
+        *abort_flag = 1;
+        atomicOr(p.w.status, kStatusTimeout);
+    };
+    // waits of a whole warp, so that every branch after it is uniform
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        const bool got = tc::mbar_wait(bar, parity, abort_flag);
+        return __all_sync(0xffffffffu, got);
+    };
+    Item it;
+
+    if (warp == 8) {
+        // ---------------- TMA producer
+        if (tc::elect_one()) {
+            int g = 0, n = 0;
+            bool ok = true;
+            for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
+                if (!it.load(p, w) || it.tiles() == 0) continue;
+                const int kv = n & 1, xk = it.hk * DH, tiles = it.tiles();
+                if (n >= 2 && !tc::mbar_wait(bars + B_KVE + kv, ((n >> 1) - 1) & 1, abort_flag)) { ok = false; break; }
+                uint8_t* kt = sm + OFF_KV + kv * 2 * TILE;
+                tc::mbar_arrive_expect_tx(bars + B_KVF + kv, 2 * TILE);
+                tc::tma_load_2d(kt, &p.mapK, xk, it.k_lo, bars + B_KVF + kv);
+                tc::tma_load_2d(kt + TILE, &p.mapV, xk, it.k_lo, bars + B_KVF + kv);
+                ++n;
+                for (int t = 0; t < it.heads * tiles; ++t, ++g) {
+                    const int s = g % NST, use = g / NST, x = (it.h0 + t / tiles) * DH;
+                    const int row = it.q0 + it.i0 + (t % tiles) * BT;
+                    if (use > 0 && !tc::mbar_wait(bars + B_QE + s, (use - 1) & 1, abort_flag)) { ok = false; break; }
+                    uint8_t* qt = sm + OFF_Q + s * 2 * TILE;
+                    tc::mbar_arrive_expect_tx(bars + B_QF + s, 2 * TILE);
+                    tc::tma_load_2d(qt, &p.mapQ, x, row, bars + B_QF + s);
+                    tc::tma_load_2d(qt + TILE, &p.mapDO, x, row, bars + B_QF + s);
+                }
+            }
+            if (!ok) give_up();
+        }
+    } else if (warp == 9) {
+        // ---------------- MMA issuer: S and dP of tile t for both groups, then the products of tile t - 1
+        if (tc::elect_one()) {
+            constexpr uint32_t ID_S = tc::instr_desc(1, BT, HALF, 0, 0);   // both K-major
+            constexpr uint32_t ID_A = tc::instr_desc(1, BT, DH, 0, 1);     // A in tensor memory, B MN-major
+            int g = 0, n = 0;
+            bool ok = true;
+            for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
+                if (!it.load(p, w) || it.tiles() == 0) continue;
+                const int kv = n & 1, steps = it.heads * it.tiles();
+                if (!tc::mbar_wait(bars + B_KVF + kv, (n >> 1) & 1, abort_flag)) { ok = false; break; }
+                const uint64_t dK = kmajor_desc(sm + OFF_KV + kv * 2 * TILE), dV = kmajor_desc(sm + OFF_KV + kv * 2 * TILE + TILE);
+                for (int t = 0; t <= steps && ok; ++t) {
+                    if (t < steps) {
+                        const int gt = g + t, s = gt % NST;
+                        if (!tc::mbar_wait(bars + B_QF + s, (gt / NST) & 1, abort_flag)) { ok = false; break; }
+                        const uint8_t* qt = sm + OFF_Q + s * 2 * TILE;
+                        for (int X = 0; X < 2; ++X) {
+                            if (gt > 0 && !tc::mbar_wait(bars + B_SR + X, (gt - 1) & 1, abort_flag)) { ok = false; break; }
+                            tc::tc_fence_after();
+                            const uint64_t dQ = kmajor_desc(qt + X * (TILE / 2)), dO = kmajor_desc(qt + TILE + X * (TILE / 2));
+#pragma unroll
+                            for (int kk = 0; kk < DH / 16; ++kk)
+                                tc::mma_f16_ss(tm + TM_X * X + TM_S, dK + 2 * kk, dQ + 2 * kk, ID_S, kk > 0);
+#pragma unroll
+                            for (int kk = 0; kk < DH / 16; ++kk)
+                                tc::mma_f16_ss(tm + TM_X * X + TM_DP, dV + 2 * kk, dO + 2 * kk, ID_S, kk > 0);
+                            tc::mma_commit(bars + B_SF + X);
+                        }
+                        if (t == steps - 1) tc::mma_commit(bars + B_KVE + kv);
+                    }
+                    if (ok && t > 0) {
+                        const int gt = g + t - 1, s = gt % NST;
+                        const uint8_t* qt = sm + OFF_Q + s * 2 * TILE;
+                        // the item before has left the accumulators
+                        if (t == 1 && n > 0 && !tc::mbar_wait(bars + B_AE, (n - 1) & 1, abort_flag)) { ok = false; break; }
+                        for (int X = 0; X < 2; ++X) {
+                            if (!tc::mbar_wait(bars + B_PF + X, gt & 1, abort_flag)) { ok = false; break; }
+                            tc::tc_fence_after();
+                            const uint64_t mQ = mnmajor_desc(qt + X * (TILE / 2)), mO = mnmajor_desc(qt + TILE + X * (TILE / 2));
+                            const uint32_t more = t > 1 || X > 0;
+#pragma unroll
+                            for (int kk = 0; kk < HALF / 16; ++kk)
+                                tc::mma_f16_ts(tm + TM_DV, tm + TM_X * X + TM_P + 8 * kk, mO + (uint64_t)(kk * 128), ID_A,
+                                               more | (kk > 0));
+#pragma unroll
+                            for (int kk = 0; kk < HALF / 16; ++kk)
+                                tc::mma_f16_ts(tm + TM_DK, tm + TM_X * X + TM_DS + 8 * kk, mQ + (uint64_t)(kk * 128), ID_A,
+                                               more | (kk > 0));
+                            tc::mma_commit(bars + B_PV + X);
+                        }
+                        if (ok) tc::mma_commit(bars + B_QE + s);
+                    }
+                }
+                if (ok) tc::mma_commit(bars + B_AF);
+                g += steps;
+                ++n;
+            }
+            if (!ok) give_up();
+        }
+    } else if (warp >= 10) {
+        // ---------------- screen of Q and dO (warp 10); lse and delta (warp 11)
+        int g = 0;
+        bool ok = true;
+        for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
+            if (!it.load(p, w)) continue;
+            const int tiles = it.tiles();
+            for (int t = 0; t < it.heads * tiles; ++t, ++g) {
+                const int s = g % NST, use = g / NST;
+                if (warp == 10) {
+                    if (!wait_all(bars + B_QF + s, use & 1)) { ok = false; break; }
+                    uint8_t* qt = sm + OFF_Q + s * 2 * TILE;
+                    uint32_t a[4], b[4];
+                    screen_tile(qt, lane, a);
+                    screen_tile(qt + TILE, lane, b);
+                    const uint4 m = make_uint4(a[0] | b[0], a[1] | b[1], a[2] | b[2], a[3] | b[3]);
+                    if (lane == 0) bad_rows[s] = m;
+                    if (m.x | m.y | m.z | m.w) tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(bars + B_SC + s);
+                } else {
+                    if (use > 0 && !wait_all(bars + B_QE + s, (use - 1) & 1)) { ok = false; break; }
+                    float* st = reinterpret_cast<float*>(sm + OFF_STAT + s * 1024);
+                    const int i0 = it.i0 + (t % tiles) * BT;
+                    const long long at = (long long)(it.h0 + t / tiles) * p.w.Tq + it.q0;
+                    float l[4], d[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = i0 + 32 * e + lane;
+                        const bool in = i < it.i1;
+                        l[e] = in ? p.w.Lse[at + i] : 0.f;
+                        d[e] = in ? p.w.delta[at + i] : 0.f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        st[32 * e + lane] = -l[e] * kLog2e;
+                        st[BT + 32 * e + lane] = -d[e];
+                    }
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(bars + B_ST + s);
+                }
+            }
+        }
+        if (!ok && lane == 0) give_up();
+    } else {
+        // ---------------- softmax groups: thread = key r of the block, queries 64 X .. 64 X + 63 of each tile
+        const int X = warp >> 2, qd = warp & 3, r = 32 * qd + lane;
+        const uint32_t lanes = (uint32_t)(32 * qd) << 16, tX = tm + lanes + TM_X * X;
+        const float c = p.c;
+        int g = 0, n = 0, nonfinite = 0;
+        bool ok = true;
+        for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
+            if (!it.load(p, w)) continue;
+            const int tiles = it.tiles(), steps = it.heads * tiles, u = it.u0 + r;
+            // queries (as indices) that see key u, cut to the item's
+            const int lo_i = max(u - p.w.right - it.first, it.i0), hi_i = u < p.w.sinks ? it.i1 : min(u + p.w.left + 1 - it.first, it.i1);
+            for (int t = 0; t < steps; ++t, ++g) {
+                const int s = g % NST, use = g / NST;
+                const int base = it.i0 + (t % tiles) * BT + HALF * X, lo = lo_i - base, hi = hi_i - base;
+                const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= HALF);
+                uint32_t vis[2], bad[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) vis[i] = win::low_bits(hi - 32 * i) & ~win::low_bits(lo - 32 * i);
+                if (!wait_all(bars + B_ST + s, use & 1) || !wait_all(bars + B_SC + s, use & 1) ||
+                    !wait_all(bars + B_SF + X, g & 1)) { ok = false; break; }
+                tc::tc_fence_after();
+                const uint32_t* bw = reinterpret_cast<const uint32_t*>(bad_rows + s) + 2 * X;
+                bad[0] = bw[0] & vis[0];
+                bad[1] = bw[1] & vis[1];
+                uint32_t sc[HALF], dp[HALF];
+                tc::tmem_ld_32x32b_x32(tX + TM_S, *reinterpret_cast<uint32_t(*)[32]>(sc));
+                tc::tmem_ld_32x32b_x32(tX + TM_S + 32, *reinterpret_cast<uint32_t(*)[32]>(sc + 32));
+                tc::tmem_ld_32x32b_x32(tX + TM_DP, *reinterpret_cast<uint32_t(*)[32]>(dp));
+                tc::tmem_ld_32x32b_x32(tX + TM_DP + 32, *reinterpret_cast<uint32_t(*)[32]>(dp + 32));
+                tc::tmem_wait_ld();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bars + B_SR + X);
+                const uint64_t* nl = reinterpret_cast<const uint64_t*>(sm + OFF_STAT + s * 1024) + HALF / 2 * X;
+                grad_scores(sc, dp, c, whole, vis, bad, [&](int k2, uint64_t& a, uint64_t& b) {
+                    a = nl[k2];
+                    b = nl[BT / 2 + k2];
+                });
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bars + B_QE + s);   // the statistics have been read
+                if (g > 0) {
+                    if (!wait_all(bars + B_PV + X, (g - 1) & 1)) { ok = false; break; }
+                    tc::tc_fence_after();
+                }
+                tc::tmem_st_32x32b_x32(tX + TM_P, *reinterpret_cast<uint32_t(*)[32]>(sc));
+                tc::tmem_st_32x32b_x32(tX + TM_DS, *reinterpret_cast<uint32_t(*)[32]>(dp));
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bars + B_PF + X);
+            }
+            if (!ok) break;
+            // ---- epilogue: group 0 takes dV, group 1 dK
+            uint32_t o[DH];
+            if (steps > 0) {
+                if (!wait_all(bars + B_AF, n & 1)) { ok = false; break; }
+                tc::tc_fence_after();
+                ++n;
+            }
+            const uint32_t acc = tm + lanes + (X ? TM_DK : TM_DV);
+            tc::tmem_ld_32x32b_x32(acc, *reinterpret_cast<uint32_t(*)[32]>(o));
+            tc::tmem_ld_32x32b_x32(acc + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
+            tc::tmem_wait_ld();
+            if (steps > 0) {
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bars + B_AE);
+            } else {
+#pragma unroll
+                for (int e = 0; e < DH; ++e) o[e] = 0;
+            }
+            if (r < it.keys) {
+                const float f = X ? p.w.scale : 1.f;
+                if (it.slot >= 0) {
+                    float4* dst = reinterpret_cast<float4*>(p.w.partial + it.slot * SLOT + (X * BT + r) * DH);
+#pragma unroll
+                    for (int e = 0; e < DH / 4; ++e)
+                        dst[e] = make_float4(f * __uint_as_float(o[4 * e]), f * __uint_as_float(o[4 * e + 1]),
+                                             f * __uint_as_float(o[4 * e + 2]), f * __uint_as_float(o[4 * e + 3]));
+                } else {
+                    const long long t = it.k_lo + r;
+                    nonfinite |= X ? store_row(p.w.dK + t * p.w.ld_dk + it.hk * DH, o, f)
+                                   : store_row(p.w.dV + t * p.w.ld_dv + it.hk * DH, o, f);
+                }
+            }
+        }
+        if (!ok && lane == 0) give_up();
+        if (__any_sync(0xffffffffu, nonfinite) && lane == 0) atomicOr(p.w.status, kStatusNonFinite);
+    }
+
+    if (*abort_flag) {
+        // let copies and products already in flight land before the CTA's memory goes away
+        const uint64_t t0 = tc::globaltimer_ns();
+        while (tc::globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tm, 512);
+    }
+}
+
+// dK and dV of the key blocks with sinks that were cut up: the window's sums, then the chunks' head by head.
+// One block per sequence, key block and key head; a thread per four columns of a key.
+__global__ void window_sink_sum_kernel(const WindowArgs p) {
+    const SeqOffsets cq{p.cu_q, p.n_seq, p.Tq}, ck{p.cu_k, p.n_seq, p.Tk};
+    const int G = p.Hq / p.Hk, hk = blockIdx.x % p.Hk, s = blockIdx.x / p.Hk, u0 = blockIdx.y * BT;
+    const int q0 = cq.begin(s), nq = max(cq.begin(s + 1) - q0, 0), k0 = ck.begin(s), nk = max(ck.begin(s + 1) - k0, 0);
+    if (u0 >= min(p.sinks, nk)) return;
+    const int keys = min(BT, nk - u0);
+    const QueryRange r = queries_of(u0, u0 + keys, nk - nq, nq, p.left, p.right);
+    if (r.ib >= nq) return;
+    const int unit = blockIdx.z * blockDim.x + threadIdx.x;   // (dV or dK, key, four columns)
+    const int X = unit / (BT * DH / 4), key = unit / (DH / 4) % BT, col = unit % (DH / 4) * 4;
+    if (key >= keys) return;
+    const long long off = (X * BT + key) * DH + col;
+    float4 sum = *reinterpret_cast<const float4*>(p.partial + (chunk_slots(p) + ((long long)s * p.Hk + hk) * SINK_BLOCKS + blockIdx.y) * SLOT + off);
+    const long long b0 = q0 / CHUNK + s;
+    if (u0 + key < p.sinks)
+        for (int h = hk * G; h < hk * G + G; ++h)
+            for (int b = r.ib / CHUNK; b * CHUNK < nq; ++b) {
+                const long long slot = ((b0 + b) * SINK_BLOCKS + blockIdx.y) * p.Hq + h;
+                const float4 v = *reinterpret_cast<const float4*>(p.partial + slot * SLOT + off);
+                sum.x += v.x;
+                sum.y += v.y;
+                sum.z += v.z;
+                sum.w += v.w;
+            }
+    if (!(isfinite(sum.x) && isfinite(sum.y) && isfinite(sum.z) && isfinite(sum.w))) atomicOr(p.status, kStatusNonFinite);
+    __nv_bfloat16* dst = X ? p.dK + (k0 + u0 + key) * p.ld_dk : p.dV + (k0 + u0 + key) * p.ld_dv;
+    *reinterpret_cast<uint2*>(dst + hk * DH + col) = make_uint2(pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w));
+}
+
+}  // namespace
+
+cudaError_t launch_window_dkv(const WindowArgs& a, int sms, cudaStream_t s) {
+    KvArgs p{};
+    p.w = a;
+    const bool q = a.Tq > 0;   // without queries the tiles are never loaded; any valid array serves the maps
+    if (!make_map(&p.mapK, a.K, a.Tk, a.Hk * DH, a.ld_k) || !make_map(&p.mapV, a.V, a.Tk, a.Hk * DH, a.ld_v) ||
+        !make_map(&p.mapQ, q ? a.Q : a.K, q ? a.Tq : a.Tk, (q ? a.Hq : a.Hk) * DH, q ? a.ld_q : a.ld_k) ||
+        !make_map(&p.mapDO, q ? a.dOut : a.K, q ? a.Tq : a.Tk, (q ? a.Hq : a.Hk) * DH, q ? a.ld_do : a.ld_k))
+        return cudaErrorInvalidValue;
+    p.c = a.scale * kLog2e;
+    p.cut = cuts_sinks(a);
+    p.n_window = win::block_numbers<BT>(a.Tk, a.n_seq) * a.Hk;
+    p.n_items = p.n_window + (p.cut ? chunk_slots(a) : 0);
+    cudaError_t e = cudaFuncSetAttribute(window_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    {
+        LaunchScope scope("window_dkv", s);
+        window_dkv_kernel<<<(unsigned)(p.n_items < sms ? p.n_items : sms), THREADS, SMEM_BYTES, s>>>(p);
+    }
+    if (p.cut) {
+        LaunchScope scope("window_sink_sum", s);
+        window_sink_sum_kernel<<<dim3((unsigned)(a.n_seq * a.Hk), (a.sinks + BT - 1) / BT, SLOT / 4 / 256), 256, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
+long long window_partial_floats(const WindowArgs& a) { return all_slots(a) * SLOT; }
+
+}  // namespace ttt

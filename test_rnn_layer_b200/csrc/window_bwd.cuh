@@ -1,0 +1,138 @@
+// Parts shared by the two kernels of the window attention's backward pass.
+#pragma once
+
+#include "attn_prims.cuh"
+#include "internal.h"
+#include "window_items.cuh"
+
+namespace ttt {
+namespace winb {
+
+using namespace attn;
+
+constexpr int DH = 64, BT = 128, HALF = 64, TILE = BT * DH * 2, THREADS = 384;
+constexpr int EMU = 1;          // pairs of every 8 whose 2^x runs on the FMA pipe
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Looks through a 128-row tile of 64 bf16 columns in shared memory for rows that are not finite, zeroes them and
+// returns this lane's verdicts as ballots (row 32 g + lane is bit `lane` of word g).  A warp calls it.
+__device__ __forceinline__ void screen_tile(uint8_t* tile, int lane, uint32_t (&word)[4]) {
+    const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        uint4* row = reinterpret_cast<uint4*>(tile + (32 * g + lane) * 128);
+        __nv_bfloat162 a0 = zero, a1 = zero;
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch) {
+            const uint4 v = row[(ch + lane) & 7];   // rotated over the lanes for the banks
+            a0 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.x), zero, a0);
+            a1 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.y), zero, a1);
+            a0 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.z), zero, a0);
+            a1 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.w), zero, a1);
+        }
+        a0 = __hadd2(a0, a1);
+        const bool bad = !(__low2float(a0) == 0.f && __high2float(a0) == 0.f);
+        word[g] = __ballot_sync(0xffffffffu, bad);
+        if (bad) {
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) row[ch] = make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
+// P = exp2(c S - lse2) and dS = P (dP - delta) of one row's 64 scores, as bf16 pairs in the front of s and dp.
+// neg(k2) gives (-lse2, -delta) of columns 2 k2 and 2 k2 + 1 as packed pairs.  `vis`: the columns seen (unless
+// whole); `bad`: columns whose other operand was not finite and was zeroed: seen, they make the row NaN.
+template <class Neg>
+__device__ __forceinline__ void grad_scores(uint32_t (&s)[HALF], uint32_t (&dp)[HALF], float c, bool whole,
+                                            const uint32_t (&vis)[2], const uint32_t (&bad)[2], Neg neg) {
+    if (bad[0] | bad[1]) {
+#pragma unroll
+        for (int k = 0; k < HALF; ++k)
+            if ((bad[k / 32] >> (k & 31)) & 1u) s[k] = 0x7fffffffu;
+    }
+    const uint64_t c2 = f2(c, c);
+#pragma unroll
+    for (int k2 = 0; k2 < HALF / 2; ++k2) {
+        uint64_t nl, nd;
+        neg(k2, nl, nd);
+        const uint64_t x = f2_fma(f2(__uint_as_float(s[2 * k2]), __uint_as_float(s[2 * k2 + 1])), c2, nl);
+        float p0, p1;
+        if ((k2 & 7) >= 8 - EMU) {
+            ex2_poly2(x, p0, p1);
+        } else {
+            float x0, x1;
+            f2_split(x, x0, x1);
+            p0 = ex2(x0);
+            p1 = ex2(x1);
+        }
+        const uint64_t t = f2_add(f2(__uint_as_float(dp[2 * k2]), __uint_as_float(dp[2 * k2 + 1])), nd);
+        float d0, d1;
+        f2_split(f2_mul(f2(p0, p1), t), d0, d1);
+        if (!whole) {
+            const uint32_t v = vis[k2 / 16] >> (2 * (k2 & 15));
+            p0 = v & 1u ? p0 : 0.f;
+            d0 = v & 1u ? d0 : 0.f;
+            p1 = v & 2u ? p1 : 0.f;
+            d1 = v & 2u ? d1 : 0.f;
+        }
+        s[k2] = pack_bf16(p0, p1);
+        dp[k2] = pack_bf16(d0, d1);
+    }
+}
+
+// 64 fp32 values of one row, times `f`, as bf16 to a row of global memory; returns whether one is not finite.
+__device__ __forceinline__ bool store_row(__nv_bfloat16* dst, const uint32_t (&o)[DH], float f) {
+    bool bad = false;
+#pragma unroll
+    for (int c8 = 0; c8 < DH / 8; ++c8) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            v[e] = __uint_as_float(o[8 * c8 + e]) * f;
+            bad |= !isfinite(v[e]);
+        }
+        reinterpret_cast<uint4*>(dst)[c8] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                                       pack_bf16(v[6], v[7]));
+    }
+    return bad;
+}
+
+// ------------------------------------------------------------------ the sinks' share of dK and dV
+// Every later query sees a sink, so a block of keys with sinks in it has a long list of query rows while the
+// others have a window's.  The rows past its window are cut into chunks that are items of their own; their sums
+// go to slots of the workspace in fp32 and are added in a fixed order.
+constexpr int CHUNK = 16 * BT;              // query rows of a chunk
+constexpr int SINK_BLOCKS = 2;              // key blocks (of 128) that are cut up like this; with more sinks none
+constexpr long long SLOT = 2LL * BT * DH;   // floats: dK and dV of one block
+constexpr long long MAX_SLOTS = 4096;       // 256 MB; calls with more sequences and heads leave the lists whole
+
+__host__ __device__ inline long long chunk_slots(const WindowArgs& p) {
+    return win::block_numbers<CHUNK>(p.Tq, p.n_seq) * p.Hq * SINK_BLOCKS;
+}
+__host__ __device__ inline long long window_slots(const WindowArgs& p) { return (long long)p.n_seq * p.Hk * SINK_BLOCKS; }
+__host__ __device__ inline long long all_slots(const WindowArgs& p) {
+    const long long n = chunk_slots(p) + window_slots(p);
+    return n <= MAX_SLOTS ? n : 0;
+}
+inline bool cuts_sinks(const WindowArgs& p) { return p.sinks > 0 && p.sinks <= SINK_BLOCKS * BT && all_slots(p) > 0; }
+
+// A sequence's queries [ia, ib) that see keys [u0, u1) inside their window (query i has position first + i).
+struct QueryRange {
+    int ia, ib;
+};
+__device__ __forceinline__ QueryRange queries_of(int u0, int u1, int first, int nq, int left, int right) {
+    QueryRange r;
+    r.ia = min(max(u0 - right - first, 0), nq);
+    r.ib = max(min(u1 + left - first, nq), r.ia);
+    return r;
+}
+
+}  // namespace winb
+}  // namespace ttt
