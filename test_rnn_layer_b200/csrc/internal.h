@@ -234,9 +234,8 @@ struct GatedScanArgs {
     const float* dH_T;
     void *dF, *dX;
     float* dH_0;
-    int* status;              // the workspace: status word first
+    int* status;              // cleared by the launch
 };
-long long gated_scan_workspace_bytes(int T, int D);      // after the status word
 long long gated_scan_chunk_state_floats(int T, int D);
 cudaError_t launch_gated_scan(const GatedScanArgs& a, cudaStream_t s);
 cudaError_t launch_gated_scan_backward(const GatedScanArgs& a, cudaStream_t s);

@@ -316,7 +316,7 @@ static ttt_status check_gated(const ttt_gated_scan_desc* q) {
 
 extern "C" TTT_API size_t ttt_gated_scan_workspace_size(const ttt_gated_scan_desc* desc) {
     if (check_gated(desc) != TTT_OK) return 0;
-    return kAlign + align_up((size_t)gated_scan_workspace_bytes(desc->T, desc->D));
+    return kAlign;
 }
 
 extern "C" TTT_API size_t ttt_gated_scan_chunk_states_size(const ttt_gated_scan_desc* desc) {
