@@ -1,0 +1,424 @@
+// Gated linear recurrence h_t = a_t h_{t-1} + s(a_t) x_t, a = sigmoid(f), over long packed sequences: what the
+// forward and the backward kernel share.
+//
+// Each pass reads its inputs and writes its outputs once.  A thread-block cluster owns a strip of channels (LC
+// lanes of two bf16 or one fp32 channel) and walks the whole length; in a step each of its CTAs takes 256 / LC
+// groups of R rows, a thread keeping its R rows' (a, s x) in registers.  The effect of a run of rows on the state
+// is h -> A h + B: groups combine theirs in their warp, warps leave theirs in shared memory, CTAs send theirs to
+// every CTA of the cluster (asynchronous stores to distributed shared memory that count on the receiver's
+// barrier), and everyone walks the state over the runs before its own, one after the other, before it runs its
+// rows from registers.  So the state never leaves the cluster, nothing waits on global memory, and the order of
+// every operation is fixed.  The inputs of the next steps are on their way meanwhile (TMA into a ring of stages).
+// The backward pass is the same walk the other way, lambda -> a (lambda + dy), with h recomputed from states that
+// the forward pass keeps every 8 rows.
+//
+// A sequence's first row in walking order does not take the state before it: such a run has A = -0.  A state that
+// is not finite would still reach through as 0 times it, so where a walk's result is not finite it is done again
+// with the runs' signs looked at.
+//
+// Narrow strips (LC = 16 or 8) serve few channels: the grid is one wave of two CTAs per SM where there are rows
+// enough.  With 1,024 bf16 channels, LC = 32 leaves one CTA per SM and the step's exchange (about 1 us) uncovered.
+// (Tiles that look back at each other's states in global memory in place of the clusters were slower: 2.25 ms for
+// 313,344 rows of 1,024 channels, the hand-over between tiles being the bound.)  Every wait is bounded.
+#pragma once
+
+#include <type_traits>
+
+#include "attn_prims.cuh"
+#include "common.cuh"
+#include "seq_offsets.cuh"
+
+namespace ttt {
+namespace scan {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kKeep = 8;          // rows between two kept states
+constexpr int kRowsF = 16;        // rows of a group, forward
+constexpr int kRowsB = kKeep;     // and backward
+constexpr int kMaxCluster = 8;    // the portable size; of 16 CTAs only 14 clusters at two CTAs per SM fit the card
+constexpr int kStages = 3;
+constexpr float kReset = -0.f;
+
+// ------------------------------------------------------------------ V channels' values, in fp32
+template <int V>
+struct Vec;
+template <>
+struct Vec<1> {
+    float x;
+    __device__ __forceinline__ float get(int) const { return x; }
+    __device__ __forceinline__ void set(int, float v) { x = v; }
+};
+template <>
+struct Vec<2> {
+    uint64_t x;   // a register pair, for the packed arithmetic
+    __device__ __forceinline__ float get(int v) const {
+        float a, b;
+        attn::f2_split(x, a, b);
+        return v ? b : a;
+    }
+    __device__ __forceinline__ void set(int v, float c) {
+        float a, b;
+        attn::f2_split(x, a, b);
+        x = v ? attn::f2(a, c) : attn::f2(c, b);
+    }
+};
+__device__ __forceinline__ Vec<1> fma(Vec<1> a, Vec<1> b, Vec<1> c) { return {fmaf(a.x, b.x, c.x)}; }
+__device__ __forceinline__ Vec<1> mul(Vec<1> a, Vec<1> b) { return {a.x * b.x}; }
+__device__ __forceinline__ Vec<1> add(Vec<1> a, Vec<1> b) { return {a.x + b.x}; }
+__device__ __forceinline__ Vec<1> sub(Vec<1> a, Vec<1> b) { return {a.x - b.x}; }
+__device__ __forceinline__ Vec<2> fma(Vec<2> a, Vec<2> b, Vec<2> c) { return {attn::f2_fma(a.x, b.x, c.x)}; }
+__device__ __forceinline__ Vec<2> add(Vec<2> a, Vec<2> b) { return {attn::f2_add(a.x, b.x)}; }
+__device__ __forceinline__ Vec<2> sub(Vec<2> a, Vec<2> b) { return {attn::f2_sub(a.x, b.x)}; }
+__device__ __forceinline__ Vec<2> mul(Vec<2> a, Vec<2> b) {
+    Vec<2> r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.x) : "l"(a.x), "l"(b.x));
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> all(float c) {
+    if constexpr (V == 1) return {c};
+    else return {attn::f2(c, c)};
+}
+// whether some channel is not finite
+template <int V>
+__device__ __forceinline__ bool wild(Vec<V> a) {
+    const Vec<V> z = mul(a, all<V>(0.f));   // 0 or NaN
+    return !(z.get(0) == 0.f && z.get(V - 1) == 0.f);
+}
+
+// ------------------------------------------------------------------ gates
+// a = sigmoid(f) and rest = 1 - a = sigmoid(-f) from t = exp(-f): 1 / (1 + t) and t / (1 + t), with the rounding
+// of f log2(e) made good (t is good to 2^-22 where the product alone would lose |f| 2^-24).  f is cut to
+// [-80, 128], where a is below 2^-115 and rest zero (exp(-f) leaves fp32 at 87); NaN stays.
+template <int V>
+__device__ __forceinline__ void gates(Vec<V> f, Vec<V>& a, Vec<V>& rest) {
+    constexpr float kL = 1.44269502f, kLow = 1.92596299e-8f, kLn2 = 0.693147182f;   // log2(e) in two parts
+    Vec<V> z, t, r;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float c;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(f.get(v)), "f"(-80.f));
+        asm("min.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(c), "f"(128.f));
+        z.set(v, c);
+    }
+    const Vec<V> y = mul(z, all<V>(-kL));
+    Vec<V> e = fma(z, all<V>(kL), y);
+    e = fma(z, all<V>(kLow), e);
+    e = mul(e, all<V>(-kLn2));
+#pragma unroll
+    for (int v = 0; v < V; ++v) t.set(v, attn::ex2(y.get(v)));
+    t = fma(t, e, t);
+    const Vec<V> d = add(t, all<V>(1.f));
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float q;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(d.get(v)));
+        r.set(v, q);
+    }
+    a = r;
+    rest = mul(t, r);
+}
+
+// b = s(a) x
+template <int FORM, int V>
+__device__ __forceinline__ Vec<V> input(Vec<V> a, Vec<V> rest, Vec<V> x) {
+    if (FORM == 0) return x;
+    if (FORM == 1) return mul(rest, x);
+    Vec<V> s;
+    const Vec<V> w = fma(rest, a, rest);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        float q;
+        asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(w.get(v)));
+        s.set(v, q);
+    }
+    return mul(s, x);
+}
+// s(a) and dh/df = h_before a (1 - a) + x ds/df
+template <int FORM, int V>
+__device__ __forceinline__ void slopes(Vec<V> a, Vec<V> rest, Vec<V> h, Vec<V> x, Vec<V>& s, Vec<V>& d) {
+    if (FORM == 0) {
+        s = all<V>(1.f);
+        d = mul(mul(a, rest), h);
+    } else if (FORM == 1) {
+        s = rest;
+        d = mul(mul(a, rest), sub(h, x));
+    } else {
+        // sqrt(1 - a^2) and its a (1 - a) d/da = -a^2 sqrt((1 - a) / (1 + a)) from one reciprocal root of
+        // 1 - a^2, kept off zero (and a NaN kept)
+        Vec<V> q;
+        const Vec<V> w = fma(rest, a, rest);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            float c;
+            asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(w.get(v)), "f"(1e-37f));
+            asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(c));
+            q.set(v, c);
+        }
+        s = mul(w, q);
+        d = mul(a, sub(mul(rest, h), mul(mul(a, mul(rest, q)), x)));
+    }
+}
+
+// ------------------------------------------------------------------ elements: V of 4 bytes in all
+template <bool BF>
+struct Elem {
+    static constexpr int V = BF ? 2 : 1;
+    using type = std::conditional_t<BF, __nv_bfloat16, float>;
+    static __device__ __forceinline__ Vec<V> get(uint32_t w) {
+        if constexpr (BF) return {attn::f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))};
+        else return {__uint_as_float(w)};
+    }
+    static __device__ __forceinline__ uint32_t put(Vec<V> x) {
+        if constexpr (BF) return attn::pack_bf16(x.get(0), x.get(1));
+        else return __float_as_uint(x.x);
+    }
+};
+
+// ------------------------------------------------------------------ rows
+// A group's R rows, first + dir k: whether they are inside one sequence and neither its first nor its last row,
+// else bits of those in a sequence and of first and last rows in walking order.
+struct Rows {
+    uint32_t valid, start, end;
+    bool plain;
+};
+// [b, e): the sequence that the last look-up found
+template <int R>
+__device__ __forceinline__ Rows rows_of(const SeqOffsets& c, long long first, int dir, int reverse, int& b, int& e) {
+    const long long lo = dir > 0 ? first : first - (R - 1), hi = lo + R - 1;
+    if (!(lo > b && hi < e - 1)) {   // not inside the one before
+        const int s = c.find((int)min(max(lo, 0LL), (long long)c.rows));
+        b = c.begin(s);
+        e = c.begin(s + 1);
+    }
+    Rows r{0, 0, 0, lo > b && hi < e - 1};
+    if (!r.plain) {
+        for (int k = 0; k < R; ++k) {
+            const long long t = first + (long long)dir * k;
+            if (t < 0 || t >= c.rows) continue;
+            const int s = c.find((int)t), sb = c.begin(s), se = c.begin(s + 1);
+            if (t < sb || t >= se) continue;
+            r.valid |= 1u << k;
+            if (t == (reverse ? se - 1 : sb)) r.start |= 1u << k;
+            if (t == (reverse ? sb : se - 1)) r.end |= 1u << k;
+        }
+    }
+    r.plain = __all_sync(0xffffffffu, r.plain);
+    if (r.plain) r.valid = (uint32_t)((1ull << R) - 1);
+    else if (lo > b && hi < e - 1) r.valid = (uint32_t)((1ull << R) - 1);
+    return r;
+}
+
+// A row's values of an fp32 array [n_seq, D] (null: zeros); `on`: the thread has channels.
+template <int V>
+__device__ __forceinline__ Vec<V> state_of(const float* p, const SeqOffsets& c, long long t, int D, int ch, bool on) {
+    Vec<V> r = all<V>(0.f);
+    if (p && on) {
+        const long long at = (long long)c.find((int)t) * D + ch;
+#pragma unroll
+        for (int v = 0; v < V; ++v) r.set(v, p[at + v]);
+    }
+    return r;
+}
+template <int V>
+__device__ __forceinline__ void put_state(float* p, const SeqOffsets& c, long long t, int D, int ch, bool on, Vec<V> h) {
+    if (!p || !on) return;
+    const long long at = (long long)c.find((int)t) * D + ch;
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[at + v] = h.get(v);
+}
+
+// States of empty sequences, and a look over the offsets.
+__device__ __forceinline__ void empty_sequences(const SeqOffsets& c, int D, const float* from, float* to, int* status) {
+    for (int s = blockIdx.x; s < c.n; s += gridDim.x) {
+        if (threadIdx.x == 0 && (c.bad(s) || c.bad(s + 1))) atomicOr(status, kStatusBadOffsets);
+        if (to && c.begin(s) >= c.begin(s + 1))
+            for (int ch = threadIdx.x; ch < D; ch += blockDim.x)
+                to[(long long)s * D + ch] = from ? from[(long long)s * D + ch] : 0.f;
+    }
+}
+
+// ------------------------------------------------------------------ runs
+template <int V>
+struct Run {
+    Vec<V> a, b;
+};
+// run `p` followed by run `q`
+template <int V>
+__device__ __forceinline__ Run<V> then(Run<V> p, Run<V> q) {
+    Run<V> r{mul(p.a, q.a), fma(q.a, p.b, q.b)};
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const bool pr = signbit(p.a.get(v)), qr = signbit(q.a.get(v));
+        if (pr || qr) r.a.set(v, kReset);
+        if (qr) r.b.set(v, q.b.get(v));
+    }
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> over(Run<V> p, Vec<V> h) { return fma(p.a, h, p.b); }
+template <int V>
+__device__ __forceinline__ Vec<V> over_exact(Run<V> p, Vec<V> h) {
+    Vec<V> r = over(p, h);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (signbit(p.a.get(v))) r.set(v, p.b.get(v));
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Run<V> from_lane(Run<V> p, int lane) {
+    Run<V> r;
+    r.a.x = __shfl_sync(0xffffffffu, p.a.x, lane);
+    r.b.x = __shfl_sync(0xffffffffu, p.b.x, lane);
+    return r;
+}
+
+template <int LC, int V>
+struct Shared {
+    Run<V> cta[2][kMaxCluster][LC];   // each CTA's run, for two steps in turn
+    Run<V> part[kWarps][LC];
+    uint64_t full[kStages], sent[2];
+};
+
+// From the groups' runs to the state that enters each group's rows; `state` (the one that enters the cluster's
+// step, the same in every thread of a channel) moves on to the next step.  `consumed` runs once every warp has
+// its inputs in registers.  Returns whether the wait ended in time, the same for the whole CTA.
+template <int LC, int V, class Consumed>
+__device__ __forceinline__ bool exchange(Shared<LC, V>& sh, int step, int cs, int rank, Run<V> mine, Vec<V>& state, Vec<V>& h,
+                                         bool ok, Consumed consumed) {
+    constexpr int G = 32 / LC;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = lane % LC, group = lane / LC;
+    Run<V> total = from_lane<V>(mine, col);
+#pragma unroll
+    for (int g = 1; g < G; ++g) total = then<V>(total, from_lane<V>(mine, g * LC + col));
+    if (lane < LC) sh.part[warp][col] = total;
+    __syncthreads();
+    uint64_t* bar = sh.sent + (step & 1);
+    if (warp == 0) {
+        Run<V> all_rows = sh.part[0][col];
+#pragma unroll
+        for (int i = 1; i < kWarps; ++i) all_rows = then<V>(all_rows, sh.part[i][col]);
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar, cs * LC * V * 8);
+        __syncwarp();
+        const uint32_t to0 = tc::smem_u32(&sh.cta[step & 1][rank][col]), on0 = tc::smem_u32(bar);
+        for (int i = group; i < cs; i += G) {
+            const uint32_t to = tc::mapa_shared(to0, i), on = tc::mapa_shared(on0, i);
+            if constexpr (V == 2)
+                tc::st_async_v4(to, (uint32_t)all_rows.a.x, (uint32_t)(all_rows.a.x >> 32), (uint32_t)all_rows.b.x,
+                                (uint32_t)(all_rows.b.x >> 32), on);
+            else
+                asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(to),
+                             "r"(__float_as_uint(all_rows.a.x)), "r"(__float_as_uint(all_rows.b.x)), "r"(on) : "memory");
+        }
+    } else if (threadIdx.x == 32) {
+        consumed();
+    }
+    // A slot is written again two steps on: its sender has then seen every CTA's next step, which each sends
+    // after it has read this one.
+    ok = tc::mbar_wait_cluster(bar, (step >> 1) & 1) && ok;
+    const Run<V>(*slot)[LC] = sh.cta[step & 1];
+    const Vec<V> before = state;
+    auto walk = [&](auto step_over) {
+        Vec<V> s = before;
+        h = s;
+#pragma unroll
+        for (int i = 0; i < kMaxCluster; ++i) {
+            if (i < cs) {
+                if (i == rank) h = s;
+                s = step_over(slot[i][col], s);
+            }
+        }
+        for (int i = 0; i < warp; ++i) h = step_over(sh.part[i][col], h);
+#pragma unroll
+        for (int g = 0; g < G - 1; ++g) {
+            const Vec<V> n = step_over(from_lane<V>(mine, g * LC + col), h);
+            if (g < group) h = n;
+        }
+        state = s;
+    };
+    walk([](Run<V> p, Vec<V> s) { return over<V>(p, s); });
+    if (__any_sync(0xffffffffu, wild<V>(h) || wild<V>(state))) walk([](Run<V> p, Vec<V> s) { return over_exact<V>(p, s); });
+    return __syncthreads_and(ok);   // part is free again
+}
+
+struct Maps {
+    CUtensorMap f, x, dy, h;   // boxes of a strip x a tile's rows; h: a tile's kept states
+};
+
+__device__ __forceinline__ int cluster_size() {
+    int n;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
+    return n;
+}
+
+// Copies in flight land before a block that gave up leaves its memory.
+__device__ __forceinline__ void settle() {
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (tc::globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+}
+
+// ------------------------------------------------------------------ host
+// rows of `cols` elements, boxes of `width` x `height`, no swizzle, zeros outside
+inline bool map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, long long rows, int cols, long long ld, int width, int height) {
+    auto fn = attn::encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld * (dt == CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 ? 2 : 4)};
+    cuuint32_t box[2] = {(cuuint32_t)width, (cuuint32_t)height};
+    cuuint32_t es[2] = {1, 1};
+    return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One launch: kernel(args, maps) on strips x cluster CTAs.  R: rows of a group; arrays: inputs per stage.
+template <bool BF, int LC, int R, class Kernel>
+cudaError_t launch(Kernel kernel, const GatedScanArgs& a, bool backward, int cs, cudaStream_t s) {
+    constexpr int W = LC * Elem<BF>::V, TILE = kThreads / LC * R, ARRAYS_F = 2, ARRAYS_B = 3;
+    static_assert(TILE <= 256 || LC < 32, "a box has at most 256 rows");
+    constexpr int BOX = TILE < 256 ? TILE : 256, HBOX = TILE / kKeep < 256 ? TILE / kKeep : 256;
+    Maps m{};
+    const CUtensorMapDataType dt = BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const long long keeps = ((long long)a.T + kKeep - 1) / kKeep;
+    if (a.T > 0 && (!map_2d(&m.f, dt, a.F, a.T, a.D, a.ld_f, W, BOX) || !map_2d(&m.x, dt, a.X, a.T, a.D, a.ld_x, W, BOX) ||
+                    (backward && (!map_2d(&m.dy, dt, a.dY, a.T, a.D, a.ld_dy, W, BOX) ||
+                                  !map_2d(&m.h, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.chunk_states, keeps, a.D, a.D, W, HBOX)))))
+        return cudaErrorInvalidValue;
+    const int smem = kStages * ((backward ? ARRAYS_B : ARRAYS_F) * TILE * LC * 4 + (backward ? TILE / kKeep * W * 4 : 0));
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((a.D + W - 1) / W * cs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = cs;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a, m);
+}
+
+// The strip's width and the cluster's size: the widest strips (whole 128-byte lines) whose clusters of up to eight
+// CTAs fill more than half of the card's two CTAs per SM, and no more CTAs than there are tiles of rows.
+struct Shape {
+    int lanes, cs;
+};
+inline Shape shape_of(const GatedScanArgs& a, int R) {
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int V = a.bf16 ? 2 : 1;
+    auto strips = [&](int lanes) { return (a.D + lanes * V - 1) / (lanes * V); };
+    Shape q{32, 1};
+    while (q.lanes > 8 && 2LL * kMaxCluster * strips(q.lanes / 2) <= 4LL * sms && strips(q.lanes / 2) > strips(q.lanes)) {
+        if ((long long)kMaxCluster * strips(q.lanes / 2) > 2 * sms) break;
+        q.lanes /= 2;
+    }
+    while (q.cs < kMaxCluster && 2LL * q.cs * strips(q.lanes) <= 2 * sms && (long long)q.cs * (kThreads / q.lanes * R) < a.T) q.cs *= 2;
+    return q;
+}
+
+}  // namespace scan
+}  // namespace ttt
