@@ -38,82 +38,86 @@ __global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(const __grid_con
     }
     tc::cluster_sync();   // every CTA runs and has its barriers: its shared memory may be written
     if (threadIdx.x == 32)
-        for (int s = 0; s < kStages; ++s) issue(s);
+        for (int s = 0; s < kStages - 1; ++s) issue(s);
 
     Vec<V> state = all<V>(0.f);
     bool bad = false, ok = true;
     int seq_b = 0, seq_e = 0;
-    for (int step = 0; step < steps && ok; ++step) {
+    Cursor at_row;
+    for (int step = 0; step < steps; ++step) {
         // the group's first row in walking order; past the last chunk outside [0, T)
-        const long long chunk = (long long)step * cs + rank;
-        const long long t0 = p.reverse ? (chunks - chunk) * TILE - 1 - group * R : chunk * TILE + group * R;
-        const Rows r = rows_of<R>(c, t0, dir, p.reverse, seq_b, seq_e);
+        const int chunk = step * cs + rank;
+        const int t0 = p.reverse ? (chunks - chunk) * TILE - 1 - group * R : chunk * TILE + group * R;
+        const bool plain = plain_rows<R>(c, t0, dir, seq_b, seq_e);
+        if (chunk < chunks) ok = tc::mbar_wait(sh.full + step % kStages, (step / kStages) & 1, nullptr);
+        const uint8_t* in = stages + step % kStages * STAGE + ((p.reverse ? TILE - 1 - group * R : group * R) * LC + col) * 4;
+        const int pitch_in = dir * LC * 4;
+        auto load = [&](const uint8_t* at, Vec<V>& a, Vec<V>& b) {
+            const Vec<V> f = Elem<BF>::get(*reinterpret_cast<const uint32_t*>(at));
+            const Vec<V> x = Elem<BF>::get(*reinterpret_cast<const uint32_t*>(at + TILE * LC * 4));
+            Vec<V> rest;
+            gates<V>(f, a, rest);
+            b = input<FORM, V>(a, rest, x);
+        };
         Vec<V> a[R], b[R], h;
         Run<V> run{all<V>(1.f), all<V>(0.f)};
-        if (chunk < chunks) ok = tc::mbar_wait(sh.full + step % kStages, (step / kStages) & 1, nullptr);
-        {
-            const uint8_t* in = stages + step % kStages * STAGE + ((p.reverse ? TILE - 1 - group * R : group * R) * LC + col) * 4;
-            const int pitch = dir * LC * 4;
+        if (plain) {
+            const uint8_t* at = in;
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                const Vec<V> f = Elem<BF>::get(*reinterpret_cast<const uint32_t*>(in));
-                const Vec<V> x = Elem<BF>::get(*reinterpret_cast<const uint32_t*>(in + TILE * LC * 4));
-                in += pitch;
-                Vec<V> rest;
-                gates<V>(f, a[k], rest);
-                b[k] = input<FORM, V>(a[k], rest, x);
-            }
-        }
-        if (r.plain) {
-#pragma unroll
-            for (int k = 0; k < R; ++k) {
+                load(at, a[k], b[k]);
+                at += pitch_in;
                 run.b = fma(a[k], run.b, b[k]);
                 run.a = mul(run.a, a[k]);
             }
         } else {
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < R; ++k) {
-                if ((r.start >> k) & 1u) {   // the first row: b includes what the initial state leaves
-                    b[k] = fma(a[k], state_of<V>(p.H_0, c, t0 + dir * k, p.D, ch, on), b[k]);
-                    run = Run<V>{all<V>(kReset), b[k]};
-                } else if ((r.valid >> k) & 1u) {
-                    run.b = fma(a[k], run.b, b[k]);
-                    run.a = mul(run.a, a[k]);   // -0 stays -0
+                const Row q = row_of(c, at_row, t0 + dir * k, p.reverse);
+                if (q.s < 0) continue;
+                Vec<V> ak, bk;
+                load(in + k * pitch_in, ak, bk);
+                if (q.start) {
+                    run = Run<V>{all<V>(kReset), fma(ak, state_of<V>(p.H_0, q.s, p.D, ch, on), bk)};
+                } else {
+                    run.b = fma(ak, run.b, bk);
+                    run.a = mul(run.a, ak);   // -0 stays -0
                 }
             }
         }
-        ok = exchange<LC, V>(sh, step, cs, rank, run, state, h, ok, [&]() { issue(step + kStages); });
-        // states that enter segments of kKeep rows
-        const long long seg0 = t0 < 0 ? -1 : t0 / kKeep;
-        auto keep = [&](int k) {
-            const long long seg = seg0 + dir * (k / kKeep);
-            if (p.chunk_states && on && seg0 >= 0 && seg * kKeep < p.T) {
+        if (!exchange<LC, V>(sh, step, cs, rank, run, state, h, ok, [&]() { issue(step + kStages - 1); })) break;
+        // the states that enter segments of kKeep rows
+        auto keep = [&](int t) {
+            const long long seg = t / kKeep;
+            if (p.chunk_states && on && t >= 0 && seg * kKeep < p.T) {
                 if constexpr (V == 2) *reinterpret_cast<uint64_t*>(p.chunk_states + seg * p.D + ch) = h.x;
                 else p.chunk_states[seg * p.D + ch] = h.x;
             }
         };
-        typename Elem<BF>::type* y = static_cast<typename Elem<BF>::type*>(p.Y) + t0 * p.ld_y + ch;
+        typename Elem<BF>::type* y = static_cast<typename Elem<BF>::type*>(p.Y) + (long long)t0 * p.ld_y + ch;
         const long long pitch = dir * p.ld_y;
-        if (r.plain) {
+        if (plain) {
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                if (k % kKeep == 0) keep(k);
+                if (k % kKeep == 0) keep(t0 + dir * k);
                 h = fma(a[k], h, b[k]);
                 if (on) __stcs(reinterpret_cast<uint32_t*>(y), Elem<BF>::put(h));
                 y += pitch;
             }
             bad |= on && wild<V>(h);   // inside a sequence a state that is not finite stays so
         } else {
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < R; ++k) {
-                if (k % kKeep == 0) keep(k);
-                if ((r.valid >> k) & 1u) {
-                    h = (r.start >> k) & 1u ? b[k] : fma(a[k], h, b[k]);
-                    bad |= on && wild<V>(h);
-                    if (on) __stcs(reinterpret_cast<uint32_t*>(y), Elem<BF>::put(h));
-                    if ((r.end >> k) & 1u) put_state<V>(p.H_T, c, t0 + dir * k, p.D, ch, on, h);
-                }
-                y += pitch;
+                if (k % kKeep == 0) keep(t0 + dir * k);
+                const Row q = row_of(c, at_row, t0 + dir * k, p.reverse);
+                if (q.s < 0) continue;
+                Vec<V> ak, bk;
+                load(in + k * pitch_in, ak, bk);
+                if (q.start) h = state_of<V>(p.H_0, q.s, p.D, ch, on);
+                h = fma(ak, h, bk);
+                bad |= on && wild<V>(h);
+                if (on) __stcs(reinterpret_cast<uint32_t*>(y + k * pitch), Elem<BF>::put(h));
+                if (q.end) put_state<V>(p.H_T, q.s, p.D, ch, on, h);
             }
         }
     }

@@ -176,54 +176,54 @@ struct Elem {
 };
 
 // ------------------------------------------------------------------ rows
-// A group's R rows, first + dir k: whether they are inside one sequence and neither its first nor its last row,
-// else bits of those in a sequence and of first and last rows in walking order.
-struct Rows {
-    uint32_t valid, start, end;
-    bool plain;
-};
-// [b, e): the sequence that the last look-up found
+// Whether R rows lie inside one sequence and none is its first or last one ([b, e): the sequence that the last
+// look-up found).  Where they do not, the rows are walked one by one from shared memory, in rolled loops: the
+// code of the common case stays small enough for the instruction cache.
 template <int R>
-__device__ __forceinline__ Rows rows_of(const SeqOffsets& c, long long first, int dir, int reverse, int& b, int& e) {
-    const long long lo = dir > 0 ? first : first - (R - 1), hi = lo + R - 1;
-    if (!(lo > b && hi < e - 1)) {   // not inside the one before
-        const int s = c.find((int)min(max(lo, 0LL), (long long)c.rows));
+__device__ __forceinline__ bool plain_rows(const SeqOffsets& c, int first, int dir, int& b, int& e) {
+    const int lo = dir > 0 ? first : first - (R - 1), hi = lo + R - 1;
+    if (!(lo > b && hi < e - 1)) {
+        const int s = c.find(min(max(lo, 0), c.rows));
         b = c.begin(s);
         e = c.begin(s + 1);
     }
-    Rows r{0, 0, 0, lo > b && hi < e - 1};
-    if (!r.plain) {
-        for (int k = 0; k < R; ++k) {
-            const long long t = first + (long long)dir * k;
-            if (t < 0 || t >= c.rows) continue;
-            const int s = c.find((int)t), sb = c.begin(s), se = c.begin(s + 1);
-            if (t < sb || t >= se) continue;
-            r.valid |= 1u << k;
-            if (t == (reverse ? se - 1 : sb)) r.start |= 1u << k;
-            if (t == (reverse ? sb : se - 1)) r.end |= 1u << k;
-        }
+    return __all_sync(0xffffffffu, lo > b && hi < e - 1);
+}
+// One row: its sequence (-1: none), and whether it is the first and the last one in walking order.  The cursor
+// holds the sequence of the row before.
+struct Row {
+    int s;
+    bool start, end;
+};
+struct Cursor {
+    int s = 0, b = 0, e = 0;
+};
+__device__ __forceinline__ Row row_of(const SeqOffsets& c, Cursor& at, int t, int reverse) {
+    if (t < 0 || t >= c.rows) return {-1, false, false};
+    if (t < at.b || t >= at.e) {
+        at.s = c.find(t);
+        at.b = c.begin(at.s);
+        at.e = c.begin(at.s + 1);
+        if (t < at.b || t >= at.e) return {-1, false, false};
     }
-    r.plain = __all_sync(0xffffffffu, r.plain);
-    if (r.plain) r.valid = (uint32_t)((1ull << R) - 1);
-    else if (lo > b && hi < e - 1) r.valid = (uint32_t)((1ull << R) - 1);
-    return r;
+    return {at.s, t == (reverse ? at.e - 1 : at.b), t == (reverse ? at.b : at.e - 1)};
 }
 
-// A row's values of an fp32 array [n_seq, D] (null: zeros); `on`: the thread has channels.
+// Sequence s's values of an fp32 array [n_seq, D] (null: zeros); `on`: the thread has channels.
 template <int V>
-__device__ __forceinline__ Vec<V> state_of(const float* p, const SeqOffsets& c, long long t, int D, int ch, bool on) {
+__device__ __forceinline__ Vec<V> state_of(const float* p, int s, int D, int ch, bool on) {
     Vec<V> r = all<V>(0.f);
     if (p && on) {
-        const long long at = (long long)c.find((int)t) * D + ch;
+        const long long at = (long long)s * D + ch;
 #pragma unroll
         for (int v = 0; v < V; ++v) r.set(v, p[at + v]);
     }
     return r;
 }
 template <int V>
-__device__ __forceinline__ void put_state(float* p, const SeqOffsets& c, long long t, int D, int ch, bool on, Vec<V> h) {
+__device__ __forceinline__ void put_state(float* p, int s, int D, int ch, bool on, Vec<V> h) {
     if (!p || !on) return;
-    const long long at = (long long)c.find((int)t) * D + ch;
+    const long long at = (long long)s * D + ch;
 #pragma unroll
     for (int v = 0; v < V; ++v) p[at + v] = h.get(v);
 }
@@ -273,72 +273,114 @@ __device__ __forceinline__ Run<V> from_lane(Run<V> p, int lane) {
     return r;
 }
 
+// Several runs in a row; the exact form only where one of them has a reset.
+template <int V, int N>
+__device__ __forceinline__ Run<V> compose(const Run<V> (&q)[N]) {
+    bool reset = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) reset |= signbit(q[i].a.get(0)) || signbit(q[i].a.get(V - 1));
+    Run<V> r = q[0];
+    if (__any_sync(0xffffffffu, reset)) {
+#pragma unroll
+        for (int i = 1; i < N; ++i) r = then<V>(r, q[i]);
+    } else {
+#pragma unroll
+        for (int i = 1; i < N; ++i) r = Run<V>{mul(r.a, q[i].a), fma(q[i].a, r.b, q[i].b)};
+    }
+    return r;
+}
+
 template <int LC, int V>
 struct Shared {
     Run<V> cta[2][kMaxCluster][LC];   // each CTA's run, for two steps in turn
-    Run<V> part[kWarps][LC];
+    Run<V> part[kWarps][LC];          // each warp's
+    Vec<V> enter[kWarps][LC];         // the state that enters each warp's rows
     uint64_t full[kStages], sent[2];
 };
 
-// From the groups' runs to the state that enters each group's rows; `state` (the one that enters the cluster's
-// step, the same in every thread of a channel) moves on to the next step.  `consumed` runs once every warp has
-// its inputs in registers.  Returns whether the wait ended in time, the same for the whole CTA.
+// From the groups' runs to the state h that enters each group's rows.  Warp 0 does the work between two barriers
+// (done by every warp for itself it was 40% of all instructions): `state`, the one that enters the cluster's
+// step, is its alone.  `consumed` runs once every warp is through with the step before.  `ok`: whether every wait
+// so far ended in time; returns false, for the whole CTA alike, if one of any thread's before this call did not.
 template <int LC, int V, class Consumed>
 __device__ __forceinline__ bool exchange(Shared<LC, V>& sh, int step, int cs, int rank, Run<V> mine, Vec<V>& state, Vec<V>& h,
-                                         bool ok, Consumed consumed) {
+                                         bool& ok, Consumed consumed) {
     constexpr int G = 32 / LC;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = lane % LC, group = lane / LC;
-    Run<V> total = from_lane<V>(mine, col);
+    Run<V> before = mine;   // G > 1: the runs of the warp's groups in front of this one
+    if constexpr (G == 1) {
+        sh.part[warp][col] = mine;
+    } else {
+        const Run<V> none{all<V>(1.f), all<V>(0.f)};
+        Run<V> groups[G], front[G];
 #pragma unroll
-    for (int g = 1; g < G; ++g) total = then<V>(total, from_lane<V>(mine, g * LC + col));
-    if (lane < LC) sh.part[warp][col] = total;
-    __syncthreads();
-    uint64_t* bar = sh.sent + (step & 1);
+        for (int g = 0; g < G; ++g) groups[g] = from_lane<V>(mine, g * LC + col);
+        front[0] = none;
+#pragma unroll
+        for (int g = 0; g < G - 1; ++g) front[g + 1] = g < group ? groups[g] : none;
+        before = compose<V, G>(front);
+        const Run<V> total = compose<V, G>(groups);
+        if (lane < LC) sh.part[warp][col] = total;
+    }
+    if (!__syncthreads_and(ok)) return false;
     if (warp == 0) {
-        Run<V> all_rows = sh.part[0][col];
+        uint64_t* bar = sh.sent + (step & 1);
+        Run<V> q[kWarps];
 #pragma unroll
-        for (int i = 1; i < kWarps; ++i) all_rows = then<V>(all_rows, sh.part[i][col]);
+        for (int i = 0; i < kWarps; ++i) q[i] = sh.part[i][col];
+        const Run<V> total = compose<V, kWarps>(q);
         if (lane == 0) tc::mbar_arrive_expect_tx(bar, cs * LC * V * 8);
         __syncwarp();
         const uint32_t to0 = tc::smem_u32(&sh.cta[step & 1][rank][col]), on0 = tc::smem_u32(bar);
-        for (int i = group; i < cs; i += G) {
-            const uint32_t to = tc::mapa_shared(to0, i), on = tc::mapa_shared(on0, i);
-            if constexpr (V == 2)
-                tc::st_async_v4(to, (uint32_t)all_rows.a.x, (uint32_t)(all_rows.a.x >> 32), (uint32_t)all_rows.b.x,
-                                (uint32_t)(all_rows.b.x >> 32), on);
-            else
-                asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(to),
-                             "r"(__float_as_uint(all_rows.a.x)), "r"(__float_as_uint(all_rows.b.x)), "r"(on) : "memory");
+#pragma unroll
+        for (int j = 0; j < kMaxCluster; j += G) {
+            const int i = j + group;
+            if (i < cs) {
+                const uint32_t to = tc::mapa_shared(to0, i), on = tc::mapa_shared(on0, i);
+                if constexpr (V == 2)
+                    tc::st_async_v4(to, (uint32_t)total.a.x, (uint32_t)(total.a.x >> 32), (uint32_t)total.b.x,
+                                    (uint32_t)(total.b.x >> 32), on);
+                else
+                    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(to),
+                                 "r"(__float_as_uint(total.a.x)), "r"(__float_as_uint(total.b.x)), "r"(on) : "memory");
+            }
         }
+        // A slot is written again two steps on: its sender has then seen every CTA's next step, which each sends
+        // after it has read this one.
+        ok = tc::mbar_wait_cluster(bar, (step >> 1) & 1);
+        const Run<V>(*slot)[LC] = sh.cta[step & 1];
+        const Vec<V> s0 = state;
+        auto walk = [&](auto step_over) {
+            Vec<V> s = s0, e = s0;
+#pragma unroll
+            for (int i = 0; i < kMaxCluster; ++i) {
+                if (i < cs) {
+                    if (i == rank) e = s;
+                    s = step_over(slot[i][col], s);
+                }
+            }
+            state = s;
+            if (lane < LC) sh.enter[0][col] = e;
+#pragma unroll
+            for (int i = 0; i < kWarps - 1; ++i) {
+                e = step_over(q[i], e);
+                if (lane < LC) sh.enter[i + 1][col] = e;
+            }
+            return wild<V>(s) || wild<V>(e);
+        };
+        if (__any_sync(0xffffffffu, walk([](Run<V> p, Vec<V> s) { return over<V>(p, s); })))
+            walk([](Run<V> p, Vec<V> s) { return over_exact<V>(p, s); });
     } else if (threadIdx.x == 32) {
         consumed();
     }
-    // A slot is written again two steps on: its sender has then seen every CTA's next step, which each sends
-    // after it has read this one.
-    ok = tc::mbar_wait_cluster(bar, (step >> 1) & 1) && ok;
-    const Run<V>(*slot)[LC] = sh.cta[step & 1];
-    const Vec<V> before = state;
-    auto walk = [&](auto step_over) {
-        Vec<V> s = before;
-        h = s;
-#pragma unroll
-        for (int i = 0; i < kMaxCluster; ++i) {
-            if (i < cs) {
-                if (i == rank) h = s;
-                s = step_over(slot[i][col], s);
-            }
-        }
-        for (int i = 0; i < warp; ++i) h = step_over(sh.part[i][col], h);
-#pragma unroll
-        for (int g = 0; g < G - 1; ++g) {
-            const Vec<V> n = step_over(from_lane<V>(mine, g * LC + col), h);
-            if (g < group) h = n;
-        }
-        state = s;
-    };
-    walk([](Run<V> p, Vec<V> s) { return over<V>(p, s); });
-    if (__any_sync(0xffffffffu, wild<V>(h) || wild<V>(state))) walk([](Run<V> p, Vec<V> s) { return over_exact<V>(p, s); });
-    return __syncthreads_and(ok);   // part is free again
+    __syncthreads();
+    h = sh.enter[warp][col];
+    if constexpr (G > 1) {
+        const Vec<V> e = h;
+        h = over<V>(before, e);
+        if (wild<V>(h)) h = over_exact<V>(before, e);
+    }
+    return true;
 }
 
 struct Maps {

@@ -41,84 +41,111 @@ __global__ void __launch_bounds__(kThreads, 2) gated_bwd_kernel(const __grid_con
     }
     tc::cluster_sync();   // every CTA runs and has its barriers: its shared memory may be written
     if (threadIdx.x == 32)
-        for (int s = 0; s < kStages; ++s) issue(s);
+        for (int s = 0; s < kStages - 1; ++s) issue(s);
 
     Vec<V> state = all<V>(0.f);
     bool bad = false, ok = true;
     int seq_b = 0, seq_e = 0;
-    for (int step = 0; step < steps && ok; ++step) {
+    Cursor at_row;
+    using T = typename Elem<BF>::type;
+    for (int step = 0; step < steps; ++step) {
         // the group's first row in lambda's order; past the last chunk outside [0, T)
-        const long long chunk = (long long)step * cs + rank;
-        const long long t0 = p.reverse ? chunk * TILE + group * R : (chunks - chunk) * TILE - 1 - group * R;
-        const Rows r = rows_of<R>(c, t0, dir, p.reverse, seq_b, seq_e);
-        Vec<V> a[R], sc[R], sl[R], lam;
-        uint32_t gw[R];
-        Run<V> run{all<V>(1.f), all<V>(0.f)};
+        const int chunk = step * cs + rank;
+        const int t0 = p.reverse ? chunk * TILE + group * R : (chunks - chunk) * TILE - 1 - group * R;
+        const bool plain = plain_rows<R>(c, t0, dir, seq_b, seq_e);
         if (chunk < chunks) ok = tc::mbar_wait(sh.full + step % kStages, (step / kStages) & 1, nullptr);
-        {
-            const uint8_t* st = stages + step % kStages * STAGE;
-            const int seg = p.reverse ? group : kThreads / LC - 1 - group;   // in the tile
-            Vec<V> h = *reinterpret_cast<const Vec<V>*>(st + 3 * ARRAY + (seg * LC + col) * V * 4);
-            // forward over the rows: from the last in lambda's order
-            const uint8_t* in = st + ((seg * R + (p.reverse ? R - 1 : 0)) * LC + col) * 4;
-            const int pitch = -dir * LC * 4;
+        const uint8_t* st = stages + step % kStages * STAGE;
+        const int seg = p.reverse ? group : kThreads / LC - 1 - group;   // in the tile
+        const Vec<V> kept = *reinterpret_cast<const Vec<V>*>(st + 3 * ARRAY + (seg * LC + col) * V * 4);
+        // row k = 0 in lambda's order; the forward walk begins at k = R - 1
+        const uint8_t* in = st + ((seg * R + (p.reverse ? 0 : R - 1)) * LC + col) * 4;
+        const int pitch_in = dir * LC * 4;
+        auto word = [&](int array, int k) { return *reinterpret_cast<const uint32_t*>(in + array * ARRAY + k * pitch_in); };
+        Vec<V> a[R], sc[R], sl[R], dy[R], lam;
+        Run<V> run{all<V>(1.f), all<V>(0.f)};
+        if (plain) {
+            Vec<V> h = kept;
 #pragma unroll
             for (int k = R - 1; k >= 0; --k) {
-                const Vec<V> f = Elem<BF>::get(*reinterpret_cast<const uint32_t*>(in));
-                const Vec<V> x = Elem<BF>::get(*reinterpret_cast<const uint32_t*>(in + ARRAY));
-                gw[k] = *reinterpret_cast<const uint32_t*>(in + 2 * ARRAY);
-                in += pitch;
+                const Vec<V> x = Elem<BF>::get(word(1, k));
                 Vec<V> rest;
-                gates<V>(f, a[k], rest);
-                if (!r.plain && ((r.start >> k) & 1u)) h = state_of<V>(p.H_0, c, t0 + dir * k, p.D, ch, on);
+                gates<V>(Elem<BF>::get(word(0, k)), a[k], rest);
                 slopes<FORM, V>(a[k], rest, h, x, sc[k], sl[k]);
-                // rows of no sequence come before a first row or after a last one: what h is there does not matter
                 h = fma(a[k], h, mul(sc[k], x));
             }
-        }
-        if (r.plain) {
 #pragma unroll
             for (int k = 0; k < R; ++k) {
-                run.b = mul(a[k], add(run.b, Elem<BF>::get(gw[k])));
+                dy[k] = Elem<BF>::get(word(2, k));
+                run.b = mul(a[k], add(run.b, dy[k]));
                 run.a = mul(run.a, a[k]);
             }
         } else {
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < R; ++k) {
-                const Vec<V> dy = Elem<BF>::get(gw[k]);
-                if ((r.end >> k) & 1u) {   // lambda starts anew, with the final state's gradient
-                    run = Run<V>{all<V>(kReset), mul(a[k], add(dy, state_of<V>(p.dH_T, c, t0 + dir * k, p.D, ch, on)))};
-                } else if ((r.valid >> k) & 1u) {
-                    run.b = mul(a[k], add(run.b, dy));
-                    run.a = mul(run.a, a[k]);   // -0 stays -0
+                const Row q = row_of(c, at_row, t0 + dir * k, p.reverse);
+                if (q.s < 0) continue;
+                Vec<V> ak, rest;
+                gates<V>(Elem<BF>::get(word(0, k)), ak, rest);
+                const Vec<V> g = Elem<BF>::get(word(2, k));
+                if (q.end) {   // lambda starts anew, with the final state's gradient
+                    run = Run<V>{all<V>(kReset), mul(ak, add(state_of<V>(p.dH_T, q.s, p.D, ch, on), g))};
+                } else {
+                    run.b = mul(ak, add(run.b, g));
+                    run.a = mul(run.a, ak);   // -0 stays -0
                 }
             }
         }
-        ok = exchange<LC, V>(sh, step, cs, rank, run, state, lam, ok, [&]() { issue(step + kStages); });
-        using T = typename Elem<BF>::type;
-        T* df = static_cast<T*>(p.dF) + t0 * p.ld_df + ch;
-        T* dx = static_cast<T*>(p.dX) + t0 * p.ld_dx + ch;
+        if (!exchange<LC, V>(sh, step, cs, rank, run, state, lam, ok, [&]() { issue(step + kStages - 1); })) break;
+        T* df = static_cast<T*>(p.dF) + (long long)t0 * p.ld_df + ch;
+        T* dx = static_cast<T*>(p.dX) + (long long)t0 * p.ld_dx + ch;
         const long long pitch_f = dir * p.ld_df, pitch_x = dir * p.ld_dx;
         Vec<V> seen = all<V>(0.f);   // 0 times what is stored: NaN where it is not finite
+        if (plain) {
 #pragma unroll
-        for (int k = 0; k < R; ++k) {
-            if (r.plain || ((r.valid >> k) & 1u)) {
-                if (!r.plain && ((r.end >> k) & 1u)) lam = state_of<V>(p.dH_T, c, t0 + dir * k, p.D, ch, on);
-                const Vec<V> l = add(lam, Elem<BF>::get(gw[k]));
-                const Vec<V> d = mul(l, sl[k]);
+            for (int k = 0; k < R; ++k) {
+                const Vec<V> l = add(lam, dy[k]), d = mul(l, sl[k]);
                 seen = fma(all<V>(0.f), d, seen);
                 lam = mul(a[k], l);
-                if (!r.plain) seen = fma(all<V>(0.f), lam, seen);
                 if (on) {
                     __stcs(reinterpret_cast<uint32_t*>(df), Elem<BF>::put(d));
                     __stcs(reinterpret_cast<uint32_t*>(dx), Elem<BF>::put(mul(l, sc[k])));
                 }
-                if (!r.plain && ((r.start >> k) & 1u)) put_state<V>(p.dH_0, c, t0 + dir * k, p.D, ch, on, lam);
+                df += pitch_f;
+                dx += pitch_x;
             }
-            df += pitch_f;
-            dx += pitch_x;
+            seen = fma(all<V>(0.f), lam, seen);   // inside a sequence what is not finite stays so
+        } else {
+            Vec<V> before[R];   // h before each row (a short array in local memory)
+            Vec<V> h = kept;
+#pragma unroll 1
+            for (int k = R - 1; k >= 0; --k) {
+                const Row q = row_of(c, at_row, t0 + dir * k, p.reverse);
+                if (q.s < 0) continue;
+                if (q.start) h = state_of<V>(p.H_0, q.s, p.D, ch, on);
+                before[k] = h;
+                Vec<V> ak, rest;
+                gates<V>(Elem<BF>::get(word(0, k)), ak, rest);
+                h = fma(ak, h, input<FORM, V>(ak, rest, Elem<BF>::get(word(1, k))));
+            }
+#pragma unroll 1
+            for (int k = 0; k < R; ++k) {
+                const Row q = row_of(c, at_row, t0 + dir * k, p.reverse);
+                if (q.s < 0) continue;
+                Vec<V> ak, rest, s, slope;
+                gates<V>(Elem<BF>::get(word(0, k)), ak, rest);
+                slopes<FORM, V>(ak, rest, before[k], Elem<BF>::get(word(1, k)), s, slope);
+                if (q.end) lam = state_of<V>(p.dH_T, q.s, p.D, ch, on);
+                const Vec<V> l = add(lam, Elem<BF>::get(word(2, k))), d = mul(l, slope);
+                lam = mul(ak, l);
+                seen = fma(all<V>(0.f), d, seen);
+                seen = fma(all<V>(0.f), lam, seen);
+                if (on) {
+                    *reinterpret_cast<uint32_t*>(df + k * pitch_f) = Elem<BF>::put(d);
+                    *reinterpret_cast<uint32_t*>(dx + k * pitch_x) = Elem<BF>::put(mul(l, s));
+                }
+                if (q.start) put_state<V>(p.dH_0, q.s, p.D, ch, on, lam);
+            }
         }
-        if (r.plain) seen = fma(all<V>(0.f), lam, seen);   // inside a sequence what is not finite stays so
         bad |= on && wild<V>(seen);
     }
     if (bad) atomicOr(p.status, kStatusNonFinite);
