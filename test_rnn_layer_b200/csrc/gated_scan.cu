@@ -7,122 +7,140 @@ namespace {
 using namespace scan;
 
 template <bool BF, int FORM, int LC>
-__global__ void __launch_bounds__(kThreads, 2) gated_fwd_kernel(const __grid_constant__ GatedScanArgs p, const __grid_constant__ Maps m) {
-    constexpr int R = kRowsF, V = Elem<BF>::V, TILE = kThreads / LC * R, STAGE = 2 * TILE * LC * 4;
-    __shared__ Shared<LC, V> sh;
+__global__ void __launch_bounds__(32 * (kWarpsF + 1), kPerSmF)
+    gated_fwd_kernel(const __grid_constant__ GatedScanArgs p, const __grid_constant__ Maps m) {
+    constexpr int R = kRows, W = kWarpsF, V = Elem<BF>::V, TILE = 32 / LC * W * R, ARRAY = TILE * LC * 4, STAGE = 2 * ARRAY;
+    __shared__ Shared<LC, V, W> sh;
     extern __shared__ __align__(128) uint8_t stages[];
     const SeqOffsets c{p.cu, p.n_seq, p.T};
     const int cs = cluster_size(), rank = tc::cluster_ctarank(), chunks = (p.T + TILE - 1) / TILE, steps = (chunks + cs - 1) / cs;
-    const int col = threadIdx.x % LC, group = threadIdx.x / LC, dir = p.reverse ? -1 : 1;
-    const int strip = blockIdx.x / cs * LC * V, ch = strip + col * V;
-    const bool on = ch < p.D;
+    const int strip = blockIdx.x / cs * LC * V;
     empty_sequences(c, p.D, p.H_0, p.H_T, p.status);
-
-    // stage s: TILE rows of the strip of F, then of X
-    auto issue = [&](int step) {
-        const int chunk = step * cs + rank, s = step % kStages;
-        if (step >= steps || chunk >= chunks) return;
-        const int row = (p.reverse ? chunks - 1 - chunk : chunk) * TILE;
-        uint8_t* to = stages + s * STAGE;
-        tc::mbar_arrive_expect_tx(sh.full + s, STAGE);
-#pragma unroll
-        for (int i = 0; i < TILE; i += 256) {
-            tc::tma_load_2d(to + i * LC * 4, &m.f, strip, row + i, sh.full + s);
-            tc::tma_load_2d(to + (TILE + i) * LC * 4, &m.x, strip, row + i, sh.full + s);
-        }
-    };
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) tc::mbar_init(sh.full + s, 1);
-        for (int s = 0; s < 2; ++s) tc::mbar_init(sh.sent + s, 1);
-        tc::fence_mbar_init();
-    }
-    tc::cluster_sync();   // every CTA runs and has its barriers: its shared memory may be written
-    if (threadIdx.x == 32)
-        for (int s = 0; s < kStages - 1; ++s) issue(s);
-
-    Vec<V> state = all<V>(0.f);
-    bool bad = false, ok = true;
-    int seq_b = 0, seq_e = 0;
-    Cursor at_row;
-    for (int step = 0; step < steps; ++step) {
-        // the group's first row in walking order; past the last chunk outside [0, T)
-        const int chunk = step * cs + rank;
-        const int t0 = p.reverse ? (chunks - chunk) * TILE - 1 - group * R : chunk * TILE + group * R;
-        const bool plain = plain_rows<R>(c, t0, dir, seq_b, seq_e);
-        if (chunk < chunks) ok = tc::mbar_wait(sh.full + step % kStages, (step / kStages) & 1, nullptr);
-        const uint8_t* in = stages + step % kStages * STAGE + ((p.reverse ? TILE - 1 - group * R : group * R) * LC + col) * 4;
+    init_barriers(sh);
+    bool ok = true;
+    if (threadIdx.x >= 32 * W) {
+        // stage s: TILE rows of the strip of F, then of X
+        ok = exchange<LC, V, W>(sh, steps, cs, rank, [&](int step) {
+            const int chunk = step * cs + rank, s = step % kStages;
+            if (step >= steps || chunk >= chunks) return;
+            const int row = (p.reverse ? chunks - 1 - chunk : chunk) * TILE;
+            uint8_t* to = stages + s * STAGE;
+            tc::mbar_arrive_expect_tx(sh.full + s, STAGE);
+            for (int i = 0; i < TILE; i += box_rows(TILE)) {
+                tc::tma_load_2d(to + i * LC * 4, &m.f, strip, row + i, sh.full + s);
+                tc::tma_load_2d(to + ARRAY + i * LC * 4, &m.x, strip, row + i, sh.full + s);
+            }
+        });
+    } else {
+        const int col = threadIdx.x % LC, group = threadIdx.x / LC, dir = p.reverse ? -1 : 1, ch = strip + col * V;
+        const bool on = ch < p.D;
+        using T = typename Elem<BF>::type;
+        bool bad = false;
+        int seq_b = 0, seq_e = 0;
+        Cursor at_row;
         const int pitch_in = dir * LC * 4;
+        const long long pitch = dir * p.ld_y;
+        // the group's first row in walking order; past the last chunk outside [0, T)
+        auto first_row = [&](int step) {
+            const int chunk = step * cs + rank;
+            return p.reverse ? (chunks - chunk) * TILE - 1 - group * R : chunk * TILE + group * R;
+        };
+        auto input_of = [&](int step) {
+            return stages + step % kStages * STAGE + ((p.reverse ? TILE - 1 - group * R : group * R) * LC + col) * 4;
+        };
         auto load = [&](const uint8_t* at, Vec<V>& a, Vec<V>& b) {
             const Vec<V> f = Elem<BF>::get(*reinterpret_cast<const uint32_t*>(at));
-            const Vec<V> x = Elem<BF>::get(*reinterpret_cast<const uint32_t*>(at + TILE * LC * 4));
+            const Vec<V> x = Elem<BF>::get(*reinterpret_cast<const uint32_t*>(at + ARRAY));
             Vec<V> rest;
             gates<V>(f, a, rest);
             b = input<FORM, V>(a, rest, x);
         };
-        Vec<V> a[R], b[R], h;
-        Run<V> run{all<V>(1.f), all<V>(0.f)};
-        if (plain) {
-            const uint8_t* at = in;
+        struct Set {
+            Vec<V> a[R], b[R];
+            Run<V> before;
+            bool plain;
+        };
+        auto first_half = [&](Set& q, int step) {
+            const int t0 = first_row(step);
+            q.plain = plain_rows<R>(c, t0, dir, seq_b, seq_e);
+            if (step * cs + rank < chunks) ok = ok && tc::mbar_wait(sh.full + step % kStages, (step / kStages) & 1, &sh.abort);
+            const uint8_t* in = input_of(step);
+            Run<V> run{all<V>(1.f), all<V>(0.f)};
+            if (q.plain) {
 #pragma unroll
-            for (int k = 0; k < R; ++k) {
-                load(at, a[k], b[k]);
-                at += pitch_in;
-                run.b = fma(a[k], run.b, b[k]);
-                run.a = mul(run.a, a[k]);
-            }
-        } else {
+                for (int k = 0; k < R; ++k) {
+                    load(in, q.a[k], q.b[k]);
+                    in += pitch_in;
+                    run.b = fma(q.a[k], run.b, q.b[k]);
+                    run.a = mul(run.a, q.a[k]);
+                }
+            } else {
 #pragma unroll 1
-            for (int k = 0; k < R; ++k) {
-                const Row q = row_of(c, at_row, t0 + dir * k, p.reverse);
-                if (q.s < 0) continue;
-                Vec<V> ak, bk;
-                load(in + k * pitch_in, ak, bk);
-                if (q.start) {
-                    run = Run<V>{all<V>(kReset), fma(ak, state_of<V>(p.H_0, q.s, p.D, ch, on), bk)};
-                } else {
-                    run.b = fma(ak, run.b, bk);
-                    run.a = mul(run.a, ak);   // -0 stays -0
+                for (int k = 0; k < R; ++k) {
+                    const Row r = row_of(c, at_row, t0 + dir * k, p.reverse);
+                    if (r.s < 0) continue;
+                    Vec<V> ak, bk;
+                    load(in + k * pitch_in, ak, bk);
+                    if (r.start) {
+                        run = Run<V>{all<V>(kReset), fma(ak, state_of<V>(p.H_0, r.s, p.D, ch, on), bk)};
+                    } else {
+                        run.b = fma(ak, run.b, bk);
+                        run.a = mul(run.a, ak);   // -0 stays -0
+                    }
                 }
             }
-        }
-        if (!exchange<LC, V>(sh, step, cs, rank, run, state, h, ok, [&]() { issue(step + kStages - 1); })) break;
-        // the states that enter segments of kKeep rows
-        auto keep = [&](int t) {
-            const long long seg = t / kKeep;
-            if (p.chunk_states && on && t >= 0 && seg * kKeep < p.T) {
-                if constexpr (V == 2) *reinterpret_cast<uint64_t*>(p.chunk_states + seg * p.D + ch) = h.x;
-                else p.chunk_states[seg * p.D + ch] = h.x;
+            q.before = hand_over<LC, V, W>(sh, step, run);
+        };
+        auto second_half = [&](Set& q, int step) {
+            const int t0 = first_row(step);
+            Vec<V> h;
+            if (!ok || !take_over<LC, V, W>(sh, step, q.before, h)) {
+                ok = false;
+                return;
+            }
+            // the state that enters the rows
+            if (p.chunk_states && on && t0 >= 0 && t0 / kKeep * kKeep < p.T) {
+                const long long at = (long long)(t0 / kKeep) * p.D + ch;
+                *reinterpret_cast<Vec<V>*>(p.chunk_states + at) = h;
+            }
+            T* y = static_cast<T*>(p.Y) + (long long)t0 * p.ld_y + ch;
+            if (q.plain) {
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    h = fma(q.a[k], h, q.b[k]);
+                    if (on) __stcs(reinterpret_cast<uint32_t*>(y), Elem<BF>::put(h));
+                    y += pitch;
+                }
+                bad |= on && wild<V>(h);   // inside a sequence a state that is not finite stays so
+            } else {
+                const uint8_t* in = input_of(step);
+#pragma unroll 1
+                for (int k = 0; k < R; ++k) {
+                    const Row r = row_of(c, at_row, t0 + dir * k, p.reverse);
+                    if (r.s < 0) continue;
+                    Vec<V> ak, bk;
+                    load(in + k * pitch_in, ak, bk);
+                    if (r.start) h = state_of<V>(p.H_0, r.s, p.D, ch, on);
+                    h = fma(ak, h, bk);
+                    bad |= on && wild<V>(h);
+                    if (on) __stcs(reinterpret_cast<uint32_t*>(y + k * pitch), Elem<BF>::put(h));
+                    if (r.end) put_state<V>(p.H_T, r.s, p.D, ch, on, h);
+                }
             }
         };
-        typename Elem<BF>::type* y = static_cast<typename Elem<BF>::type*>(p.Y) + (long long)t0 * p.ld_y + ch;
-        const long long pitch = dir * p.ld_y;
-        if (plain) {
-#pragma unroll
-            for (int k = 0; k < R; ++k) {
-                if (k % kKeep == 0) keep(t0 + dir * k);
-                h = fma(a[k], h, b[k]);
-                if (on) __stcs(reinterpret_cast<uint32_t*>(y), Elem<BF>::put(h));
-                y += pitch;
-            }
-            bad |= on && wild<V>(h);   // inside a sequence a state that is not finite stays so
-        } else {
-#pragma unroll 1
-            for (int k = 0; k < R; ++k) {
-                if (k % kKeep == 0) keep(t0 + dir * k);
-                const Row q = row_of(c, at_row, t0 + dir * k, p.reverse);
-                if (q.s < 0) continue;
-                Vec<V> ak, bk;
-                load(in + k * pitch_in, ak, bk);
-                if (q.start) h = state_of<V>(p.H_0, q.s, p.D, ch, on);
-                h = fma(ak, h, bk);
-                bad |= on && wild<V>(h);
-                if (on) __stcs(reinterpret_cast<uint32_t*>(y + k * pitch), Elem<BF>::put(h));
-                if (q.end) put_state<V>(p.H_T, q.s, p.D, ch, on, h);
-            }
+        Set q0, q1;
+        if (steps > 0) first_half(q0, 0);
+        for (int step = 0; step < steps && __all_sync(0xffffffffu, ok); step += 2) {
+            if (step + 1 < steps) first_half(q1, step + 1);
+            second_half(q0, step);
+            if (step + 1 >= steps) break;
+            if (step + 2 < steps) first_half(q0, step + 2);
+            second_half(q1, step + 1);
         }
+        if (bad) atomicOr(p.status, kStatusNonFinite);
     }
-    if (bad) atomicOr(p.status, kStatusNonFinite);
     if (!ok) {
+        sh.abort = 1;
         atomicOr(p.status, kStatusTimeout);
         settle();
     }
@@ -169,10 +187,10 @@ __global__ void __launch_bounds__(128) gated_step_kernel(int D, long long units,
 
 template <bool BF, int FORM>
 cudaError_t forward(const GatedScanArgs& a, cudaStream_t s) {
-    const Shape q = shape_of(a, kRowsF);
-    if (q.lanes == 32) return launch<BF, 32, kRowsF>(gated_fwd_kernel<BF, FORM, 32>, a, false, q.cs, s);
-    if (q.lanes == 16) return launch<BF, 16, kRowsF>(gated_fwd_kernel<BF, FORM, 16>, a, false, q.cs, s);
-    return launch<BF, 8, kRowsF>(gated_fwd_kernel<BF, FORM, 8>, a, false, q.cs, s);
+    const Shape q = shape_of(a, false);
+    if (q.lanes == 32) return launch<BF, 32>(gated_fwd_kernel<BF, FORM, 32>, a, false, q.cs, s);
+    if (q.lanes == 16) return launch<BF, 16>(gated_fwd_kernel<BF, FORM, 16>, a, false, q.cs, s);
+    return launch<BF, 8>(gated_fwd_kernel<BF, FORM, 8>, a, false, q.cs, s);
 }
 
 }  // namespace

@@ -2,24 +2,23 @@
 // forward and the backward kernel share.
 //
 // Each pass reads its inputs and writes its outputs once.  A thread-block cluster owns a strip of channels (LC
-// lanes of two bf16 or one fp32 channel) and walks the whole length; in a step each of its CTAs takes 256 / LC
-// groups of R rows, a thread keeping its R rows' (a, s x) in registers.  The effect of a run of rows on the state
-// is h -> A h + B: groups combine theirs in their warp, warps leave theirs in shared memory, CTAs send theirs to
-// every CTA of the cluster (asynchronous stores to distributed shared memory that count on the receiver's
-// barrier), and everyone walks the state over the runs before its own, one after the other, before it runs its
-// rows from registers.  So the state never leaves the cluster, nothing waits on global memory, and the order of
-// every operation is fixed.  The inputs of the next steps are on their way meanwhile (TMA into a ring of stages).
-// The backward pass is the same walk the other way, lambda -> a (lambda + dy), with h recomputed from states that
-// the forward pass keeps every 8 rows.
+// lanes of two bf16 or one fp32 channel) and walks the whole length; in a step each of its CTAs takes 32 / LC groups
+// of 8 rows a warp, a thread keeping its rows' (a, s x) in registers.  The effect of a run of rows on the state is
+// h -> A h + B: groups combine theirs in their warp, warps leave theirs in shared memory, and a warp of its own sends
+// the CTA's to every CTA of the cluster (asynchronous stores to distributed shared memory that count on the
+// receiver's barrier) and walks the state over the runs, one after the other.  Meanwhile the other warps compute the
+// gates of the next step: two steps are in registers.  So the state never leaves the cluster, nothing waits on
+// global memory, and the order of every operation is fixed.  The inputs come by TMA into a ring of stages.  The
+// backward pass is the same walk the other way, lambda -> a (lambda + dy), with h recomputed from states that the
+// forward pass keeps every 8 rows.
 //
 // A sequence's first row in walking order does not take the state before it: such a run has A = -0.  A state that
 // is not finite would still reach through as 0 times it, so where a walk's result is not finite it is done again
 // with the runs' signs looked at.
 //
-// Narrow strips (LC = 16 or 8) serve few channels: the grid is one wave of two CTAs per SM where there are rows
-// enough.  With 1,024 bf16 channels, LC = 32 leaves one CTA per SM and the step's exchange (about 1 us) uncovered.
-// (Tiles that look back at each other's states in global memory in place of the clusters were slower: 2.25 ms for
-// 313,344 rows of 1,024 channels, the hand-over between tiles being the bound.)  Every wait is bounded.
+// Narrow strips (LC = 16 or 8) serve few channels, so that the grid is about one wave.  (Tiles that look back at
+// each other's states in global memory in place of the clusters were slower: 2.25 ms for 313,344 rows of 1,024
+// channels, the hand-over between tiles being the bound.)  Every wait is bounded.
 #pragma once
 
 #include <type_traits>
@@ -31,53 +30,53 @@
 namespace ttt {
 namespace scan {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kKeep = 8;          // rows between two kept states
-constexpr int kRowsF = 16;        // rows of a group, forward
-constexpr int kRowsB = kKeep;     // and backward
+constexpr int kKeep = 8;          // rows between two kept states, and of a group
+constexpr int kRows = kKeep;
 constexpr int kMaxCluster = 8;    // the portable size; of 16 CTAs only 14 clusters at two CTAs per SM fit the card
-constexpr int kStages = 3;
+constexpr int kStages = 4;
 constexpr float kReset = -0.f;
+// Warps that walk rows (one more exchanges) and CTAs of them per SM: two steps' rows of the forward pass take 64
+// registers of a thread, of the backward pass 128.
+constexpr int kWarpsF = 7, kPerSmF = 2, kWarpsB = 11, kPerSmB = 1;
 
 // ------------------------------------------------------------------ V channels' values, in fp32
+// (Two channels in packed fp32 pairs took as many instructions: the moves that build and split the pairs.)
 template <int V>
-struct Vec;
-template <>
-struct Vec<1> {
-    float x;
-    __device__ __forceinline__ float get(int) const { return x; }
-    __device__ __forceinline__ void set(int, float v) { x = v; }
+struct alignas(4 * V) Vec {
+    float x[V];
+    __device__ __forceinline__ float get(int v) const { return x[v]; }
+    __device__ __forceinline__ void set(int v, float c) { x[v] = c; }
 };
-template <>
-struct Vec<2> {
-    uint64_t x;   // a register pair, for the packed arithmetic
-    __device__ __forceinline__ float get(int v) const {
-        float a, b;
-        attn::f2_split(x, a, b);
-        return v ? b : a;
-    }
-    __device__ __forceinline__ void set(int v, float c) {
-        float a, b;
-        attn::f2_split(x, a, b);
-        x = v ? attn::f2(a, c) : attn::f2(c, b);
-    }
-};
-__device__ __forceinline__ Vec<1> fma(Vec<1> a, Vec<1> b, Vec<1> c) { return {fmaf(a.x, b.x, c.x)}; }
-__device__ __forceinline__ Vec<1> mul(Vec<1> a, Vec<1> b) { return {a.x * b.x}; }
-__device__ __forceinline__ Vec<1> add(Vec<1> a, Vec<1> b) { return {a.x + b.x}; }
-__device__ __forceinline__ Vec<1> sub(Vec<1> a, Vec<1> b) { return {a.x - b.x}; }
-__device__ __forceinline__ Vec<2> fma(Vec<2> a, Vec<2> b, Vec<2> c) { return {attn::f2_fma(a.x, b.x, c.x)}; }
-__device__ __forceinline__ Vec<2> add(Vec<2> a, Vec<2> b) { return {attn::f2_add(a.x, b.x)}; }
-__device__ __forceinline__ Vec<2> sub(Vec<2> a, Vec<2> b) { return {attn::f2_sub(a.x, b.x)}; }
-__device__ __forceinline__ Vec<2> mul(Vec<2> a, Vec<2> b) {
-    Vec<2> r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.x) : "l"(a.x), "l"(b.x));
-    return r;
+template <int V>
+__device__ __forceinline__ Vec<V> fma(Vec<V> a, Vec<V> b, Vec<V> c) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) c.x[v] = fmaf(a.x[v], b.x[v], c.x[v]);
+    return c;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> mul(Vec<V> a, Vec<V> b) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) a.x[v] *= b.x[v];
+    return a;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> add(Vec<V> a, Vec<V> b) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) a.x[v] += b.x[v];
+    return a;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> sub(Vec<V> a, Vec<V> b) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) a.x[v] -= b.x[v];
+    return a;
 }
 template <int V>
 __device__ __forceinline__ Vec<V> all(float c) {
-    if constexpr (V == 1) return {c};
-    else return {attn::f2(c, c)};
+    Vec<V> r;
+#pragma unroll
+    for (int v = 0; v < V; ++v) r.x[v] = c;
+    return r;
 }
 // whether some channel is not finite
 template <int V>
@@ -166,12 +165,14 @@ struct Elem {
     static constexpr int V = BF ? 2 : 1;
     using type = std::conditional_t<BF, __nv_bfloat16, float>;
     static __device__ __forceinline__ Vec<V> get(uint32_t w) {
-        if constexpr (BF) return {attn::f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u))};
-        else return {__uint_as_float(w)};
+        Vec<V> r;
+        r.x[0] = __uint_as_float(BF ? w << 16 : w);
+        if constexpr (BF) r.x[1] = __uint_as_float(w & 0xffff0000u);
+        return r;
     }
     static __device__ __forceinline__ uint32_t put(Vec<V> x) {
         if constexpr (BF) return attn::pack_bf16(x.get(0), x.get(1));
-        else return __float_as_uint(x.x);
+        else return __float_as_uint(x.get(0));
     }
 };
 
@@ -240,7 +241,7 @@ __device__ __forceinline__ void empty_sequences(const SeqOffsets& c, int D, cons
 
 // ------------------------------------------------------------------ runs
 template <int V>
-struct Run {
+struct alignas(8 * V) Run {
     Vec<V> a, b;
 };
 // run `p` followed by run `q`
@@ -267,10 +268,12 @@ __device__ __forceinline__ Vec<V> over_exact(Run<V> p, Vec<V> h) {
 }
 template <int V>
 __device__ __forceinline__ Run<V> from_lane(Run<V> p, int lane) {
-    Run<V> r;
-    r.a.x = __shfl_sync(0xffffffffu, p.a.x, lane);
-    r.b.x = __shfl_sync(0xffffffffu, p.b.x, lane);
-    return r;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        p.a.x[v] = __shfl_sync(0xffffffffu, p.a.x[v], lane);
+        p.b.x[v] = __shfl_sync(0xffffffffu, p.b.x[v], lane);
+    }
+    return p;
 }
 
 // Several runs in a row; the exact form only where one of them has a reset.
@@ -290,26 +293,43 @@ __device__ __forceinline__ Run<V> compose(const Run<V> (&q)[N]) {
     return r;
 }
 
-template <int LC, int V>
+template <int LC, int V, int W>
 struct Shared {
-    Run<V> cta[2][kMaxCluster][LC];   // each CTA's run, for two steps in turn
-    Run<V> part[kWarps][LC];          // each warp's
-    Vec<V> enter[kWarps][LC];         // the state that enters each warp's rows
-    uint64_t full[kStages], sent[2];
+    // each for two steps in turn
+    Run<V> cta[2][kMaxCluster][LC];   // each CTA's run
+    Run<V> part[2][W][LC];            // each warp's
+    Vec<V> enter[2][W][LC];           // the state that enters each warp's rows
+    uint64_t full[kStages];           // inputs landed
+    uint64_t ready[2];                // part is written (W warps)
+    uint64_t sent[2];                 // cta is written (bytes)
+    uint64_t entered[2];              // enter is written
+    volatile int abort;
 };
 
-// From the groups' runs to the state h that enters each group's rows.  Warp 0 does the work between two barriers
-// (done by every warp for itself it was 40% of all instructions): `state`, the one that enters the cluster's
-// step, is its alone.  `consumed` runs once every warp is through with the step before.  `ok`: whether every wait
-// so far ended in time; returns false, for the whole CTA alike, if one of any thread's before this call did not.
-template <int LC, int V, class Consumed>
-__device__ __forceinline__ bool exchange(Shared<LC, V>& sh, int step, int cs, int rank, Run<V> mine, Vec<V>& state, Vec<V>& h,
-                                         bool& ok, Consumed consumed) {
+template <int LC, int V, int W>
+__device__ __forceinline__ void init_barriers(Shared<LC, V, W>& sh) {
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) tc::mbar_init(sh.full + s, 1);
+        for (int s = 0; s < 2; ++s) {
+            tc::mbar_init(sh.ready + s, W);
+            tc::mbar_init(sh.sent + s, 1);
+            tc::mbar_init(sh.entered + s, 1);
+        }
+        sh.abort = 0;
+        tc::fence_mbar_init();
+    }
+    tc::cluster_sync();   // every CTA runs and has its barriers: its shared memory may be written
+}
+
+// A step's first half, by a walking warp: its groups' runs to the exchange.  Returns, for G > 1, the runs of the
+// warp's groups in front of this one.
+template <int LC, int V, int W>
+__device__ __forceinline__ Run<V> hand_over(Shared<LC, V, W>& sh, int step, Run<V> mine) {
     constexpr int G = 32 / LC;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = lane % LC, group = lane / LC;
-    Run<V> before = mine;   // G > 1: the runs of the warp's groups in front of this one
+    Run<V> before = mine;
     if constexpr (G == 1) {
-        sh.part[warp][col] = mine;
+        sh.part[step & 1][warp][col] = mine;
     } else {
         const Run<V> none{all<V>(1.f), all<V>(0.f)};
         Run<V> groups[G], front[G];
@@ -320,35 +340,64 @@ __device__ __forceinline__ bool exchange(Shared<LC, V>& sh, int step, int cs, in
         for (int g = 0; g < G - 1; ++g) front[g + 1] = g < group ? groups[g] : none;
         before = compose<V, G>(front);
         const Run<V> total = compose<V, G>(groups);
-        if (lane < LC) sh.part[warp][col] = total;
+        if (lane < LC) sh.part[step & 1][warp][col] = total;
     }
-    if (!__syncthreads_and(ok)) return false;
-    if (warp == 0) {
-        uint64_t* bar = sh.sent + (step & 1);
-        Run<V> q[kWarps];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(sh.ready + (step & 1));
+    return before;
+}
+// Its second half: the state that enters this thread's rows.
+template <int LC, int V, int W>
+__device__ __forceinline__ bool take_over(Shared<LC, V, W>& sh, int step, Run<V> before, Vec<V>& h) {
+    if (!tc::mbar_wait(sh.entered + (step & 1), (step >> 1) & 1, &sh.abort)) return false;
+    const Vec<V> e = sh.enter[step & 1][threadIdx.x >> 5][threadIdx.x % LC];
+    h = e;
+    if constexpr (LC < 32) {
+        h = over<V>(before, e);
+        if (wild<V>(h)) h = over_exact<V>(before, e);
+    }
+    return true;
+}
+
+// The exchanging warp: issues the inputs' copies (issue(step)), sends the CTA's run of each step to the cluster and
+// walks the state over the runs of the CTAs and of the warps.  (Every warp doing this for itself took 40% of all
+// instructions; one of the walking warps doing it between two barriers left the others waiting 60% of the time.)
+template <int LC, int V, int W, class Issue>
+__device__ __forceinline__ bool exchange(Shared<LC, V, W>& sh, int steps, int cs, int rank, Issue issue) {
+    constexpr int G = 32 / LC;
+    const int lane = threadIdx.x & 31, col = lane % LC, group = lane / LC;
+    Vec<V> state = all<V>(0.f);
+    if (lane == 0)
+        for (int s = 0; s < 2; ++s) issue(s);
+    for (int step = 0; step < steps; ++step) {
+        const int p = step & 1, phase = (step >> 1) & 1;
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(sh.ready + p, phase, &sh.abort))) return false;
+        Run<V> q[W];
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) q[i] = sh.part[i][col];
-        const Run<V> total = compose<V, kWarps>(q);
-        if (lane == 0) tc::mbar_arrive_expect_tx(bar, cs * LC * V * 8);
+        for (int i = 0; i < W; ++i) q[i] = sh.part[p][i][col];
+        const Run<V> total = compose<V, W>(q);
+        if (lane == 0) tc::mbar_arrive_expect_tx(sh.sent + p, cs * LC * V * 8);
         __syncwarp();
-        const uint32_t to0 = tc::smem_u32(&sh.cta[step & 1][rank][col]), on0 = tc::smem_u32(bar);
+        const uint32_t to0 = tc::smem_u32(&sh.cta[p][rank][col]), on0 = tc::smem_u32(sh.sent + p);
 #pragma unroll
         for (int j = 0; j < kMaxCluster; j += G) {
             const int i = j + group;
             if (i < cs) {
                 const uint32_t to = tc::mapa_shared(to0, i), on = tc::mapa_shared(on0, i);
                 if constexpr (V == 2)
-                    tc::st_async_v4(to, (uint32_t)total.a.x, (uint32_t)(total.a.x >> 32), (uint32_t)total.b.x,
-                                    (uint32_t)(total.b.x >> 32), on);
+                    tc::st_async_v4(to, __float_as_uint(total.a.x[0]), __float_as_uint(total.a.x[1]),
+                                    __float_as_uint(total.b.x[0]), __float_as_uint(total.b.x[1]), on);
                 else
                     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(to),
-                                 "r"(__float_as_uint(total.a.x)), "r"(__float_as_uint(total.b.x)), "r"(on) : "memory");
+                                 "r"(__float_as_uint(total.a.x[0])), "r"(__float_as_uint(total.b.x[0])), "r"(on) : "memory");
             }
         }
+        // every warp has handed this step over, so is through with the one before the last: its stage is free
+        if (lane == 0) issue(step + 2);
         // A slot is written again two steps on: its sender has then seen every CTA's next step, which each sends
-        // after it has read this one.
-        ok = tc::mbar_wait_cluster(bar, (step >> 1) & 1);
-        const Run<V>(*slot)[LC] = sh.cta[step & 1];
+        // after it has walked over this one.
+        if (!__all_sync(0xffffffffu, tc::mbar_wait_cluster_abort(sh.sent + p, phase, &sh.abort))) return false;
+        const Run<V>(*slot)[LC] = sh.cta[p];
         const Vec<V> s0 = state;
         auto walk = [&](auto step_over) {
             Vec<V> s = s0, e = s0;
@@ -360,25 +409,18 @@ __device__ __forceinline__ bool exchange(Shared<LC, V>& sh, int step, int cs, in
                 }
             }
             state = s;
-            if (lane < LC) sh.enter[0][col] = e;
+            if (lane < LC) sh.enter[p][0][col] = e;
 #pragma unroll
-            for (int i = 0; i < kWarps - 1; ++i) {
+            for (int i = 0; i < W - 1; ++i) {
                 e = step_over(q[i], e);
-                if (lane < LC) sh.enter[i + 1][col] = e;
+                if (lane < LC) sh.enter[p][i + 1][col] = e;
             }
             return wild<V>(s) || wild<V>(e);
         };
-        if (__any_sync(0xffffffffu, walk([](Run<V> p, Vec<V> s) { return over<V>(p, s); })))
-            walk([](Run<V> p, Vec<V> s) { return over_exact<V>(p, s); });
-    } else if (threadIdx.x == 32) {
-        consumed();
-    }
-    __syncthreads();
-    h = sh.enter[warp][col];
-    if constexpr (G > 1) {
-        const Vec<V> e = h;
-        h = over<V>(before, e);
-        if (wild<V>(h)) h = over_exact<V>(before, e);
+        if (__any_sync(0xffffffffu, walk([](Run<V> r, Vec<V> s) { return over<V>(r, s); })))
+            walk([](Run<V> r, Vec<V> s) { return over_exact<V>(r, s); });
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(sh.entered + p);
     }
     return true;
 }
@@ -392,6 +434,9 @@ __device__ __forceinline__ int cluster_size() {
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
     return n;
 }
+
+// A tile of more rows than a box may have (256) comes in two.
+__host__ __device__ constexpr int box_rows(int tile) { return tile <= 256 ? tile : tile / 2; }
 
 // Copies in flight land before a block that gave up leaves its memory.
 __device__ __forceinline__ void settle() {
@@ -412,12 +457,11 @@ inline bool map_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, lon
               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// One launch: kernel(args, maps) on strips x cluster CTAs.  R: rows of a group; arrays: inputs per stage.
-template <bool BF, int LC, int R, class Kernel>
+// One launch: kernel(args, maps) on strips x cluster CTAs.
+template <bool BF, int LC, class Kernel>
 cudaError_t launch(Kernel kernel, const GatedScanArgs& a, bool backward, int cs, cudaStream_t s) {
-    constexpr int W = LC * Elem<BF>::V, TILE = kThreads / LC * R, ARRAYS_F = 2, ARRAYS_B = 3;
-    static_assert(TILE <= 256 || LC < 32, "a box has at most 256 rows");
-    constexpr int BOX = TILE < 256 ? TILE : 256, HBOX = TILE / kKeep < 256 ? TILE / kKeep : 256;
+    constexpr int W = LC * Elem<BF>::V, ARRAYS_F = 2, ARRAYS_B = 3;
+    const int warps = backward ? kWarpsB : kWarpsF, TILE = 32 / LC * warps * kRows, BOX = box_rows(TILE), HBOX = TILE / kKeep;
     Maps m{};
     const CUtensorMapDataType dt = BF ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
     const long long keeps = ((long long)a.T + kKeep - 1) / kKeep;
@@ -425,12 +469,12 @@ cudaError_t launch(Kernel kernel, const GatedScanArgs& a, bool backward, int cs,
                     (backward && (!map_2d(&m.dy, dt, a.dY, a.T, a.D, a.ld_dy, W, BOX) ||
                                   !map_2d(&m.h, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.chunk_states, keeps, a.D, a.D, W, HBOX)))))
         return cudaErrorInvalidValue;
-    const int smem = kStages * ((backward ? ARRAYS_B : ARRAYS_F) * TILE * LC * 4 + (backward ? TILE / kKeep * W * 4 : 0));
+    const int smem = kStages * (((backward ? ARRAYS_B : ARRAYS_F) * TILE * LC * 4 + (backward ? HBOX * W * 4 : 0) + 127) / 128 * 128);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((a.D + W - 1) / W * cs));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(32 * (warps + 1));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at{};
@@ -443,22 +487,19 @@ cudaError_t launch(Kernel kernel, const GatedScanArgs& a, bool backward, int cs,
 }
 
 // The strip's width and the cluster's size: the widest strips (whole 128-byte lines) whose clusters of up to eight
-// CTAs fill more than half of the card's two CTAs per SM, and no more CTAs than there are tiles of rows.
+// CTAs fill more than half of the card, and no more CTAs than there are tiles of rows.
 struct Shape {
     int lanes, cs;
 };
-inline Shape shape_of(const GatedScanArgs& a, int R) {
+inline Shape shape_of(const GatedScanArgs& a, bool backward) {
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int V = a.bf16 ? 2 : 1;
+    const int V = a.bf16 ? 2 : 1, room = sms * (backward ? kPerSmB : kPerSmF), rows = (backward ? kWarpsB : kWarpsF) * kRows;
     auto strips = [&](int lanes) { return (a.D + lanes * V - 1) / (lanes * V); };
     Shape q{32, 1};
-    while (q.lanes > 8 && 2LL * kMaxCluster * strips(q.lanes / 2) <= 4LL * sms && strips(q.lanes / 2) > strips(q.lanes)) {
-        if ((long long)kMaxCluster * strips(q.lanes / 2) > 2 * sms) break;
-        q.lanes /= 2;
-    }
-    while (q.cs < kMaxCluster && 2LL * q.cs * strips(q.lanes) <= 2 * sms && (long long)q.cs * (kThreads / q.lanes * R) < a.T) q.cs *= 2;
+    while (q.lanes > 8 && strips(q.lanes / 2) > strips(q.lanes) && kMaxCluster * strips(q.lanes / 2) <= room) q.lanes /= 2;
+    while (q.cs < kMaxCluster && 2LL * q.cs * strips(q.lanes) <= room && (long long)q.cs * (32 / q.lanes) * rows < a.T) q.cs *= 2;
     return q;
 }
 
