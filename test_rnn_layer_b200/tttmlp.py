@@ -8,6 +8,7 @@ library is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -178,17 +179,15 @@ def lib():
 def _p(x):
     if x is None:
         return None
-    if isinstance(x, torch.Tensor):
-        return ctypes.c_void_p(x.data_ptr())
-    return ctypes.c_void_p(int(x))
+    return x.data_ptr() if isinstance(x, torch.Tensor) else int(x)
 
 
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())   # current_stream() builds an object
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 # ------------------------------------------------------------------ the C entry points
@@ -535,25 +534,27 @@ class _Place:
     """Runs a call with the tensors' device current and, if one is given, on `stream`
     (new tensors then belong to that stream)."""
 
+    __slots__ = ("stack",)
+
     def __init__(self, tensor, stream):
-        self.index, self.stream = tensor.device.index, stream
-        self.stack = []
+        self.stack = None
+        if stream is None and tensor.get_device() == torch.cuda.current_device():
+            return
+        self.stack = [torch.cuda.device(tensor.device)]
+        if isinstance(stream, torch.cuda.Stream):
+            self.stack.append(torch.cuda.stream(stream))
 
     def __enter__(self):
-        if self.index != torch.cuda.current_device():
-            self.stack.append(torch.cuda.device(self.index))
-        if isinstance(self.stream, torch.cuda.Stream):
-            self.stack.append(torch.cuda.stream(self.stream))
-        for c in self.stack:
+        for c in self.stack or ():
             c.__enter__()
-        return self.stream
 
     def __exit__(self, *exc):
-        for c in reversed(self.stack):
+        for c in reversed(self.stack or ()):
             c.__exit__(*exc)
         return False
 
 
+# The checks run on every call of a few microseconds: messages are put together only for a refusal.
 def _ask(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
@@ -561,28 +562,33 @@ def _ask(ok: bool, what: str) -> None:
 
 def _rows(x, shape, dtype, device, name) -> int:
     """Row stride of a tensor of `shape` whose rows are dense (checked with its type and device)."""
-    _ask(x.dtype == dtype and x.device == device, f"{name}: {x.dtype} on {x.device}, wanted {dtype} on {device}")
-    _ask(tuple(x.shape) == tuple(shape), f"{name}: shape {tuple(x.shape)}, wanted {tuple(shape)}")
-    width, strides = 1, x.stride()
+    if x.dtype is not dtype or x.device != device:
+        raise ValueError(f"{name}: {x.dtype} on {x.device}, wanted {dtype} on {device}")
+    if x.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(x.shape)}, wanted {tuple(shape)}")
+    strides = x.stride()
+    width = 1
     for k in range(len(shape) - 1, 0, -1):
-        _ask(shape[k] <= 1 or strides[k] == width, f"{name}: the columns of a row must be dense, strides {strides}")
+        if strides[k] != width and shape[k] > 1:
+            raise ValueError(f"{name}: the columns of a row must be dense, strides {strides}")
         width *= shape[k]
     ld = strides[0] if shape[0] > 1 else -(-width // 8) * 8
-    _ask(ld < 2 ** 31, f"{name}: row stride {ld}")
+    if ld >= 2 ** 31:
+        raise ValueError(f"{name}: row stride {ld}")
     return ld
 
 
 def _offsets(cu, device, name):
     if cu is None:
         return 1
-    _ask(cu.dtype == torch.int32 and cu.device == device and cu.dim() == 1 and cu.numel() >= 2 and cu.is_contiguous(),
-         f"{name}: a dense int32 vector of n_seq + 1 offsets on {device} is wanted")
+    if not (cu.dtype is torch.int32 and cu.device == device and cu.dim() == 1 and cu.numel() >= 2 and cu.is_contiguous()):
+        raise ValueError(f"{name}: a dense int32 vector of n_seq + 1 offsets on {device} is wanted")
     return cu.numel() - 1
 
 
 def _dense(x, shape, dtype, device, name):
-    _ask(x.dtype == dtype and x.device == device and tuple(x.shape) == tuple(shape) and x.is_contiguous(),
-         f"{name}: a dense {dtype} tensor of shape {tuple(shape)} on {device} is wanted")
+    if not (x.dtype is dtype and x.device == device and x.shape == shape and x.is_contiguous()):
+        raise ValueError(f"{name}: a dense {dtype} tensor of shape {tuple(shape)} on {device} is wanted")
     return x
 
 
@@ -591,41 +597,50 @@ def _space(workspace, n, device):
         raise TTTError(TTT_ERR_INVALID_ARG, "workspace size")
     if workspace is None:
         return torch.empty(n, dtype=torch.uint8, device=device)
-    _ask(workspace.device == device, f"workspace on {workspace.device}, wanted {device}")
+    if workspace.device != device:
+        raise ValueError(f"workspace on {workspace.device}, wanted {device}")
     return workspace
 
 
 def _dtype_code(x, name) -> int:
-    _ask(x.is_cuda and x.dtype in (torch.float32, torch.bfloat16), f"{name}: float32 or bfloat16 on a GPU is wanted")
+    if not (x.is_cuda and (x.dtype is torch.bfloat16 or x.dtype is torch.float32)):
+        raise ValueError(f"{name}: float32 or bfloat16 on a GPU is wanted")
     return TTT_BF16 if x.dtype == torch.bfloat16 else TTT_F32
+
+
+_ROPE_KEYS = {"kind", "factor", "length", "low", "high", "amplitude"}
+# descriptors by their sizes: building one costs as much as a launch
+_rope_desc, _window_sizes, _decode_sizes, _gated_sizes = (
+    functools.lru_cache(maxsize=256)(lambda *args, _type=c: _type(*args))
+    for c in (ttt_rope_desc, ttt_window_desc, ttt_window_decode_desc, ttt_gated_scan_desc))
 
 
 def rope(x, positions=None, *, pos0: int = 0, rot: int | None = None, layout: str = "half", base: float = 10000.0,
          scaling: dict | None = None, inverse: bool = False, out=None, stream=None):
     """Rotary positions of x [T, H, d] (ttt_rope).  `scaling`: {"kind": "linear" | "base", "factor": f} or
     {"kind": "ramp", "factor": f, "length": n, "low": l, "high": h}, with "amplitude" optional.  `out` may be x."""
-    code = _dtype_code(x, "x")
-    T, H, d = x.shape
+    code, shape, dev = _dtype_code(x, "x"), x.shape, x.device
+    T, H, d = shape
     sc = scaling or {}
-    known = {"kind", "factor", "length", "low", "high", "amplitude"}
-    _ask(set(sc) <= known and sc.get("kind", "none") in TTT_ROPE_SCALINGS, f"scaling {scaling}")
-    desc = ttt_rope_desc(T, H, d, d if rot is None else rot, TTT_ROPE_LAYOUTS[layout], code,
-                         TTT_ROPE_SCALINGS[sc.get("kind", "none")], base, sc.get("factor", 1.0), sc.get("length", 0.0),
-                         sc.get("low", 0.0), sc.get("high", 0.0), sc.get("amplitude", 1.0))
+    if not (_ROPE_KEYS >= sc.keys() and sc.get("kind", "none") in TTT_ROPE_SCALINGS):
+        raise ValueError(f"scaling {scaling}")
+    desc = _rope_desc(T, H, d, d if rot is None else rot, TTT_ROPE_LAYOUTS[layout], code,
+                      TTT_ROPE_SCALINGS[sc.get("kind", "none")], base, sc.get("factor", 1.0), sc.get("length", 0.0),
+                      sc.get("low", 0.0), sc.get("high", 0.0), sc.get("amplitude", 1.0))
     if positions is not None:
-        _dense(positions, (T,), torch.int32, x.device, "positions")
+        _dense(positions, (T,), torch.int32, dev, "positions")
     with _Place(x, stream):
         if out is None:
-            out = torch.empty((T, H, d), dtype=x.dtype, device=x.device)
-        check(ttt_rope(desc, x, _rows(x, x.shape, x.dtype, x.device, "x"), out,
-                       _rows(out, x.shape, x.dtype, x.device, "out"), positions, pos0, inverse, stream), "ttt_rope")
+            out = torch.empty(shape, dtype=x.dtype, device=dev)
+        check(ttt_rope(desc, x, _rows(x, shape, x.dtype, dev, "x"), out, _rows(out, shape, x.dtype, dev, "out"),
+                       positions, pos0, inverse, stream), "ttt_rope")
     return out
 
 
 def _window_desc(q, k, n_seq, left, right, sinks, scale):
     _ask(q.is_cuda and q.dim() == 3 and k.dim() == 3, "q and k: [T, H, 64] on a GPU")
-    return ttt_window_desc(q.shape[0], k.shape[0], n_seq, q.shape[1], k.shape[1], q.shape[2], left, right, sinks,
-                           q.shape[2] ** -0.5 if scale is None else scale)
+    (Tq, Hq, d), (Tk, Hk, _) = q.shape, k.shape
+    return _window_sizes(Tq, Tk, n_seq, Hq, Hk, d, left, right, sinks, d ** -0.5 if scale is None else scale)
 
 
 def window_attention_workspace(q, k, n_seq: int = 1, backward: bool = False) -> torch.Tensor:
@@ -694,8 +709,9 @@ def _decode_desc(q, cache, left, sinks, scale):
          cache.shape[3] == q.shape[2], "q [B, Hq, 64] and a cache [B, slots, Hk, 64] on a GPU")
     _ask(cache.stride(3) == 1, "the cache's last axis must be dense")
     B, slots, Hk, d = cache.shape
-    return ttt_window_decode_desc(B, q.shape[1], Hk, d, slots, left, sinks, d ** -0.5 if scale is None else scale,
-                                  cache.stride(0), cache.stride(1) if slots > 1 else d, cache.stride(2))
+    s0, s1, s2, _ = cache.stride()
+    return _decode_sizes(B, q.shape[1], Hk, d, slots, left, sinks, d ** -0.5 if scale is None else scale,
+                         s0, s1 if slots > 1 else d, s2)
 
 
 def window_attention_decode_workspace(q, cache) -> torch.Tensor:
@@ -711,9 +727,9 @@ def window_attention_decode(q, cache_k, cache_v, lens, *, left: int, sinks: int 
     A given workspace must have been zeroed once (window_attention_decode_workspace)."""
     dev, bf = q.device, torch.bfloat16
     desc = _decode_desc(q, cache_k, left, sinks, scale)
-    _ask(cache_k.dtype == bf and cache_v.dtype == bf and cache_k.device == dev and cache_v.device == dev and
-         cache_k.shape == cache_v.shape and cache_k.stride() == cache_v.stride(),
-         f"the caches: bfloat16 on {dev}, of the same shape and strides")
+    if not (cache_k.dtype is bf and cache_v.dtype is bf and cache_k.device == dev and cache_v.device == dev and
+            cache_k.shape == cache_v.shape and cache_k.stride() == cache_v.stride()):
+        raise ValueError(f"the caches: bfloat16 on {dev}, of the same shape and strides")
     _dense(lens, (q.shape[0],), torch.int32, dev, "lens")
     ld_q = _rows(q, q.shape, bf, dev, "q")
     ld_new = 0
@@ -737,7 +753,8 @@ def window_attention_decode(q, cache_k, cache_v, lens, *, left: int, sinks: int 
 
 def _gated_desc(x, n_seq, form, dirs):
     _ask(x.dim() == 2, "x: [T, D]")
-    return ttt_gated_scan_desc(x.shape[0], x.shape[1], n_seq, TTT_GATE_FORMS[form], DIRS[dirs], _dtype_code(x, "x"))
+    T, D = x.shape
+    return _gated_sizes(T, D, n_seq, TTT_GATE_FORMS[form], DIRS[dirs], _dtype_code(x, "x"))
 
 
 def gated_scan_workspace(x, n_seq: int = 1) -> torch.Tensor:
