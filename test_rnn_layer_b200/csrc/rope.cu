@@ -5,28 +5,163 @@
 // part, so that a far position (2^20 and more radians) keeps its angle to
 // 2^-31 turns; the rest is sinpi/cospi in fp32.  One angle serves every head
 // of a row, so a block first fills a table of cos and sin for its rows in
-// shared memory and then streams the heads past it.
+// shared memory and then streams the heads past it, 16 bytes at a time and
+// four loads a thread under way while the table is made.  Bound by memory:
+// each element is read and written once.
+//
+// A unit is what one thread turns at once: two 16-byte pieces, the pairs'
+// halves (HALF layout) or two neighbouring pieces of whole pairs.  Layouts
+// whose pieces do not fall on 16 bytes (rot / 2 or rot no multiple of the
+// piece) go pair by pair.
 #include "common.cuh"
 
 namespace ttt {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kMaxRows = 8, kBatch = 4;
 
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs p) {
-    const int pairs = p.rot / 2, units = p.H * p.d / 2;
+__device__ __forceinline__ void fill_table(const RopeArgs& p, int t0, int rows, float2* cs) {
+    const int pairs = p.rot / 2;
+    for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
+        const int r = i / pairs, j = i - r * pairs;
+        const long long pos = p.positions ? p.positions[t0 + r] : p.pos0 + t0 + r;
+        const double u = (double)pos * p.turns[j];
+        float sn, c;
+        sincospif(2.f * (float)(u - rint(u)), &sn, &c);
+        cs[i] = make_float2(p.amplitude * c, p.amplitude * (p.inverse ? -sn : sn));
+    }
+}
+
+// Piece: 16 bytes as fp32 values
+template <bool BF>
+struct Piece {
+    static constexpr int N = BF ? 8 : 4;
+    static __device__ __forceinline__ void unpack(const uint4& w, float (&v)[N]) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (BF) {
+                v[2 * i] = __uint_as_float(u[i] << 16);
+                v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            } else {
+                v[i] = __uint_as_float(u[i]);
+            }
+        }
+    }
+    static __device__ __forceinline__ uint4 pack(const float (&v)[N]) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (BF) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                u[i] = *reinterpret_cast<const uint32_t*>(&b);
+            } else {
+                u[i] = __float_as_uint(v[i]);
+            }
+        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
+    }
+};
+
+// rows [t0, t0 + rows) of a block; `turned` units a head, then `copied` pieces behind the turned columns
+template <bool BF, bool HALF>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs p, int block_rows, int turned, int copied) {
+    constexpr int N = Piece<BF>::N, E = BF ? 2 : 4;
+    extern __shared__ float2 cs[];
+    const int t0 = blockIdx.x * block_rows, rows = min(block_rows, p.T - t0), pairs = p.rot / 2;
+    const int per_head = turned + copied, per_row = p.H * per_head, units = rows * per_row;
+    const char* X = static_cast<const char*>(p.X) + (long long)t0 * p.ld_x * E;
+    char* Y = static_cast<char*>(p.Y) + (long long)t0 * p.ld_y * E;
+    // a unit's row, its first column in the row, the second piece's distance and its first pair (-1: to copy)
+    struct Unit {
+        int r, col, second, pair;
+    };
+    auto unit_of = [&](int u) {
+        Unit q;
+        q.r = u / per_row;
+        const int in_row = u - q.r * per_row, h = in_row / per_head, k = in_row - h * per_head;
+        if (k < turned) {
+            q.col = h * p.d + (HALF ? k * N : 2 * k * N);
+            q.second = HALF ? pairs : N;
+            q.pair = k * N;
+            if (!HALF && 2 * k * N + N >= p.rot) q.second = 0;   // the last piece of an odd number
+        } else {
+            q.col = h * p.d + p.rot + (k - turned) * N;
+            q.second = 0;
+            q.pair = -1;
+        }
+        return q;
+    };
+    bool made = false;
+    for (int u0 = threadIdx.x; u0 - threadIdx.x < units; u0 += kBatch * kThreads) {
+        uint4 a[kBatch], b[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int u = u0 + i * kThreads;
+            if (u < units) {
+                const Unit q = unit_of(u);
+                const char* x = X + (q.r * p.ld_x + q.col) * E;
+                a[i] = __ldcs(reinterpret_cast<const uint4*>(x));
+                if (q.second) b[i] = __ldcs(reinterpret_cast<const uint4*>(x + q.second * E));
+            }
+        }
+        if (!made) {
+            fill_table(p, t0, rows, cs);
+            __syncthreads();
+            made = true;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int u = u0 + i * kThreads;
+            if (u >= units) continue;
+            const Unit q = unit_of(u);
+            char* y = Y + (q.r * p.ld_y + q.col) * E;
+            if (q.pair >= 0) {
+                const float2* w = cs + q.r * pairs + q.pair;
+                float v0[N], v1[N];
+                Piece<BF>::unpack(a[i], v0);
+                if (q.second) Piece<BF>::unpack(b[i], v1);
+                if constexpr (HALF) {
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        const float x0 = v0[e], x1 = v1[e];
+                        v0[e] = x0 * w[e].x - x1 * w[e].y;
+                        v1[e] = x0 * w[e].y + x1 * w[e].x;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < N; e += 2) {
+                        const float x0 = v0[e], x1 = v0[e + 1];
+                        const float2 c = w[e / 2];
+                        v0[e] = x0 * c.x - x1 * c.y;
+                        v0[e + 1] = x0 * c.y + x1 * c.x;
+                    }
+                    if (q.second) {
+#pragma unroll
+                        for (int e = 0; e < N; e += 2) {
+                            const float x0 = v1[e], x1 = v1[e + 1];
+                            const float2 c = w[(N + e) / 2];
+                            v1[e] = x0 * c.x - x1 * c.y;
+                            v1[e + 1] = x0 * c.y + x1 * c.x;
+                        }
+                    }
+                }
+                a[i] = Piece<BF>::pack(v0);
+                if (q.second) b[i] = Piece<BF>::pack(v1);
+            }
+            __stcs(reinterpret_cast<uint4*>(y), a[i]);
+            if (q.second) __stcs(reinterpret_cast<uint4*>(y + q.second * E), b[i]);
+        }
+    }
+}
+
+// Pair by pair, for layouts whose pieces do not fall on 16 bytes.
+__global__ void __launch_bounds__(kThreads) rope_pairs_kernel(const __grid_constant__ RopeArgs p) {
+    const int pairs = p.rot / 2, units = p.H * p.d / 2, rest = (p.d - p.rot) / 2;
     __shared__ float2 cs[kRopeMaxPairs];
     for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
-        const long long pos = p.positions ? p.positions[t] : p.pos0 + t;
-        for (int i = threadIdx.x; i < pairs; i += kThreads) {
-            const double u = (double)pos * p.turns[i];
-            const float r = (float)(u - rint(u));
-            float sn, c;
-            sincospif(2.f * r, &sn, &c);
-            cs[i] = make_float2(p.amplitude * c, p.amplitude * (p.inverse ? -sn : sn));
-        }
+        fill_table(p, t, 1, cs);
         __syncthreads();
-        const int rest = (p.d - p.rot) / 2;
         for (int k = threadIdx.x; k < units; k += kThreads) {
             const int h = k / (p.d / 2), i = k - h * (p.d / 2);
             int j0, j1;
@@ -50,8 +185,31 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     LaunchScope scope("rope", s);
-    rope_kernel<<<min(a.T, 148 * 8), kThreads, 0, s>>>(a);
+    const int n = a.bf16 ? 8 : 4;
+    // strides are multiples of 8 elements and d of 8, so only the split columns can fall off 16 bytes
+    const bool pieces = a.half ? a.rot / 2 % n == 0 : a.rot % n == 0;
+    if (!pieces) {
+        rope_pairs_kernel<<<min(a.T, sms * 8), kThreads, 0, s>>>(a);
+        return cudaGetLastError();
+    }
+    const int turned = a.half ? a.rot / 2 / n : (a.rot / n + 1) / 2;
+    const int copied = a.X == a.Y ? 0 : (a.d - a.rot) / n;
+    // rows of a block: enough for four loads a thread, fewer where blocks would be short of the SMs
+    int rows = 1;
+    while (rows < kMaxRows && (long long)rows * a.H * (turned + copied) < kBatch * kThreads && a.T / (2 * rows) >= 2 * sms) rows *= 2;
+    const unsigned grid = (unsigned)((a.T + rows - 1) / rows);
+    const size_t smem = (size_t)rows * (a.rot / 2) * sizeof(float2);
+    if (a.bf16) {
+        if (a.half) rope_kernel<true, true><<<grid, kThreads, smem, s>>>(a, rows, turned, copied);
+        else rope_kernel<true, false><<<grid, kThreads, smem, s>>>(a, rows, turned, copied);
+    } else {
+        if (a.half) rope_kernel<false, true><<<grid, kThreads, smem, s>>>(a, rows, turned, copied);
+        else rope_kernel<false, false><<<grid, kThreads, smem, s>>>(a, rows, turned, copied);
+    }
     return cudaGetLastError();
 }
 
