@@ -82,7 +82,7 @@ struct Item {
 
 __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_constant__ QArgs p) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sm = smem_raw + (-tc::smem_u32(smem_raw) & 1023u);   // (an offset: the pointer stays known as shared)
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_SLOT);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -289,10 +289,12 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
                     tc::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(bars + B_SR + X);
-                    grad_scores(sc, dp, c, whole, vis, bad, [&](int, uint64_t& l, uint64_t& d) {
-                        l = nl2;
-                        d = nd2;
-                    });
+                    auto neg = [&](int, uint64_t& l0, uint64_t& l1, uint64_t& d0, uint64_t& d1) {
+                        l0 = l1 = nl2;
+                        d0 = d1 = nd2;
+                    };
+                    if (whole) grad_scores<true, false>(sc, dp, c, vis, bad, neg);
+                    else grad_scores<false, false>(sc, dp, c, vis, bad, neg);
                     if (gs > 0) {
                         if (!wait_all(bars + B_PV + X, (gs - 1) & 1)) { ok = false; break; }
                         tc::tc_fence_after();

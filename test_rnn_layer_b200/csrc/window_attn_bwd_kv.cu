@@ -121,7 +121,7 @@ struct Item {
 
 __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_constant__ KvArgs p) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sm = smem_raw + (-tc::smem_u32(smem_raw) & 1023u);   // (an offset: the pointer stays known as shared)
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + B_SLOT);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -336,11 +336,16 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bars + B_SR + X);
-                const uint64_t* nl = reinterpret_cast<const uint64_t*>(sm + OFF_STAT + s * 1024) + HALF / 2 * X;
-                grad_scores(sc, dp, c, whole, vis, bad, [&](int k2, uint64_t& a, uint64_t& b) {
-                    a = nl[k2];
-                    b = nl[BT / 2 + k2];
-                });
+                const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(sm + OFF_STAT + s * 1024) + HALF / 4 * X;
+                auto neg = [&](int k4, uint64_t& l0, uint64_t& l1, uint64_t& d0, uint64_t& d1) {
+                    const ulonglong2 l = nl[k4], d = nl[BT / 4 + k4];
+                    l0 = l.x;
+                    l1 = l.y;
+                    d0 = d.x;
+                    d1 = d.y;
+                };
+                if (whole) grad_scores<true, true>(sc, dp, c, vis, bad, neg);
+                else grad_scores<false, true>(sc, dp, c, vis, bad, neg);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bars + B_QE + s);   // the statistics have been read
                 if (g > 0) {

@@ -46,12 +46,13 @@ __device__ __forceinline__ void screen_tile(uint8_t* tile, int lane, uint32_t (&
     }
 }
 
-// P = exp2(c S - lse2) and dS = P (dP - delta) of one row's 64 scores, as bf16 pairs in the front of s and dp.
-// neg(k2) gives (-lse2, -delta) of columns 2 k2 and 2 k2 + 1 as packed pairs.  `vis`: the columns seen (unless
-// whole); `bad`: columns whose other operand was not finite and was zeroed: seen, they make the row NaN.
-template <class Neg>
-__device__ __forceinline__ void grad_scores(uint32_t (&s)[HALF], uint32_t (&dp)[HALF], float c, bool whole,
-                                            const uint32_t (&vis)[2], const uint32_t (&bad)[2], Neg neg) {
+// P = exp2(c S - lse2) and dS = P (dP - delta) of one row's 64 scores, as bf16 pairs in the front of s (KEEP_P) and
+// dp.  neg(k4, a, b, c, d) gives the packed pairs (-lse2) and (-delta) of columns 4 k4 .. 4 k4 + 3.  Unless WHOLE,
+// `vis` has the bits of the columns seen.  `bad`: columns whose other operand was not finite and was zeroed: seen,
+// they make the row NaN.
+template <bool WHOLE, bool KEEP_P, class Neg>
+__device__ __forceinline__ void grad_scores(uint32_t (&s)[HALF], uint32_t (&dp)[HALF], float c, const uint32_t (&vis)[2],
+                                            const uint32_t (&bad)[2], Neg neg) {
     if (bad[0] | bad[1]) {
 #pragma unroll
         for (int k = 0; k < HALF; ++k)
@@ -59,31 +60,35 @@ __device__ __forceinline__ void grad_scores(uint32_t (&s)[HALF], uint32_t (&dp)[
     }
     const uint64_t c2 = f2(c, c);
 #pragma unroll
-    for (int k2 = 0; k2 < HALF / 2; ++k2) {
-        uint64_t nl, nd;
-        neg(k2, nl, nd);
-        const uint64_t x = f2_fma(f2(__uint_as_float(s[2 * k2]), __uint_as_float(s[2 * k2 + 1])), c2, nl);
-        float p0, p1;
-        if ((k2 & 7) >= 8 - EMU) {
-            ex2_poly2(x, p0, p1);
-        } else {
-            float x0, x1;
-            f2_split(x, x0, x1);
-            p0 = ex2(x0);
-            p1 = ex2(x1);
+    for (int k4 = 0; k4 < HALF / 4; ++k4) {
+        uint64_t nl[2], nd[2];
+        neg(k4, nl[0], nl[1], nd[0], nd[1]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int k2 = 2 * k4 + j;
+            const uint32_t v = WHOLE ? 3u : vis[k2 / 16] >> (2 * (k2 & 15));
+            const uint64_t x = f2_fma(f2(__uint_as_float(s[2 * k2]), __uint_as_float(s[2 * k2 + 1])), c2, nl[j]);
+            float p0, p1;
+            if ((k2 & 7) >= 8 - EMU) {
+                ex2_poly2(x, p0, p1);
+            } else {
+                float x0, x1;
+                f2_split(x, x0, x1);
+                p0 = ex2(x0);
+                p1 = ex2(x1);
+            }
+            const uint64_t t = f2_add(f2(__uint_as_float(dp[2 * k2]), __uint_as_float(dp[2 * k2 + 1])), nd[j]);
+            float d0, d1;
+            f2_split(f2_mul(f2(p0, p1), t), d0, d1);
+            if (!WHOLE) {   // selected, not multiplied: a masked score or product may be anything
+                d0 = v & 1u ? d0 : 0.f;
+                d1 = v & 2u ? d1 : 0.f;
+                p0 = v & 1u ? p0 : 0.f;
+                p1 = v & 2u ? p1 : 0.f;
+            }
+            if (KEEP_P) s[k2] = pack_bf16(p0, p1);
+            dp[k2] = pack_bf16(d0, d1);
         }
-        const uint64_t t = f2_add(f2(__uint_as_float(dp[2 * k2]), __uint_as_float(dp[2 * k2 + 1])), nd);
-        float d0, d1;
-        f2_split(f2_mul(f2(p0, p1), t), d0, d1);
-        if (!whole) {
-            const uint32_t v = vis[k2 / 16] >> (2 * (k2 & 15));
-            p0 = v & 1u ? p0 : 0.f;
-            d0 = v & 1u ? d0 : 0.f;
-            p1 = v & 2u ? p1 : 0.f;
-            d1 = v & 2u ? d1 : 0.f;
-        }
-        s[k2] = pack_bf16(p0, p1);
-        dp[k2] = pack_bf16(d0, d1);
     }
 }
 
