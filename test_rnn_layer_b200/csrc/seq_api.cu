@@ -85,6 +85,9 @@ ttt_status check_window(const ttt_window_desc* q) {
     if (!(q->scale > 0.f) || !std::isfinite(q->scale))
         return set_error(TTT_ERR_INVALID_ARG, "scale must be positive and finite");
     if (q->n_seq < 1 || q->n_seq > kMaxRows) return set_error(TTT_ERR_INVALID_ARG, "n_seq=%d must be at least 1", q->n_seq);
+    // blocks of 128 rows and heads are counted in an int (with room for the sinks' chunks and the counter's overshoot)
+    if (std::max((q->Tq / 128LL + q->n_seq) * q->Hq, (q->Tk / 128LL + q->n_seq) * q->Hk) > (1LL << 31) - (1 << 21))
+        return set_error(TTT_ERR_UNSUPPORTED, "n_seq=%d, Hq=%d: too many blocks of rows for one call", q->n_seq, q->Hq);
     return TTT_OK;
 }
 

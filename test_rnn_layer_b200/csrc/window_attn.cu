@@ -53,9 +53,13 @@ enum : int {
     B_PF = B_SR + 2,       // [2] P_X written, O_X rescaled (4 warp arrivals)
     B_PV = B_PF + 2,       // [2] O_X += P_X V done (MMA commit)
     B_SLOT = B_PV + 2,     // tensor memory address (u32) and the abort flag (int)
-    B_BAD = 32             // [NST] 16 bytes: bits of the stage's V rows that are not finite
+    B_BAD = 32,            // [NST] 16 bytes: bits of the stage's V rows that are not finite
+    B_IF = B_BAD + 2 * NST,  // [4] the CTA's items: handed out, taken; their numbers (4 ints)
+    B_IE = B_IF + win::kItemSlots,
+    B_ITEM = B_IE + win::kItemSlots
 };
-static_assert(B_SLOT < B_BAD && B_BAD * 8 + NST * 16 <= 512, "barrier area");
+static_assert(B_SLOT < B_BAD && B_BAD % 2 == 0 && B_ITEM * 8 + 16 <= 512, "barrier area");
+constexpr int kTicket = 1;   // the item counter's place behind the status word (cleared with it)
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 
 struct FwdArgs {
@@ -169,7 +173,10 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
     uint4* bad_rows = reinterpret_cast<uint4*>(bars + B_BAD);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    const win::ItemQueue items{bars + B_IF, bars + B_IE, reinterpret_cast<volatile int*>(bars + B_ITEM), abort_flag};
+
     if (tid == 0) {
+        items.init(2 + 1 + 8);   // MMA issuers, side warps, softmax warps
         tc::mbar_init(bars + B_QF, 1);
         tc::mbar_init(bars + B_QE, 2);
         for (int s = 0; s < NST; ++s) {
@@ -215,8 +222,14 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
         if (tc::elect_one()) {
             int gkv = 0, n = 0;
             bool ok = true;
-            for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
+            for (int w = blockIdx.x, next, k = 0; ok && !*abort_flag; w = next) {
+                if (w >= p.n_items) {
+                    ok = items.put(k, -1);
+                    break;
+                }
+                next = gridDim.x + atomicAdd(p.w.status + kTicket, 1);
                 if (!it.load(p.w, w)) continue;
+                if (!items.put(k++, w)) { ok = false; break; }
                 if (n > 0 && !tc::mbar_wait(bars + B_QE, (n - 1) & 1, abort_flag)) { ok = false; break; }
                 ++n;
                 const int xq = it.h * DH, xk = it.hk * DH;
@@ -242,8 +255,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
         int gkv = 0;
         bool ok = true;
         const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
-        for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
-            if (!it.load(p.w, w)) continue;
+        for (int k = 0; ok; ++k) {
+            const int w = items.take_warp(k);
+            if (w < 0) {
+                ok = w == -1;
+                break;
+            }
+            it.load(p.w, w);
             for (int j = 0; j < it.nt; ++j, ++gkv) {
                 const int s = gkv % NST, use = gkv / NST;
                 if (!__all_sync(0xffffffffu, tc::mbar_wait(bars + B_VF + s, use & 1, abort_flag))) { ok = false; break; }
@@ -299,8 +317,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
                 tc::mma_commit(bars + B_KVE + s);
                 return true;
             };
-            for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
-                if (!it.load(p.w, w)) continue;
+            for (int k = 0; ok; ++k) {
+                const int w = items.take(k);
+                if (w < 0) {
+                    ok = w == -1;
+                    break;
+                }
+                it.load(p.w, w);
                 int a, b;
                 it.range(p.w, X, a, b);
                 const int steps = (it.rows > BQ * X ? it.ns : 0) + b - a;
@@ -350,8 +373,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
             const bool got = tc::mbar_wait(bar, parity, abort_flag);
             return __all_sync(0xffffffffu, got);
         };
-        for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
-            if (!it.load(p.w, w)) continue;
+        for (int k = 0; ok; ++k) {
+            const int w = items.take_warp(k);
+            if (w < 0) {
+                ok = w == -1;
+                break;
+            }
+            it.load(p.w, w);
             int a, b;
             it.range(p.w, X, a, b);
             const int pos = it.pos0 + BQ * X + r;

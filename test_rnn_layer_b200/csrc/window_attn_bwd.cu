@@ -34,9 +34,13 @@ enum : int {
     B_PF = B_SR + 2,       // [2] dS_X written (4 warps)
     B_PV = B_PF + 2,       // [2] its product is done
     B_SLOT = B_PV + 2,
-    B_BAD = 32             // [NST] 16 bytes: bits of the stage's key rows that are not finite
+    B_BAD = 32,            // [NST] 16 bytes: bits of the stage's key rows that are not finite
+    B_IF = B_BAD + 2 * NST,  // [4] the CTA's items: handed out, taken; their numbers (4 ints)
+    B_IE = B_IF + win::kItemSlots,
+    B_ITEM = B_IE + win::kItemSlots
 };
-static_assert(B_SLOT < B_BAD && B_BAD * 8 + NST * 16 <= 512, "barrier area");
+static_assert(B_SLOT < B_BAD && B_BAD % 2 == 0 && B_ITEM * 8 + 16 <= 512, "barrier area");
+constexpr int kTicket = 2;   // the item counter's place behind the status word (cleared with it)
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 
 struct QArgs {
@@ -89,7 +93,10 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
     uint4* bad_rows = reinterpret_cast<uint4*>(bars + B_BAD);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    const win::ItemQueue items{bars + B_IF, bars + B_IE, reinterpret_cast<volatile int*>(bars + B_ITEM), abort_flag};
+
     if (tid == 0) {
+        items.init(2 + 1 + 8);   // MMA issuers, side warps, softmax warps
         tc::mbar_init(bars + B_QF, 1);
         tc::mbar_init(bars + B_QE, 2);
         for (int s = 0; s < NST; ++s) {
@@ -135,8 +142,14 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
         if (tc::elect_one()) {
             int g = 0, n = 0;
             bool ok = true;
-            for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
+            for (int w = blockIdx.x, next, k = 0; ok && !*abort_flag; w = next) {
+                if (w >= p.n_items) {
+                    ok = items.put(k, -1);
+                    break;
+                }
+                next = gridDim.x + atomicAdd(p.w.status + kTicket, 1);
                 if (!it.load(p.w, w)) continue;
+                if (!items.put(k++, w)) { ok = false; break; }
                 if (n > 0 && !tc::mbar_wait(bars + B_QE, (n - 1) & 1, abort_flag)) { ok = false; break; }
                 ++n;
                 const int xq = it.h * DH, xk = it.hk * DH;
@@ -162,8 +175,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
         // ---------------- screen of the keys
         int g = 0;
         bool ok = true;
-        for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
-            if (!it.load(p.w, w)) continue;
+        for (int k = 0; ok; ++k) {
+            const int w = items.take_warp(k);
+            if (w < 0) {
+                ok = w == -1;
+                break;
+            }
+            it.load(p.w, w);
             for (int j = 0; j < it.nt; ++j, ++g) {
                 const int s = g % NST, use = g / NST;
                 if (!wait_all(bars + B_KF + s, use & 1)) { ok = false; break; }
@@ -199,8 +217,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
                 if (release) tc::mma_commit(bars + B_KVE + s);
                 return true;
             };
-            for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
-                if (!it.load(p.w, w)) continue;
+            for (int k = 0; ok; ++k) {
+                const int w = items.take(k);
+                if (w < 0) {
+                    ok = w == -1;
+                    break;
+                }
+                it.load(p.w, w);
                 int a, b;
                 it.range(p.w, X, a, b);
                 if (!tc::mbar_wait(bars + B_QF, n & 1, abort_flag)) { ok = false; break; }
@@ -249,8 +272,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
         const float c = p.c;
         int g = 0, gs = 0, nonfinite = 0;
         bool ok = true;
-        for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
-            if (!it.load(p.w, w)) continue;
+        for (int k = 0; ok; ++k) {
+            const int w = items.take_warp(k);
+            if (w < 0) {
+                ok = w == -1;
+                break;
+            }
+            it.load(p.w, w);
             int a, b;
             it.range(p.w, X, a, b);
             const int pos = it.pos0 + BT * X + r;

@@ -45,15 +45,21 @@ enum : int {
     B_AF = B_PV + 2,       // the item's dV and dK are complete
     B_AE = B_AF + 1,       // and read (8 warps)
     B_SLOT = B_AE + 1,
-    B_BAD = 36             // [NST] 16 bytes: bits of the stage's query rows that are not finite
+    B_BAD = 36,            // [NST] 16 bytes: bits of the stage's query rows that are not finite
+    B_IF = B_BAD + 2 * NST,  // [4] the CTA's items: handed out, taken; their numbers (4 ints)
+    B_IE = B_IF + win::kItemSlots,
+    B_ITEM = B_IE + win::kItemSlots
 };
-static_assert(B_SLOT < B_BAD && B_BAD * 8 + NST * 16 <= 512 && B_BAD % 2 == 0, "barrier area");
+static_assert(B_SLOT < B_BAD && B_BAD % 2 == 0 && B_ITEM * 8 + 16 <= 512, "barrier area");
+constexpr int kTicket = 1;   // the item counter's place behind the status word (cleared with it)
 static_assert(SMEM_BYTES <= 232448, "shared memory");
 
 struct KvArgs {
     CUtensorMap mapQ, mapK, mapV, mapDO;
     WindowArgs w;
-    long long n_window, n_items;   // window items, then chunks of the sinks' further queries
+    long long n_window, n_chunk, n_items;   // window items and chunks of the sinks' further queries
+    int blocks;                    // key blocks with sinks
+    int chunks_first;              // the longer kind of item goes first
     float c;
     int cut;                       // whether sinks are cut up (partial sums in w.partial)
 };
@@ -68,21 +74,23 @@ struct Item {
         const WindowArgs& p = a.w;
         const SeqOffsets cq{p.cu_q, p.n_seq, p.Tq}, ck{p.cu_k, p.n_seq, p.Tk};
         const int G = p.Hq / p.Hk;
-        const bool window = w < a.n_window;
+        const bool window = a.chunks_first ? w >= a.n_chunk : w < a.n_window;
+        if (window && a.chunks_first) w -= a.n_chunk;
+        if (!window && !a.chunks_first) w -= a.n_window;
         int s, c0 = 0, c1 = 0;
+        long long number = 0;
         if (window) {
             hk = (int)(w % p.Hk);
             h0 = hk * G;
             heads = G;
             s = win::block_of<BT>(ck, (int)(w / p.Hk), k_lo, keys);
         } else {
-            const long long r = w - a.n_window;
-            h0 = (int)(r % p.Hq);
+            h0 = (int)(w % p.Hq);
             hk = h0 / G;
             heads = 1;
-            const long long b = r / p.Hq;
-            s = win::block_of<CHUNK>(cq, (int)(b / SINK_BLOCKS), c0, c1);
-            u0 = (int)(b % SINK_BLOCKS) * BT;
+            number = w / p.Hq / a.blocks;
+            s = win::block_of<CHUNK>(cq, (int)number, c0, c1);
+            u0 = (int)(w / p.Hq % a.blocks) * BT;
         }
         if (s < 0) return false;
         q0 = cq.begin(s);
@@ -112,7 +120,7 @@ struct Item {
             i0 = max(i1, c0 - q0);
             i1 = min(nq, c0 - q0 + c1);
             if (i1 <= i0) return false;
-            slot = w - a.n_window;
+            slot = (number * SINK_BLOCKS + u0 / BT) * p.Hq + h0;
         }
         return true;
     }
@@ -128,7 +136,10 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
     uint4* bad_rows = reinterpret_cast<uint4*>(bars + B_BAD);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    const win::ItemQueue items{bars + B_IF, bars + B_IE, reinterpret_cast<volatile int*>(bars + B_ITEM), abort_flag};
+
     if (tid == 0) {
+        items.init(1 + 2 + 8);   // MMA issuers, side warps, softmax warps
         for (int x = 0; x < 2; ++x) {
             tc::mbar_init(bars + B_KVF + x, 1);
             tc::mbar_init(bars + B_KVE + x, 1);
@@ -177,8 +188,15 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
         if (tc::elect_one()) {
             int g = 0, n = 0;
             bool ok = true;
-            for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
-                if (!it.load(p, w) || it.tiles() == 0) continue;
+            for (int w = blockIdx.x, next, k = 0; ok && !*abort_flag; w = next) {
+                if (w >= p.n_items) {
+                    ok = items.put(k, -1);
+                    break;
+                }
+                next = gridDim.x + atomicAdd(p.w.status + kTicket, 1);
+                if (!it.load(p, w)) continue;
+                if (!items.put(k++, w)) { ok = false; break; }
+                if (it.tiles() == 0) continue;
                 const int kv = n & 1, xk = it.hk * DH, tiles = it.tiles();
                 if (n >= 2 && !tc::mbar_wait(bars + B_KVE + kv, ((n >> 1) - 1) & 1, abort_flag)) { ok = false; break; }
                 uint8_t* kt = sm + OFF_KV + kv * 2 * TILE;
@@ -205,8 +223,14 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
             constexpr uint32_t ID_A = tc::instr_desc(1, BT, DH, 0, 1);     // A in tensor memory, B MN-major
             int g = 0, n = 0;
             bool ok = true;
-            for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
-                if (!it.load(p, w) || it.tiles() == 0) continue;
+            for (int k = 0; ok; ++k) {
+                const int w = items.take(k);
+                if (w < 0) {
+                    ok = w == -1;
+                    break;
+                }
+                it.load(p, w);
+                if (it.tiles() == 0) continue;
                 const int kv = n & 1, steps = it.heads * it.tiles();
                 if (!tc::mbar_wait(bars + B_KVF + kv, (n >> 1) & 1, abort_flag)) { ok = false; break; }
                 const uint64_t dK = kmajor_desc(sm + OFF_KV + kv * 2 * TILE), dV = kmajor_desc(sm + OFF_KV + kv * 2 * TILE + TILE);
@@ -262,8 +286,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
         // ---------------- screen of Q and dO (warp 10); lse and delta (warp 11)
         int g = 0;
         bool ok = true;
-        for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
-            if (!it.load(p, w)) continue;
+        for (int k = 0; ok; ++k) {
+            const int w = items.take_warp(k);
+            if (w < 0) {
+                ok = w == -1;
+                break;
+            }
+            it.load(p, w);
             const int tiles = it.tiles();
             for (int t = 0; t < it.heads * tiles; ++t, ++g) {
                 const int s = g % NST, use = g / NST;
@@ -309,8 +338,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
         const float c = p.c;
         int g = 0, n = 0, nonfinite = 0;
         bool ok = true;
-        for (long long w = blockIdx.x; w < p.n_items && ok && !*abort_flag; w += gridDim.x) {
-            if (!it.load(p, w)) continue;
+        for (int k = 0; ok; ++k) {
+            const int w = items.take_warp(k);
+            if (w < 0) {
+                ok = w == -1;
+                break;
+            }
+            it.load(p, w);
             const int tiles = it.tiles(), steps = it.heads * tiles, u = it.u0 + r;
             // queries (as indices) that see key u, cut to the item's
             const int lo_i = max(u - p.w.right - it.first, it.i0), hi_i = u < p.w.sinks ? it.i1 : min(u + p.w.left + 1 - it.first, it.i1);
@@ -455,7 +489,10 @@ cudaError_t launch_window_dkv(const WindowArgs& a, int sms, cudaStream_t s) {
     p.c = a.scale * kLog2e;
     p.cut = cuts_sinks(a);
     p.n_window = win::block_numbers<BT>(a.Tk, a.n_seq) * a.Hk;
-    p.n_items = p.n_window + (p.cut ? chunk_slots(a) : 0);
+    p.blocks = (a.sinks + BT - 1) / BT;
+    p.n_chunk = p.cut ? win::block_numbers<CHUNK>(a.Tq, a.n_seq) * a.Hq * p.blocks : 0;
+    p.n_items = p.n_window + p.n_chunk;
+    p.chunks_first = (long long)CHUNK > (a.Hq / a.Hk) * ((long long)a.left + a.right + BT);
     cudaError_t e = cudaFuncSetAttribute(window_dkv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
     {

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "seq_offsets.cuh"
+#include "tc_prims.cuh"
 
 namespace ttt {
 namespace win {
@@ -44,6 +45,52 @@ __device__ __forceinline__ KeyRange keys_of(int pos0, int rows, int nk, int left
     r.sk = min(sinks, r.lo);
     return r;
 }
+
+// The items a persistent CTA works on: its first is its own number, the others come from a counter in global memory
+// (items differ in length, and a fixed share left some CTAs with 1.4 times the average).  The producer thread draws
+// them and hands them to the CTA's other roles through four slots.
+constexpr int kItemSlots = 4;
+constexpr uint64_t kItemWait = 60000000000ull;   // ns: others may work on one item for long
+struct ItemQueue {
+    uint64_t *full, *empty;     // [kItemSlots] barriers: 1 arrival, and one of each taker
+    volatile int* slot;         // [kItemSlots]
+    const volatile int* abort;
+
+    __device__ __forceinline__ void init(int takers) const {
+        for (int s = 0; s < kItemSlots; ++s) {
+            tc::mbar_init(full + s, 1);
+            tc::mbar_init(empty + s, takers);
+        }
+    }
+    // the n-th item of this CTA (-1: no more)
+    __device__ __forceinline__ bool put(int n, int w) const {
+        const int s = n % kItemSlots, use = n / kItemSlots;
+        if (use > 0 && !tc::mbar_wait(empty + s, (use - 1) & 1, abort, kItemWait)) return false;
+        slot[s] = w;
+        tc::mbar_arrive(full + s);
+        return true;
+    }
+    // by one thread; -2 where the wait ran out
+    __device__ __forceinline__ int take(int n) const {
+        const int s = n % kItemSlots, use = n / kItemSlots;
+        if (!tc::mbar_wait(full + s, use & 1, abort, kItemWait)) return -2;
+        const int w = slot[s];
+        tc::mbar_arrive(empty + s);
+        return w;
+    }
+    // by a warp
+    __device__ __forceinline__ int take_warp(int n) const {
+        const int s = n % kItemSlots, use = n / kItemSlots;
+        const bool ok = tc::mbar_wait(full + s, use & 1, abort, kItemWait);
+        if (!__all_sync(0xffffffffu, ok)) return -2;
+        const int w = slot[s];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) tc::mbar_arrive(empty + s);
+        return w;
+    }
+};
+// most items of a launch: the counter and its overshoot stay inside an int
+constexpr long long kMaxItems = (1LL << 31) - (1 << 20);
 
 }  // namespace win
 }  // namespace ttt
