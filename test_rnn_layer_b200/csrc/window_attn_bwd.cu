@@ -4,9 +4,9 @@
 //
 // Work: an item is 256 query rows of a sequence (tiles A and B of 128) of one head, walking the forward pass's
 // key tiles in steps of 64 keys: S_X = Q_X K^T and dP_X = dO_X V^T into tensor memory, dS_X back to it as bf16,
-// dQ_X += dS_X K.  A thread holds the 64 scores and products of its query row; lse and delta are two registers.
-// Roles (384 threads): warps 0-3 tile A, 4-7 tile B, warp 8 the TMA producer, warps 9 and 10 the MMA issuers,
-// warp 11 the screen for key rows that are not finite.
+// dQ_X += dS_X K.  A thread holds 32 scores and products of its query row; lse and delta are two registers.
+// Roles (640 threads): warps 0-7 tile A, 8-15 tile B, warp 16 the TMA producer, warps 17 and 18 the MMA issuers,
+// warp 19 the screen for key rows that are not finite.
 // Tensor memory, tile X: S 256 X, dP 256 X + 64, dQ 256 X + 128, dS 256 X + 192.
 // Every wait is bounded, as in the forward kernel.
 #include "window_bwd.cuh"
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
     const win::ItemQueue items{bars + B_IF, bars + B_IE, reinterpret_cast<volatile int*>(bars + B_ITEM), abort_flag};
 
     if (tid == 0) {
-        items.init(2 + 1 + 8);   // MMA issuers, side warps, softmax warps
+        items.init(2 + 1 + SOFT);   // MMA issuers, side warps, softmax warps
         tc::mbar_init(bars + B_QF, 1);
         tc::mbar_init(bars + B_QE, 2);
         for (int s = 0; s < NST; ++s) {
@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
         }
         for (int x = 0; x < 2; ++x) {
             tc::mbar_init(bars + B_SF + x, 1);
-            tc::mbar_init(bars + B_SR + x, 4);
-            tc::mbar_init(bars + B_PF + x, 4);
+            tc::mbar_init(bars + B_SR + x, SOFT / 2);
+            tc::mbar_init(bars + B_PF + x, SOFT / 2);
             tc::mbar_init(bars + B_PV + x, 1);
         }
         *abort_flag = 0;
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
         tc::tma_prefetch_desc(&p.mapV);
         tc::tma_prefetch_desc(&p.mapDO);
     }
-    if (warp == 9) {
+    if (warp == SOFT + 1) {
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
     }
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
     };
     Item it;
 
-    if (warp == 8) {
+    if (warp == SOFT) {
         // ---------------- TMA producer
         if (tc::elect_one()) {
             int g = 0, n = 0;
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
             }
             if (!ok) give_up();
         }
-    } else if (warp == 11) {
+    } else if (warp == SOFT + 3) {
         // ---------------- screen of the keys
         int g = 0;
         bool ok = true;
@@ -194,9 +194,9 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
             }
         }
         if (!ok && lane == 0) give_up();
-    } else if (warp >= 9) {
+    } else if (warp > SOFT) {
         // ---------------- MMA issuers, one per tile: S_X and dP_X of a step, then the product of the step before
-        const int X = warp - 9;
+        const int X = warp - SOFT - 1;
         if (tc::elect_one()) {
             constexpr uint32_t ID_S = tc::instr_desc(1, BT, HALF, 0, 0);   // both K-major
             constexpr uint32_t ID_Q = tc::instr_desc(1, BT, DH, 0, 1);     // A in tensor memory, B MN-major
@@ -266,8 +266,8 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
             if (!ok) give_up();
         }
     } else {
-        // ---------------- softmax groups: thread = query row r of tile X
-        const int X = warp >> 2, qd = warp & 3, r = 32 * qd + lane;
+        // ---------------- softmax groups: thread = query row r of tile X, part y of each step's keys
+        const int X = warp / (SOFT / 2), y = (warp >> 2) & 1, qd = warp & 3, r = 32 * qd + lane;
         const uint32_t tX = tm + TM_X * X + ((uint32_t)(32 * qd) << 16);
         const float c = p.c;
         int g = 0, gs = 0, nonfinite = 0;
@@ -291,28 +291,21 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
                 const int s = g % NST, use = g / NST;
                 for (int hh = 0; hh < 2; ++hh) {
                     if (!it.sees(X, j, hh, a, b)) continue;
-                    const int t0 = it.start(j) + HALF * hh;
+                    const int t0 = it.start(j) + HALF * hh + COLS * y;
                     int lo = 0, hi = it.r.sk - t0, sk = 0;
                     if (j >= it.ns) {
                         lo = pos - p.w.left - t0;
                         hi = min(pos + p.w.right + 1, it.nk) - t0;
                         sk = p.w.sinks - t0;
                     }
-                    const bool whole = __all_sync(0xffffffffu, hi >= HALF && lo <= 0);
-                    uint32_t vis[2], bad[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        vis[i] = win::low_bits(hi - 32 * i) & (~win::low_bits(lo - 32 * i) | win::low_bits(sk - 32 * i));
+                    const bool whole = __all_sync(0xffffffffu, hi >= COLS && lo <= 0);
+                    const uint32_t vis = win::low_bits(hi) & (~win::low_bits(lo) | win::low_bits(sk));
                     if (!wait_all(bars + B_SC + s, use & 1) || !wait_all(bars + B_SF + X, gs & 1)) { ok = false; break; }
                     tc::tc_fence_after();
-                    const uint32_t* bw = reinterpret_cast<const uint32_t*>(bad_rows + s) + 2 * hh;
-                    bad[0] = bw[0] & vis[0];
-                    bad[1] = bw[1] & vis[1];
-                    uint32_t sc[HALF], dp[HALF];
-                    tc::tmem_ld_32x32b_x32(tX + TM_S, *reinterpret_cast<uint32_t(*)[32]>(sc));
-                    tc::tmem_ld_32x32b_x32(tX + TM_S + 32, *reinterpret_cast<uint32_t(*)[32]>(sc + 32));
-                    tc::tmem_ld_32x32b_x32(tX + TM_DP, *reinterpret_cast<uint32_t(*)[32]>(dp));
-                    tc::tmem_ld_32x32b_x32(tX + TM_DP + 32, *reinterpret_cast<uint32_t(*)[32]>(dp + 32));
+                    const uint32_t bad = reinterpret_cast<const uint32_t*>(bad_rows + s)[2 * hh + y] & vis;
+                    uint32_t sc[COLS], dp[COLS];
+                    tc::tmem_ld_32x32b_x32(tX + TM_S + COLS * y, sc);
+                    tc::tmem_ld_32x32b_x32(tX + TM_DP + COLS * y, dp);
                     tc::tmem_wait_ld();
                     tc::tc_fence_before();
                     __syncwarp();
@@ -327,7 +320,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
                         if (!wait_all(bars + B_PV + X, (gs - 1) & 1)) { ok = false; break; }
                         tc::tc_fence_after();
                     }
-                    tc::tmem_st_32x32b_x32(tX + TM_DS, *reinterpret_cast<uint32_t(*)[32]>(dp));
+                    tc::tmem_st_32x32b_x16(tX + TM_DS + COLS / 2 * y, *reinterpret_cast<uint32_t(*)[16]>(dp));
                     tc::tmem_wait_st();
                     tc::tc_fence_before();
                     __syncwarp();
@@ -342,17 +335,16 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
                 if (!wait_all(bars + B_PV + X, (gs - 1) & 1)) { ok = false; break; }
                 tc::tc_fence_after();
             }
-            uint32_t o[DH];
-            tc::tmem_ld_32x32b_x32(tX + TM_DQ, *reinterpret_cast<uint32_t(*)[32]>(o));
-            tc::tmem_ld_32x32b_x32(tX + TM_DQ + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
+            uint32_t o[COLS];
+            tc::tmem_ld_32x32b_x32(tX + TM_DQ + COLS * y, o);
             tc::tmem_wait_ld();
             if (!any) {   // rows that see nothing
 #pragma unroll
-                for (int e = 0; e < DH; ++e) o[e] = 0;
+                for (int e = 0; e < COLS; ++e) o[e] = 0;
             }
             if (mine) {
                 const long long t = it.q_lo + BT * X + r;
-                nonfinite |= store_row(p.w.dQ + t * p.w.ld_dq + it.h * DH, o, p.w.scale);
+                nonfinite |= store_row(p.w.dQ + t * p.w.ld_dq + it.h * DH + COLS * y, o, p.w.scale);
             }
         }
         if (!ok && lane == 0) give_up();
@@ -366,7 +358,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == SOFT + 1) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tm, 512);
     }

@@ -5,13 +5,13 @@
 // Work: an item is 128 keys of a sequence of one key head; it walks the query tiles of 128 rows that see them,
 // head after head, so that each sum has one owner and one order (no atomics).  The transposed scores are
 // computed, S^T = K Q^T and dP^T = V dO^T with a key per tensor-memory lane, so that P^T and dS^T are the A
-// operands of dV += P^T dO and dK += dS^T Q straight from tensor memory.  Two softmax groups take 64 queries of
-// a tile each: a thread holds 64 scores and 64 products of its key.  The rows' lse and delta lie in shared
+// operands of dV += P^T dO and dK += dS^T Q straight from tensor memory.  Four softmax groups take 32 queries of
+// a tile each: a thread holds 32 scores and 32 products of its key.  The rows' lse and delta lie in shared
 // memory beside the tile.
 //
-// Roles (384 threads): warps 0-3 queries 0..63 of a tile, 4-7 queries 64..127, warp 8 the TMA producer, warp 9
-// the MMA issuer (one, so that the sums' order is fixed), warp 10 the screen for rows of Q and dO that are not
-// finite, warp 11 loads lse and delta.
+// Roles (640 threads): warps 0-7 queries 0..63 of a tile, 8-15 queries 64..127, warp 16 the TMA producer, warp 17
+// the MMA issuer (one, so that the sums' order is fixed), warp 18 the screen for rows of Q and dO that are not
+// finite, warp 19 loads lse and delta.
 // Tensor memory (512 columns), group X: S 192 X, dP 192 X + 64, P 192 X + 128, dS 192 X + 160; dV 384, dK 448.
 // Per tile of 128 x 128 scores the tensor cores have 4 products of 2.1 MFLOP and the exponential unit 14,336
 // results (1,024 and 896 cycles): S and dP of the next tile are issued as soon as this one's are in registers.
@@ -139,23 +139,23 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
     const win::ItemQueue items{bars + B_IF, bars + B_IE, reinterpret_cast<volatile int*>(bars + B_ITEM), abort_flag};
 
     if (tid == 0) {
-        items.init(1 + 2 + 8);   // MMA issuers, side warps, softmax warps
+        items.init(1 + 2 + SOFT);   // MMA issuers, side warps, softmax warps
         for (int x = 0; x < 2; ++x) {
             tc::mbar_init(bars + B_KVF + x, 1);
             tc::mbar_init(bars + B_KVE + x, 1);
             tc::mbar_init(bars + B_SF + x, 1);
-            tc::mbar_init(bars + B_SR + x, 4);
-            tc::mbar_init(bars + B_PF + x, 4);
+            tc::mbar_init(bars + B_SR + x, SOFT / 2);
+            tc::mbar_init(bars + B_PF + x, SOFT / 2);
             tc::mbar_init(bars + B_PV + x, 1);
         }
         for (int s = 0; s < NST; ++s) {
             tc::mbar_init(bars + B_QF + s, 1);
             tc::mbar_init(bars + B_ST + s, 1);
             tc::mbar_init(bars + B_SC + s, 1);
-            tc::mbar_init(bars + B_QE + s, 9);
+            tc::mbar_init(bars + B_QE + s, 1 + SOFT);
         }
         tc::mbar_init(bars + B_AF, 1);
-        tc::mbar_init(bars + B_AE, 8);
+        tc::mbar_init(bars + B_AE, SOFT);
         *abort_flag = 0;
         tc::fence_mbar_init();
         tc::tma_prefetch_desc(&p.mapQ);
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
         tc::tma_prefetch_desc(&p.mapV);
         tc::tma_prefetch_desc(&p.mapDO);
     }
-    if (warp == 9) {
+    if (warp == SOFT + 1) {
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
     }
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
     };
     Item it;
 
-    if (warp == 8) {
+    if (warp == SOFT) {
         // ---------------- TMA producer
         if (tc::elect_one()) {
             int g = 0, n = 0;
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
             }
             if (!ok) give_up();
         }
-    } else if (warp == 9) {
+    } else if (warp == SOFT + 1) {
         // ---------------- MMA issuer: S and dP of tile t for both groups, then the products of tile t - 1
         if (tc::elect_one()) {
             constexpr uint32_t ID_S = tc::instr_desc(1, BT, HALF, 0, 0);   // both K-major
@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
             }
             if (!ok) give_up();
         }
-    } else if (warp >= 10) {
-        // ---------------- screen of Q and dO (warp 10); lse and delta (warp 11)
+    } else if (warp > SOFT) {
+        // ---------------- screen of Q and dO (warp 18); lse and delta (warp 19)
         int g = 0;
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
             const int tiles = it.tiles();
             for (int t = 0; t < it.heads * tiles; ++t, ++g) {
                 const int s = g % NST, use = g / NST;
-                if (warp == 10) {
+                if (warp == SOFT + 2) {
                     if (!wait_all(bars + B_QF + s, use & 1)) { ok = false; break; }
                     uint8_t* qt = sm + OFF_Q + s * 2 * TILE;
                     uint32_t a[4], b[4];
@@ -332,8 +332,8 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
         }
         if (!ok && lane == 0) give_up();
     } else {
-        // ---------------- softmax groups: thread = key r of the block, queries 64 X .. 64 X + 63 of each tile
-        const int X = warp >> 2, qd = warp & 3, r = 32 * qd + lane;
+        // ---------------- softmax groups: thread = key r of the block, queries 64 X + 32 y ... + 31 of each tile
+        const int X = warp / (SOFT / 2), y = (warp >> 2) & 1, qd = warp & 3, r = 32 * qd + lane;
         const uint32_t lanes = (uint32_t)(32 * qd) << 16, tX = tm + lanes + TM_X * X;
         const float c = p.c;
         int g = 0, n = 0, nonfinite = 0;
@@ -350,27 +350,21 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
             const int lo_i = max(u - p.w.right - it.first, it.i0), hi_i = u < p.w.sinks ? it.i1 : min(u + p.w.left + 1 - it.first, it.i1);
             for (int t = 0; t < steps; ++t, ++g) {
                 const int s = g % NST, use = g / NST;
-                const int base = it.i0 + (t % tiles) * BT + HALF * X, lo = lo_i - base, hi = hi_i - base;
-                const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= HALF);
-                uint32_t vis[2], bad[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) vis[i] = win::low_bits(hi - 32 * i) & ~win::low_bits(lo - 32 * i);
+                const int base = it.i0 + (t % tiles) * BT + HALF * X + COLS * y, lo = lo_i - base, hi = hi_i - base;
+                const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= COLS);
+                const uint32_t vis = win::low_bits(hi) & ~win::low_bits(lo);
                 if (!wait_all(bars + B_ST + s, use & 1) || !wait_all(bars + B_SC + s, use & 1) ||
                     !wait_all(bars + B_SF + X, g & 1)) { ok = false; break; }
                 tc::tc_fence_after();
-                const uint32_t* bw = reinterpret_cast<const uint32_t*>(bad_rows + s) + 2 * X;
-                bad[0] = bw[0] & vis[0];
-                bad[1] = bw[1] & vis[1];
-                uint32_t sc[HALF], dp[HALF];
-                tc::tmem_ld_32x32b_x32(tX + TM_S, *reinterpret_cast<uint32_t(*)[32]>(sc));
-                tc::tmem_ld_32x32b_x32(tX + TM_S + 32, *reinterpret_cast<uint32_t(*)[32]>(sc + 32));
-                tc::tmem_ld_32x32b_x32(tX + TM_DP, *reinterpret_cast<uint32_t(*)[32]>(dp));
-                tc::tmem_ld_32x32b_x32(tX + TM_DP + 32, *reinterpret_cast<uint32_t(*)[32]>(dp + 32));
+                const uint32_t bad = reinterpret_cast<const uint32_t*>(bad_rows + s)[2 * X + y] & vis;
+                uint32_t sc[COLS], dp[COLS];
+                tc::tmem_ld_32x32b_x32(tX + TM_S + COLS * y, sc);
+                tc::tmem_ld_32x32b_x32(tX + TM_DP + COLS * y, dp);
                 tc::tmem_wait_ld();
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bars + B_SR + X);
-                const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(sm + OFF_STAT + s * 1024) + HALF / 4 * X;
+                const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(sm + OFF_STAT + s * 1024) + HALF / 4 * X + COLS / 4 * y;
                 auto neg = [&](int k4, uint64_t& l0, uint64_t& l1, uint64_t& d0, uint64_t& d1) {
                     const ulonglong2 l = nl[k4], d = nl[BT / 4 + k4];
                     l0 = l.x;
@@ -386,24 +380,22 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
                     if (!wait_all(bars + B_PV + X, (g - 1) & 1)) { ok = false; break; }
                     tc::tc_fence_after();
                 }
-                tc::tmem_st_32x32b_x32(tX + TM_P, *reinterpret_cast<uint32_t(*)[32]>(sc));
-                tc::tmem_st_32x32b_x32(tX + TM_DS, *reinterpret_cast<uint32_t(*)[32]>(dp));
+                tc::tmem_st_32x32b_x16(tX + TM_P + COLS / 2 * y, *reinterpret_cast<uint32_t(*)[16]>(sc));
+                tc::tmem_st_32x32b_x16(tX + TM_DS + COLS / 2 * y, *reinterpret_cast<uint32_t(*)[16]>(dp));
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bars + B_PF + X);
             }
             if (!ok) break;
-            // ---- epilogue: group 0 takes dV, group 1 dK
-            uint32_t o[DH];
+            // ---- epilogue: groups X = 0 take dV, X = 1 dK, 32 columns a thread
             if (steps > 0) {
                 if (!wait_all(bars + B_AF, n & 1)) { ok = false; break; }
                 tc::tc_fence_after();
                 ++n;
             }
-            const uint32_t acc = tm + lanes + (X ? TM_DK : TM_DV);
-            tc::tmem_ld_32x32b_x32(acc, *reinterpret_cast<uint32_t(*)[32]>(o));
-            tc::tmem_ld_32x32b_x32(acc + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
+            uint32_t o[COLS];
+            tc::tmem_ld_32x32b_x32(tm + lanes + (X ? TM_DK : TM_DV) + COLS * y, o);
             tc::tmem_wait_ld();
             if (steps > 0) {
                 tc::tc_fence_before();
@@ -411,20 +403,20 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
                 if (lane == 0) tc::mbar_arrive(bars + B_AE);
             } else {
 #pragma unroll
-                for (int e = 0; e < DH; ++e) o[e] = 0;
+                for (int e = 0; e < COLS; ++e) o[e] = 0;
             }
             if (r < it.keys) {
                 const float f = X ? p.w.scale : 1.f;
                 if (it.slot >= 0) {
-                    float4* dst = reinterpret_cast<float4*>(p.w.partial + it.slot * SLOT + (X * BT + r) * DH);
+                    float4* dst = reinterpret_cast<float4*>(p.w.partial + it.slot * SLOT + (X * BT + r) * DH + COLS * y);
 #pragma unroll
-                    for (int e = 0; e < DH / 4; ++e)
+                    for (int e = 0; e < COLS / 4; ++e)
                         dst[e] = make_float4(f * __uint_as_float(o[4 * e]), f * __uint_as_float(o[4 * e + 1]),
                                              f * __uint_as_float(o[4 * e + 2]), f * __uint_as_float(o[4 * e + 3]));
                 } else {
                     const long long t = it.k_lo + r;
-                    nonfinite |= X ? store_row(p.w.dK + t * p.w.ld_dk + it.hk * DH, o, f)
-                                   : store_row(p.w.dV + t * p.w.ld_dv + it.hk * DH, o, f);
+                    const int col = it.hk * DH + COLS * y;
+                    nonfinite |= X ? store_row(p.w.dK + t * p.w.ld_dk + col, o, f) : store_row(p.w.dV + t * p.w.ld_dv + col, o, f);
                 }
             }
         }
@@ -439,7 +431,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == SOFT + 1) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tm, 512);
     }

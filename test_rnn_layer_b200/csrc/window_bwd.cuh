@@ -10,7 +10,10 @@ namespace winb {
 
 using namespace attn;
 
-constexpr int DH = 64, BT = 128, HALF = 64, TILE = BT * DH * 2, THREADS = 384;
+constexpr int DH = 64, BT = 128, HALF = 64, TILE = BT * DH * 2;
+// Sixteen softmax warps (four per scheduler; eight, with 64 scores a thread, left 60% of the issue slots empty) and
+// four others.  A thread holds COLS scores and as many products.
+constexpr int SOFT = 16, THREADS = 32 * (SOFT + 4), COLS = 32;
 constexpr int EMU = 1;          // pairs of every 8 whose 2^x runs on the FMA pipe
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -46,27 +49,26 @@ __device__ __forceinline__ void screen_tile(uint8_t* tile, int lane, uint32_t (&
     }
 }
 
-// P = exp2(c S - lse2) and dS = P (dP - delta) of one row's 64 scores, as bf16 pairs in the front of s (KEEP_P) and
+// P = exp2(c S - lse2) and dS = P (dP - delta) of COLS scores of one row, as bf16 pairs in the front of s (KEEP_P) and
 // dp.  neg(k4, a, b, c, d) gives the packed pairs (-lse2) and (-delta) of columns 4 k4 .. 4 k4 + 3.  Unless WHOLE,
 // `vis` has the bits of the columns seen.  `bad`: columns whose other operand was not finite and was zeroed: seen,
 // they make the row NaN.
 template <bool WHOLE, bool KEEP_P, class Neg>
-__device__ __forceinline__ void grad_scores(uint32_t (&s)[HALF], uint32_t (&dp)[HALF], float c, const uint32_t (&vis)[2],
-                                            const uint32_t (&bad)[2], Neg neg) {
-    if (bad[0] | bad[1]) {
+__device__ __forceinline__ void grad_scores(uint32_t (&s)[COLS], uint32_t (&dp)[COLS], float c, uint32_t vis, uint32_t bad, Neg neg) {
+    if (bad) {
 #pragma unroll
-        for (int k = 0; k < HALF; ++k)
-            if ((bad[k / 32] >> (k & 31)) & 1u) s[k] = 0x7fffffffu;
+        for (int k = 0; k < COLS; ++k)
+            if ((bad >> k) & 1u) s[k] = 0x7fffffffu;
     }
     const uint64_t c2 = f2(c, c);
 #pragma unroll
-    for (int k4 = 0; k4 < HALF / 4; ++k4) {
+    for (int k4 = 0; k4 < COLS / 4; ++k4) {
         uint64_t nl[2], nd[2];
         neg(k4, nl[0], nl[1], nd[0], nd[1]);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int k2 = 2 * k4 + j;
-            const uint32_t v = WHOLE ? 3u : vis[k2 / 16] >> (2 * (k2 & 15));
+            const uint32_t v = WHOLE ? 3u : vis >> (2 * k2);
             const uint64_t x = f2_fma(f2(__uint_as_float(s[2 * k2]), __uint_as_float(s[2 * k2 + 1])), c2, nl[j]);
             float p0, p1;
             if ((k2 & 7) >= 8 - EMU) {
@@ -92,11 +94,11 @@ __device__ __forceinline__ void grad_scores(uint32_t (&s)[HALF], uint32_t (&dp)[
     }
 }
 
-// 64 fp32 values of one row, times `f`, as bf16 to a row of global memory; returns whether one is not finite.
-__device__ __forceinline__ bool store_row(__nv_bfloat16* dst, const uint32_t (&o)[DH], float f) {
+// COLS fp32 values of one row, times `f`, as bf16 to global memory; returns whether one is not finite.
+__device__ __forceinline__ bool store_row(__nv_bfloat16* dst, const uint32_t (&o)[COLS], float f) {
     bool bad = false;
 #pragma unroll
-    for (int c8 = 0; c8 < DH / 8; ++c8) {
+    for (int c8 = 0; c8 < COLS / 8; ++c8) {
         float v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
