@@ -199,6 +199,7 @@ struct WindowArgs {
     __nv_bfloat16 *dQ, *dK, *dV;
     long long ld_do, ld_dq, ld_dk, ld_dv;
     float* delta;                // [Hq, Tq] scratch: rowsum(dOut * Out)
+    uint8_t* key_odd;            // [Hk, Tk] scratch: whether a key is not finite
     float* partial;              // scratch: partial sums of the sinks' dK and dV
 };
 cudaError_t launch_window_attention(const WindowArgs& a, cudaStream_t s);

@@ -175,7 +175,8 @@ extern "C" TTT_API size_t ttt_window_attention_backward_workspace_size(const ttt
     if (check_window(desc) != TTT_OK) return 0;
     WindowArgs a{};
     a.Tq = desc->Tq; a.n_seq = desc->n_seq; a.Hq = desc->Hq; a.Hk = desc->Hk;
-    return kAlign + align_up((size_t)desc->Hq * desc->Tq * sizeof(float)) + (size_t)window_partial_floats(a) * sizeof(float);
+    return kAlign + align_up((size_t)desc->Hq * desc->Tq * sizeof(float)) + align_up((size_t)desc->Hk * desc->Tk) +
+           (size_t)window_partial_floats(a) * sizeof(float);
 }
 
 extern "C" TTT_API ttt_status ttt_window_attention(const ttt_window_desc* desc, const int* cu_q, const int* cu_k, const void* Q,
@@ -246,8 +247,11 @@ extern "C" TTT_API ttt_status ttt_window_attention_backward(const ttt_window_des
     a.dK = static_cast<__nv_bfloat16*>(dK); a.ld_dk = ld_dk;
     a.dV = static_cast<__nv_bfloat16*>(dV); a.ld_dv = ld_dv;
     a.status = static_cast<int*>(workspace);
-    a.delta = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign);
-    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kAlign + align_up((size_t)q.Hq * q.Tq * sizeof(float)));
+    char* space = static_cast<char*>(workspace) + kAlign;
+    a.delta = reinterpret_cast<float*>(space);
+    space += align_up((size_t)q.Hq * q.Tq * sizeof(float));
+    a.key_odd = reinterpret_cast<uint8_t*>(space);
+    a.partial = reinterpret_cast<float*>(space + align_up((size_t)q.Hk * q.Tk));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     SEQ_TRY(cudaMemsetAsync(workspace, 0, 16, s));
     if (q.Tq || q.Tk) SEQ_TRY(launch_window_attention_backward(a, s));

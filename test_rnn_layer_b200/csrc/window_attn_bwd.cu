@@ -6,7 +6,7 @@
 // key tiles in steps of 64 keys: S_X = Q_X K^T and dP_X = dO_X V^T into tensor memory, dS_X back to it as bf16,
 // dQ_X += dS_X K.  A thread holds 32 scores and products of its query row; lse and delta are two registers.
 // Roles (640 threads): warps 0-7 tile A, 8-15 tile B, warp 16 the TMA producer, warps 17 and 18 the MMA issuers,
-// warp 19 the screen for key rows that are not finite.
+// warp 19 zeroes key rows that are not finite.
 // Tensor memory, tile X: S 256 X, dP 256 X + 64, dQ 256 X + 128, dS 256 X + 192.
 // Every wait is bounded, as in the forward kernel.
 #include "window_bwd.cuh"
@@ -27,7 +27,7 @@ enum : int {
     B_QF = 0,              // Q and dO landed
     B_QE = 1,              // the item's S and dP products are done (2 arrivals)
     B_KF = 2,              // [NST] K and V landed
-    B_SC = 2 + NST,        // [NST] K screened
+    B_SC = 2 + NST,        // [NST] K's rows that must not take part are zeroed
     B_KVE = 2 + 2 * NST,   // [NST] both tiles are done with the stage (2 arrivals)
     B_SF = 2 + 3 * NST,    // [2] S_X and dP_X in tensor memory
     B_SR = B_SF + 2,       // [2] the group has read them (4 warps)
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
             if (!ok) give_up();
         }
     } else if (warp == SOFT + 3) {
-        // ---------------- screen of the keys
+        // ---------------- key rows that are not finite, or behind the sequence's last key
         int g = 0;
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -183,12 +183,21 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
             }
             it.load(p.w, w);
             for (int j = 0; j < it.nt; ++j, ++g) {
-                const int s = g % NST, use = g / NST;
+                const int s = g % NST, use = g / NST, u0 = it.start(j);
+                const uint8_t* odd = p.w.key_odd + (long long)it.hk * p.w.Tk + it.k0;
+                uint32_t bad[4], out[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int u = u0 + 32 * e + lane;
+                    bad[e] = __ballot_sync(0xffffffffu, u < it.nk && odd[u]);
+                    out[e] = bad[e] | ~win::low_bits(it.nk - u0 - 32 * e);
+                }
                 if (!wait_all(bars + B_KF + s, use & 1)) { ok = false; break; }
-                uint32_t a[4];
-                screen_tile(sm + OFF_KV + s * 2 * TILE, lane, a);
-                if (lane == 0) bad_rows[s] = make_uint4(a[0], a[1], a[2], a[3]);
-                if (a[0] | a[1] | a[2] | a[3]) tc::fence_proxy_async_smem();
+                if (out[0] | out[1] | out[2] | out[3]) {
+                    zero_rows(sm + OFF_KV + s * 2 * TILE, lane, out);
+                    tc::fence_proxy_async_smem();
+                }
+                if (lane == 0) bad_rows[s] = make_uint4(bad[0], bad[1], bad[2], bad[3]);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bars + B_SC + s);
             }
@@ -364,34 +373,48 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
     }
 }
 
-// delta[h, t] = sum of dO Out over the head's columns: eight lanes a row of 64, 16 bytes each; a warp takes four
-// consecutive rows of one head.  Also looks over the offsets.
-__global__ void __launch_bounds__(256) window_delta_kernel(const WindowArgs p) {
+// delta[h, t] = sum of dO Out over the head's columns, NaN where the row's q is not finite (so that delta is finite
+// only where q, dO and Out are), and key_odd[h, u]: whether the key is not finite.  Eight lanes a row of 64, 16
+// bytes each; a warp takes four consecutive rows of one head.  Also looks over the offsets.
+__global__ void __launch_bounds__(256) window_delta_kernel(const WindowArgs p, long long q_warps, long long warps) {
     if (blockIdx.x == 0) {
         const SeqOffsets cq{p.cu_q, p.n_seq, p.Tq}, ck{p.cu_k, p.n_seq, p.Tk};
         for (int s = threadIdx.x; s <= p.n_seq; s += blockDim.x)
             if (cq.bad(s) || ck.bad(s)) atomicOr(p.status, kStatusBadOffsets);
     }
     const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int h = (int)(w % p.Hq);
-    const long long t = w / p.Hq * 4 + (lane >> 3);
+    long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (w >= warps) return;
+    const bool key = w >= q_warps;
+    if (key) w -= q_warps;
+    const int heads = key ? p.Hk : p.Hq, h = (int)(w % heads), rows = key ? p.Tk : p.Tq;
+    const long long t = w / heads * 4 + (lane >> 3);
+    const int col = h * DH + (lane & 7) * 8;
     float sum = 0.f;
-    if (t < p.Tq) {
-        const int col = h * 64 + (lane & 7) * 8;
-        const uint4 g = *reinterpret_cast<const uint4*>(p.dOut + t * p.ld_do + col);
-        const uint4 o = *reinterpret_cast<const uint4*>(p.Out + t * p.ld_out + col);
-        const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, ow[4] = {o.x, o.y, o.z, o.w};
+    bool odd = false;
+    if (t < rows) {
+        odd = odd_values(*reinterpret_cast<const uint4*>((key ? p.K + t * p.ld_k : p.Q + t * p.ld_q) + col));
+        if (!key) {
+            const uint4 g = *reinterpret_cast<const uint4*>(p.dOut + t * p.ld_do + col);
+            const uint4 o = *reinterpret_cast<const uint4*>(p.Out + t * p.ld_out + col);
+            const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, ow[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&gw[e]), b = *reinterpret_cast<const __nv_bfloat162*>(&ow[e]);
-            sum = fmaf(__low2float(a), __low2float(b), sum);
-            sum = fmaf(__high2float(a), __high2float(b), sum);
+            for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&gw[e]), b = *reinterpret_cast<const __nv_bfloat162*>(&ow[e]);
+                sum = fmaf(__low2float(a), __low2float(b), sum);
+                sum = fmaf(__high2float(a), __high2float(b), sum);
+            }
+            if (odd) sum = NAN;
         }
+    }
+    if (key) {
+        const uint32_t any = __ballot_sync(0xffffffffu, odd);
+        if (t < rows && (lane & 7) == 0) p.key_odd[(long long)h * p.Tk + t] = (any >> lane) & 0xffu ? 1 : 0;
+        return;
     }
 #pragma unroll
     for (int m = 1; m < 8; m *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    if (t < p.Tq && (lane & 7) == 0) p.delta[(long long)h * p.Tq + t] = sum;
+    if (t < rows && (lane & 7) == 0) p.delta[(long long)h * p.Tq + t] = sum;
 }
 
 cudaError_t launch_dq(const WindowArgs& a, int sms, cudaStream_t s) {
@@ -419,8 +442,8 @@ cudaError_t launch_window_attention_backward(const WindowArgs& a, cudaStream_t s
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     {
         LaunchScope scope("window_delta", s);
-        const long long warps = ((long long)a.Tq + 3) / 4 * a.Hq;
-        window_delta_kernel<<<(unsigned)((warps + 7) / 8 ? (warps + 7) / 8 : 1), 256, 0, s>>>(a);
+        const long long q = ((long long)a.Tq + 3) / 4 * a.Hq, warps = q + ((long long)a.Tk + 3) / 4 * a.Hk;
+        window_delta_kernel<<<(unsigned)((warps + 7) / 8 ? (warps + 7) / 8 : 1), 256, 0, s>>>(a, q, warps);
     }
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && a.Tk) e = launch_window_dkv(a, sms, s);

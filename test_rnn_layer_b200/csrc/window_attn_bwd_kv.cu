@@ -9,13 +9,12 @@
 // a tile each: a thread holds 32 scores and 32 products of its key.  The rows' lse and delta lie in shared
 // memory beside the tile.
 //
-// Roles (640 threads): warps 0-7 queries 0..63 of a tile, 8-15 queries 64..127, warp 16 the TMA producer, warp 17
-// the MMA issuer (one, so that the sums' order is fixed), warp 18 the screen for rows of Q and dO that are not
-// finite, warp 19 loads lse and delta.
-// Tensor memory (512 columns), group X: S 192 X, dP 192 X + 64, P 192 X + 128, dS 192 X + 160; dV 384, dK 448.
+// Roles (640 threads): warps 0-7 queries 0..63 of a tile, 8-15 queries 64..127, warp 16 the TMA producer, warps 17
+// and 18 the MMA issuers of the two halves, warp 19 loads lse and delta and zeroes rows that are not finite.
+// Tensor memory (512 columns), half X: S 256 X, dP 256 X + 64 (P and dS, as bf16 pairs, in the first 16 columns of
+// every 32 of theirs); dV 256 X + 128, dK 256 X + 192.  The halves' sums are added in the end.
 // Per tile of 128 x 128 scores the tensor cores have 4 products of 2.1 MFLOP and the exponential unit 14,336
-// results (1,024 and 896 cycles): S and dP of the next tile are issued as soon as this one's are in registers.
-// Every wait is bounded, as in the forward kernel.
+// results (1,024 and 896 cycles).  Every wait is bounded, as in the forward kernel.
 #include "window_bwd.cuh"
 
 namespace ttt {
@@ -29,21 +28,18 @@ constexpr int OFF_Q = 4 * TILE;                       // stage s: Q at OFF_Q + 2
 constexpr int OFF_STAT = OFF_Q + NST * 2 * TILE;      // stage s: 128 x -lse2, 128 x -delta
 constexpr int OFF_BAR = OFF_STAT + NST * 1024;
 constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
-constexpr uint32_t TM_X = 192, TM_S = 0, TM_DP = 64, TM_P = 128, TM_DS = 160, TM_DV = 384, TM_DK = 448;
+constexpr uint32_t TM_X = 256, TM_S = 0, TM_DP = 64, TM_DV = 128, TM_DK = 192;   // P and dS lie where S and dP were
 
 enum : int {
     B_KVF = 0,             // [2] the item's K and V landed
     B_KVE = 2,             // [2] its S and dP products are done
     B_QF = 4,              // [NST] Q and dO landed
-    B_ST = 4 + NST,        // [NST] lse and delta written
-    B_SC = 4 + 2 * NST,    // [NST] Q and dO screened
-    B_QE = 4 + 3 * NST,    // [NST] stage free (a commit and 8 warps)
-    B_SF = 4 + 4 * NST,    // [2] S_X and dP_X in tensor memory
-    B_SR = B_SF + 2,       // [2] the group has read them (4 warps)
-    B_PF = B_SR + 2,       // [2] P_X and dS_X written (4 warps)
-    B_PV = B_PF + 2,       // [2] their products are done
-    B_AF = B_PV + 2,       // the item's dV and dK are complete
-    B_AE = B_AF + 1,       // and read (8 warps)
+    B_ST = 4 + NST,        // [NST] lse and delta written, rows that must not take part zeroed
+    B_QE = 4 + 2 * NST,    // [NST] stage free (2 commits and 16 warps)
+    B_SF = 4 + 3 * NST,    // [2] S_X and dP_X in tensor memory
+    B_PF = B_SF + 2,       // [2] P_X and dS_X written in their place (8 warps)
+    B_AF = B_PF + 2,       // the item's dV and dK are complete (2 commits)
+    B_AE = B_AF + 1,       // and read (16 warps)
     B_SLOT = B_AE + 1,
     B_BAD = 36,            // [NST] 16 bytes: bits of the stage's query rows that are not finite
     B_IF = B_BAD + 2 * NST,  // [4] the CTA's items: handed out, taken; their numbers (4 ints)
@@ -139,22 +135,19 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
     const win::ItemQueue items{bars + B_IF, bars + B_IE, reinterpret_cast<volatile int*>(bars + B_ITEM), abort_flag};
 
     if (tid == 0) {
-        items.init(1 + 2 + SOFT);   // MMA issuers, side warps, softmax warps
+        items.init(2 + 1 + SOFT);   // MMA issuers, side warps, softmax warps
         for (int x = 0; x < 2; ++x) {
             tc::mbar_init(bars + B_KVF + x, 1);
-            tc::mbar_init(bars + B_KVE + x, 1);
+            tc::mbar_init(bars + B_KVE + x, 2);
             tc::mbar_init(bars + B_SF + x, 1);
-            tc::mbar_init(bars + B_SR + x, SOFT / 2);
             tc::mbar_init(bars + B_PF + x, SOFT / 2);
-            tc::mbar_init(bars + B_PV + x, 1);
         }
         for (int s = 0; s < NST; ++s) {
             tc::mbar_init(bars + B_QF + s, 1);
             tc::mbar_init(bars + B_ST + s, 1);
-            tc::mbar_init(bars + B_SC + s, 1);
-            tc::mbar_init(bars + B_QE + s, 1 + SOFT);
+            tc::mbar_init(bars + B_QE + s, 2 + SOFT);
         }
-        tc::mbar_init(bars + B_AF, 1);
+        tc::mbar_init(bars + B_AF, 2);
         tc::mbar_init(bars + B_AE, SOFT);
         *abort_flag = 0;
         tc::fence_mbar_init();
@@ -216,11 +209,15 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
             }
             if (!ok) give_up();
         }
-    } else if (warp == SOFT + 1) {
-        // ---------------- MMA issuer: S and dP of tile t for both groups, then the products of tile t - 1
+    } else if (warp == SOFT + 1 || warp == SOFT + 2) {
+        // ---------------- MMA issuers, one per half of the queries, each with sums of its own (so that neither's
+        // order depends on the other): S and dP of a tile, then the products of P and dS, which the softmax has put
+        // in their place.  One half's products run while the other's scores are worked on.
+        const int X = warp - SOFT - 1;
         if (tc::elect_one()) {
             constexpr uint32_t ID_S = tc::instr_desc(1, BT, HALF, 0, 0);   // both K-major
             constexpr uint32_t ID_A = tc::instr_desc(1, BT, DH, 0, 1);     // A in tensor memory, B MN-major
+            const uint32_t tX = tm + TM_X * X;
             int g = 0, n = 0;
             bool ok = true;
             for (int k = 0; ok; ++k) {
@@ -234,56 +231,39 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
                 const int kv = n & 1, steps = it.heads * it.tiles();
                 if (!tc::mbar_wait(bars + B_KVF + kv, (n >> 1) & 1, abort_flag)) { ok = false; break; }
                 const uint64_t dK = kmajor_desc(sm + OFF_KV + kv * 2 * TILE), dV = kmajor_desc(sm + OFF_KV + kv * 2 * TILE + TILE);
-                for (int t = 0; t <= steps && ok; ++t) {
-                    if (t < steps) {
-                        const int gt = g + t, s = gt % NST;
-                        if (!tc::mbar_wait(bars + B_QF + s, (gt / NST) & 1, abort_flag)) { ok = false; break; }
-                        const uint8_t* qt = sm + OFF_Q + s * 2 * TILE;
-                        for (int X = 0; X < 2; ++X) {
-                            if (gt > 0 && !tc::mbar_wait(bars + B_SR + X, (gt - 1) & 1, abort_flag)) { ok = false; break; }
-                            tc::tc_fence_after();
-                            const uint64_t dQ = kmajor_desc(qt + X * (TILE / 2)), dO = kmajor_desc(qt + TILE + X * (TILE / 2));
+                for (int t = 0; t < steps; ++t, ++g) {
+                    const int s = g % NST;
+                    if (!tc::mbar_wait(bars + B_QF + s, (g / NST) & 1, abort_flag)) { ok = false; break; }
+                    tc::tc_fence_after();
+                    const uint8_t *qt = sm + OFF_Q + s * 2 * TILE + X * (TILE / 2), *ot = qt + TILE;
+                    const uint64_t dQ = kmajor_desc(qt), dO = kmajor_desc(ot);
 #pragma unroll
-                            for (int kk = 0; kk < DH / 16; ++kk)
-                                tc::mma_f16_ss(tm + TM_X * X + TM_S, dK + 2 * kk, dQ + 2 * kk, ID_S, kk > 0);
+                    for (int kk = 0; kk < DH / 16; ++kk) tc::mma_f16_ss(tX + TM_S, dK + 2 * kk, dQ + 2 * kk, ID_S, kk > 0);
 #pragma unroll
-                            for (int kk = 0; kk < DH / 16; ++kk)
-                                tc::mma_f16_ss(tm + TM_X * X + TM_DP, dV + 2 * kk, dO + 2 * kk, ID_S, kk > 0);
-                            tc::mma_commit(bars + B_SF + X);
-                        }
-                        if (t == steps - 1) tc::mma_commit(bars + B_KVE + kv);
-                    }
-                    if (ok && t > 0) {
-                        const int gt = g + t - 1, s = gt % NST;
-                        const uint8_t* qt = sm + OFF_Q + s * 2 * TILE;
-                        // the item before has left the accumulators
-                        if (t == 1 && n > 0 && !tc::mbar_wait(bars + B_AE, (n - 1) & 1, abort_flag)) { ok = false; break; }
-                        for (int X = 0; X < 2; ++X) {
-                            if (!tc::mbar_wait(bars + B_PF + X, gt & 1, abort_flag)) { ok = false; break; }
-                            tc::tc_fence_after();
-                            const uint64_t mQ = mnmajor_desc(qt + X * (TILE / 2)), mO = mnmajor_desc(qt + TILE + X * (TILE / 2));
-                            const uint32_t more = t > 1 || X > 0;
+                    for (int kk = 0; kk < DH / 16; ++kk) tc::mma_f16_ss(tX + TM_DP, dV + 2 * kk, dO + 2 * kk, ID_S, kk > 0);
+                    tc::mma_commit(bars + B_SF + X);
+                    if (t == steps - 1) tc::mma_commit(bars + B_KVE + kv);
+                    // the item before has left the sums
+                    if (t == 0 && n > 0 && !tc::mbar_wait(bars + B_AE, (n - 1) & 1, abort_flag)) { ok = false; break; }
+                    if (!tc::mbar_wait(bars + B_PF + X, g & 1, abort_flag)) { ok = false; break; }
+                    tc::tc_fence_after();
+                    const uint64_t mQ = mnmajor_desc(qt), mO = mnmajor_desc(ot);
 #pragma unroll
-                            for (int kk = 0; kk < HALF / 16; ++kk)
-                                tc::mma_f16_ts(tm + TM_DV, tm + TM_X * X + TM_P + 8 * kk, mO + (uint64_t)(kk * 128), ID_A,
-                                               more | (kk > 0));
+                    for (int kk = 0; kk < HALF / 16; ++kk)   // 16 queries: 8 columns, 32 queries' columns begin 32 apart
+                        tc::mma_f16_ts(tX + TM_DV, tX + TM_S + 8 * kk + 16 * (kk / 2), mO + (uint64_t)(kk * 128), ID_A, t > 0 || kk > 0);
 #pragma unroll
-                            for (int kk = 0; kk < HALF / 16; ++kk)
-                                tc::mma_f16_ts(tm + TM_DK, tm + TM_X * X + TM_DS + 8 * kk, mQ + (uint64_t)(kk * 128), ID_A,
-                                               more | (kk > 0));
-                            tc::mma_commit(bars + B_PV + X);
-                        }
-                        if (ok) tc::mma_commit(bars + B_QE + s);
-                    }
+                    for (int kk = 0; kk < HALF / 16; ++kk)
+                        tc::mma_f16_ts(tX + TM_DK, tX + TM_DP + 8 * kk + 16 * (kk / 2), mQ + (uint64_t)(kk * 128), ID_A, t > 0 || kk > 0);
+                    tc::mma_commit(bars + B_QE + s);
                 }
                 if (ok) tc::mma_commit(bars + B_AF);
-                g += steps;
                 ++n;
             }
             if (!ok) give_up();
         }
     } else if (warp > SOFT) {
-        // ---------------- screen of Q and dO (warp 18); lse and delta (warp 19)
+        // ---------------- lse and delta of the tile's rows; rows of Q and dO that are not finite (delta says so), or
+        // behind the sequence's last query, are zeroed
         int g = 0;
         bool ok = true;
         for (int k = 0; ok; ++k) {
@@ -296,38 +276,38 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
             const int tiles = it.tiles();
             for (int t = 0; t < it.heads * tiles; ++t, ++g) {
                 const int s = g % NST, use = g / NST;
-                if (warp == SOFT + 2) {
-                    if (!wait_all(bars + B_QF + s, use & 1)) { ok = false; break; }
-                    uint8_t* qt = sm + OFF_Q + s * 2 * TILE;
-                    uint32_t a[4], b[4];
-                    screen_tile(qt, lane, a);
-                    screen_tile(qt + TILE, lane, b);
-                    const uint4 m = make_uint4(a[0] | b[0], a[1] | b[1], a[2] | b[2], a[3] | b[3]);
-                    if (lane == 0) bad_rows[s] = m;
-                    if (m.x | m.y | m.z | m.w) tc::fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(bars + B_SC + s);
-                } else {
-                    if (use > 0 && !wait_all(bars + B_QE + s, (use - 1) & 1)) { ok = false; break; }
-                    float* st = reinterpret_cast<float*>(sm + OFF_STAT + s * 1024);
-                    const int i0 = it.i0 + (t % tiles) * BT;
-                    const long long at = (long long)(it.h0 + t / tiles) * p.w.Tq + it.q0;
-                    float l[4], d[4];
+                const int i0 = it.i0 + (t % tiles) * BT;
+                const long long at = (long long)(it.h0 + t / tiles) * p.w.Tq + it.q0;
+                float l[4], d[4];
+                uint32_t bad[4], out[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int i = i0 + 32 * e + lane;
-                        const bool in = i < it.i1;
-                        l[e] = in ? p.w.Lse[at + i] : 0.f;
-                        d[e] = in ? p.w.delta[at + i] : 0.f;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        st[32 * e + lane] = -l[e] * kLog2e;
-                        st[BT + 32 * e + lane] = -d[e];
-                    }
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(bars + B_ST + s);
+                for (int e = 0; e < 4; ++e) {
+                    const int i = i0 + 32 * e + lane;
+                    const bool in = i < it.nq;
+                    l[e] = in ? p.w.Lse[at + i] : 0.f;
+                    d[e] = in ? p.w.delta[at + i] : 0.f;
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    bad[e] = __ballot_sync(0xffffffffu, !isfinite(d[e]));
+                    out[e] = bad[e] | ~win::low_bits(it.nq - i0 - 32 * e);
+                }
+                if (use > 0 && !wait_all(bars + B_QE + s, (use - 1) & 1)) { ok = false; break; }
+                float* st = reinterpret_cast<float*>(sm + OFF_STAT + s * 1024);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    st[32 * e + lane] = -l[e] * kLog2e;
+                    st[BT + 32 * e + lane] = -d[e];
+                }
+                if (out[0] | out[1] | out[2] | out[3]) {
+                    if (!wait_all(bars + B_QF + s, use & 1)) { ok = false; break; }
+                    zero_rows(sm + OFF_Q + s * 2 * TILE, lane, out);
+                    zero_rows(sm + OFF_Q + s * 2 * TILE + TILE, lane, out);
+                    tc::fence_proxy_async_smem();
+                }
+                if (lane == 0) bad_rows[s] = make_uint4(bad[0], bad[1], bad[2], bad[3]);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bars + B_ST + s);
             }
         }
         if (!ok && lane == 0) give_up();
@@ -353,17 +333,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
                 const int base = it.i0 + (t % tiles) * BT + HALF * X + COLS * y, lo = lo_i - base, hi = hi_i - base;
                 const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= COLS);
                 const uint32_t vis = win::low_bits(hi) & ~win::low_bits(lo);
-                if (!wait_all(bars + B_ST + s, use & 1) || !wait_all(bars + B_SC + s, use & 1) ||
-                    !wait_all(bars + B_SF + X, g & 1)) { ok = false; break; }
+                if (!wait_all(bars + B_ST + s, use & 1) || !wait_all(bars + B_SF + X, g & 1)) { ok = false; break; }
                 tc::tc_fence_after();
                 const uint32_t bad = reinterpret_cast<const uint32_t*>(bad_rows + s)[2 * X + y] & vis;
                 uint32_t sc[COLS], dp[COLS];
                 tc::tmem_ld_32x32b_x32(tX + TM_S + COLS * y, sc);
                 tc::tmem_ld_32x32b_x32(tX + TM_DP + COLS * y, dp);
                 tc::tmem_wait_ld();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bars + B_SR + X);
                 const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(sm + OFF_STAT + s * 1024) + HALF / 4 * X + COLS / 4 * y;
                 auto neg = [&](int k4, uint64_t& l0, uint64_t& l1, uint64_t& d0, uint64_t& d1) {
                     const ulonglong2 l = nl[k4], d = nl[BT / 4 + k4];
@@ -376,12 +352,8 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
                 else grad_scores<false, true>(sc, dp, c, vis, bad, neg);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bars + B_QE + s);   // the statistics have been read
-                if (g > 0) {
-                    if (!wait_all(bars + B_PV + X, (g - 1) & 1)) { ok = false; break; }
-                    tc::tc_fence_after();
-                }
-                tc::tmem_st_32x32b_x16(tX + TM_P + COLS / 2 * y, *reinterpret_cast<uint32_t(*)[16]>(sc));
-                tc::tmem_st_32x32b_x16(tX + TM_DS + COLS / 2 * y, *reinterpret_cast<uint32_t(*)[16]>(dp));
+                tc::tmem_st_32x32b_x16(tX + TM_S + COLS * y, *reinterpret_cast<uint32_t(*)[16]>(sc));
+                tc::tmem_st_32x32b_x16(tX + TM_DP + COLS * y, *reinterpret_cast<uint32_t(*)[16]>(dp));
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 __syncwarp();
@@ -394,9 +366,12 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
                 tc::tc_fence_after();
                 ++n;
             }
-            uint32_t o[COLS];
+            uint32_t o[COLS], o1[COLS];
             tc::tmem_ld_32x32b_x32(tm + lanes + (X ? TM_DK : TM_DV) + COLS * y, o);
+            tc::tmem_ld_32x32b_x32(tm + lanes + TM_X + (X ? TM_DK : TM_DV) + COLS * y, o1);
             tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < COLS; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(o1[e]));
             if (steps > 0) {
                 tc::tc_fence_before();
                 __syncwarp();

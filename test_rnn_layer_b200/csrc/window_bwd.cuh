@@ -23,30 +23,28 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     return r;
 }
 
-// Looks through a 128-row tile of 64 bf16 columns in shared memory for rows that are not finite, zeroes them and
-// returns this lane's verdicts as ballots (row 32 g + lane is bit `lane` of word g).  A warp calls it.
-__device__ __forceinline__ void screen_tile(uint8_t* tile, int lane, uint32_t (&word)[4]) {
-    const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+// Rows of a 128-row tile in shared memory that must not enter a product (not finite, or not the sequence's: a weight
+// of zero would not keep them out) are zeroed; bit `lane` of word g is row 32 g + lane.  A warp calls it.
+// Which rows of the inputs are not finite is found by the pass that computes delta: looking through every tile here
+// took longer (3,100 cycles of one warp a step) than the step's products and exponentials.
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int lane, const uint32_t (&word)[4]) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-        uint4* row = reinterpret_cast<uint4*>(tile + (32 * g + lane) * 128);
-        __nv_bfloat162 a0 = zero, a1 = zero;
-#pragma unroll
-        for (int ch = 0; ch < 8; ++ch) {
-            const uint4 v = row[(ch + lane) & 7];   // rotated over the lanes for the banks
-            a0 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.x), zero, a0);
-            a1 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.y), zero, a1);
-            a0 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.z), zero, a0);
-            a1 = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.w), zero, a1);
-        }
-        a0 = __hadd2(a0, a1);
-        const bool bad = !(__low2float(a0) == 0.f && __high2float(a0) == 0.f);
-        word[g] = __ballot_sync(0xffffffffu, bad);
-        if (bad) {
+        if ((word[g] >> lane) & 1u) {
+            uint4* row = reinterpret_cast<uint4*>(tile + (32 * g + lane) * 128);   // a row's 128 bytes lie together
 #pragma unroll
             for (int ch = 0; ch < 8; ++ch) row[ch] = make_uint4(0, 0, 0, 0);
         }
     }
+}
+// whether one of eight bf16 values is not finite
+__device__ __forceinline__ bool odd_values(const uint4& v) {
+    const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+    __nv_bfloat162 a = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&v.x), zero);
+    a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.y), zero, a);
+    a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.z), zero, a);
+    a = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.w), zero, a);
+    return !(__low2float(a) == 0.f && __high2float(a) == 0.f);
 }
 
 // P = exp2(c S - lse2) and dS = P (dP - delta) of COLS scores of one row, as bf16 pairs in the front of s (KEEP_P) and
