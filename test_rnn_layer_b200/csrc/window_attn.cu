@@ -2,21 +2,25 @@
 //   Out[i, h] = Xres[i, h] + sum_u softmax_u(scale q_i . k_u) v_u over the keys u that row i sees:
 //   u <= p + right and (u >= p - left or u < sinks), p = nk - nq + i.
 //
-// Work: an item is 256 query rows of a sequence (tiles A and B of 128) of one head; a persistent grid walks the
+// Work: an item is 256 query rows of a sequence (tiles A and B of 128) of one head; a persistent grid draws the
 // items, heads fastest, so that the CTAs running at a time share the keys and values of few windows in L2.  An
-// item's key tiles are those of its sinks (one of 32 keys where they are that few) and those of the window of
-// its rows; a tile that only one of A and B sees is skipped by the other.  Per key tile, as in the
-// segment-local kernel: S_X = Q_X K^T (tensor memory), P_X = exp2(c S_X - m_X) with a lazily raised maximum,
-// O_X += P_X V.  Masks are four 32-bit words per row, applied only where the tile is not seen whole.
+// item's key tiles are those of its sinks and those of the window of its rows, 128 keys each.  A tile's halves of 64
+// keys go to two softmax groups with a running maximum, a sum and an output of their own (two threads a row, joined
+// at the item's end), so there are four streams (A and B, first and second half) that take turns on the tensor
+// cores and the issue slots; a half that a stream's rows do not see is skipped.  Per half tile, as in the
+// segment-local kernel: S = Q K^T (tensor memory), P = exp2(c S - m) with a lazily raised maximum, O += P V.  P lies
+// where S was.  Masks are two 32-bit words per row, applied only where the half tile is not seen whole.
+// (Two streams of whole rows, eight softmax warps: 4,000 cycles a tile of A and B, 44% of the issue slots used.)
 //
 // A weight of zero times a non-finite value is NaN, and a tile's rows behind the sequence's end may hold
 // anything: warp 11 looks through each value tile in shared memory (one product by zero per pair of elements,
 // well below a tenth of the tile's softmax), zeroes the rows that are not finite and leaves their bits for the
 // softmax, which spoils exactly the query rows that see them.
 //
-// Roles (384 threads): warps 0-3 the softmax of tile A, 4-7 that of tile B (a thread per query row), warp 8 the
-// TMA producer, warps 9 and 10 the MMA issuers of A and B, warp 11 the value screen.
-// Tensor memory (512 columns): S_A 0, S_B 128; O_A 256, O_B 320; P_A 384, P_B 448.
+// Roles (640 threads): warps 0-7 the softmax of tile A, 8-15 that of tile B (first half, second half; a thread per
+// query row), warp 16 the TMA producer, warps 17 and 18 the MMA issuers of A and B, warp 19 the value screen.
+// Tensor memory (512 columns), tile X: S 256 X (second half + 64), P in the first 32 columns of each, O 256 X + 128
+// (second half + 64).
 // Every wait is bounded; on a timeout the CTA sets the status word, lets its copies and products in flight
 // land and returns.
 #include <type_traits>
@@ -30,30 +34,30 @@ namespace {
 
 using namespace attn;
 
-constexpr int DH = 64, BQ = 128, BKV = 128, ROWS = 2 * BQ, NARROW = 32, NST = 4, THREADS = 384;
+constexpr int DH = 64, BQ = 128, BKV = 128, HALF = 64, ROWS = 2 * BQ, NST = 4, SOFT = 16, THREADS = 32 * (SOFT + 4);
 constexpr int TILE = BQ * DH * 2;                 // 16 KB: a 128 x 64 bf16 tile
 constexpr int OFF_Q = 0;                          // Q_A, Q_B
 constexpr int OFF_KV = 2 * TILE;                  // stage s: K at OFF_KV + 2 s TILE, V after it
 constexpr int OFF_BAR = OFF_KV + NST * 2 * TILE;
-constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
-constexpr uint32_t TM_S = 0, TM_O = 256, TM_P = 384;   // + 128 X (S), + 64 X (O, P) for tile X
+constexpr int OFF_ML = OFF_BAR + 512;             // [2][2][128] float2: a row's maximum and sum in each half
+constexpr int SMEM_BYTES = OFF_ML + 4096 + 1024;
+constexpr uint32_t TM_X = 256, TM_O = 128;        // tile X's S at TM_X X + 64 y, its O at TM_X X + TM_O + 64 y
 constexpr float kLazy = 8.0f;                     // log2 of the largest unscaled exponential
 constexpr int EMU = 1;                            // pairs of every 8 whose 2^x runs on the FMA pipe
 
 // Barrier slots (8 bytes each) from OFF_BAR.
 enum : int {
     B_QF = 0,              // Q_A, Q_B landed (TMA bytes)
-    B_QE = 1,              // the item's last S products of both tiles are done (2 arrivals)
+    B_QE = 1,              // the item's S products are done (2 commits)
     B_KF = 2,              // [NST] K tile landed
     B_VF = 2 + NST,        // [NST] V tile landed
     B_VS = 2 + 2 * NST,    // [NST] V tile screened
-    B_KVE = 2 + 3 * NST,   // [NST] both tiles are done with the stage (2 arrivals)
-    B_SF = 2 + 4 * NST,    // [2] S_X is in tensor memory (MMA commit)
-    B_SR = B_SF + 2,       // [2] the softmax group has read S_X (4 warp arrivals)
-    B_PF = B_SR + 2,       // [2] P_X written, O_X rescaled (4 warp arrivals)
-    B_PV = B_PF + 2,       // [2] O_X += P_X V done (MMA commit)
-    B_SLOT = B_PV + 2,     // tensor memory address (u32) and the abort flag (int)
-    B_BAD = 32,            // [NST] 16 bytes: bits of the stage's V rows that are not finite
+    B_KVE = 2 + 3 * NST,   // [NST] the streams are done with the stage (4 arrivals)
+    B_SF = 2 + 4 * NST,    // [4] a stream's S is in tensor memory, its products before are done (MMA commit)
+    B_PF = B_SF + 4,       // [4] its P is written, its O rescaled (4 warp arrivals)
+    B_OD = B_PF + 4,       // [4] its O is complete (MMA commit)
+    B_SLOT = B_OD + 4,     // tensor memory address (u32) and the abort flag (int)
+    B_BAD = 36,            // [NST] 16 bytes: bits of the stage's V rows that are not finite
     B_IF = B_BAD + 2 * NST,  // [4] the CTA's items: handed out, taken; their numbers (4 ints)
     B_IE = B_IF + win::kItemSlots,
     B_ITEM = B_IE + win::kItemSlots
@@ -72,7 +76,6 @@ struct FwdArgs {
 struct Item {
     int q_lo, rows, pos0, k0, nk, h, hk;
     int ns, nt;                     // sink tiles, all tiles
-    bool narrow;                    // the one sink tile has NARROW keys
     win::KeyRange r;
 
     __device__ __forceinline__ bool load(const WindowArgs& p, long long w) {
@@ -86,25 +89,22 @@ struct Item {
         nk = max(ck.begin(s + 1) - k0, 0);
         pos0 = nk - nq + (q_lo - q0);
         r = win::keys_of(pos0, rows, nk, p.left, p.right, p.sinks);
-        narrow = r.sk > 0 && r.sk <= NARROW;
         ns = (r.sk + BKV - 1) / BKV;
         nt = ns + (r.hi - r.lo + BKV - 1) / BKV;
         return true;
     }
     __device__ __forceinline__ int start(int j) const { return j < ns ? BKV * j : r.lo + BKV * (j - ns); }
-    // tile X's window tiles [a, b), counted from the item's first tile (sinks that reach into the window begin it)
+    // the window keys [a, b) of tile X's rows (sinks that reach into the window begin it)
     __device__ __forceinline__ void range(const WindowArgs& p, int X, int& a, int& b) const {
         const int n = min(rows - BQ * X, BQ), q = pos0 + BQ * X;
-        const int lo = p.sinks > r.lo ? r.lo : max(q - p.left, r.lo), hi = min(q + n + p.right, r.hi);
-        if (n <= 0 || hi <= lo) {
-            a = b = ns;
-            return;
-        }
-        a = ns + (lo - r.lo) / BKV;
-        b = ns + (hi - r.lo + BKV - 1) / BKV;
+        a = p.sinks > r.lo ? r.lo : max(q - p.left, r.lo);
+        b = n > 0 ? max(min(q + n + p.right, r.hi), a) : a;
     }
-    // sinks lie in front of the item's window, so every row of the item sees them
-    __device__ __forceinline__ bool sees(int X, int j, int a, int b) const { return j < ns ? rows > BQ * X : j >= a && j < b; }
+    // whether tile X meets keys of half y of key tile j (sinks lie in front of the window: every row sees them)
+    __device__ __forceinline__ bool sees(int X, int j, int y, int a, int b) const {
+        const int t0 = start(j) + HALF * y;
+        return j < ns ? rows > BQ * X && t0 < r.sk : t0 < b && t0 + HALF > a;
+    }
 };
 
 struct RowState {
@@ -176,20 +176,19 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
     const win::ItemQueue items{bars + B_IF, bars + B_IE, reinterpret_cast<volatile int*>(bars + B_ITEM), abort_flag};
 
     if (tid == 0) {
-        items.init(2 + 1 + 8);   // MMA issuers, side warps, softmax warps
+        items.init(2 + 1 + SOFT);   // MMA issuers, screen, softmax warps
         tc::mbar_init(bars + B_QF, 1);
         tc::mbar_init(bars + B_QE, 2);
         for (int s = 0; s < NST; ++s) {
             tc::mbar_init(bars + B_KF + s, 1);
             tc::mbar_init(bars + B_VF + s, 1);
             tc::mbar_init(bars + B_VS + s, 1);
-            tc::mbar_init(bars + B_KVE + s, 2);
+            tc::mbar_init(bars + B_KVE + s, 4);
         }
-        for (int x = 0; x < 2; ++x) {
-            tc::mbar_init(bars + B_SF + x, 1);
-            tc::mbar_init(bars + B_SR + x, 4);
-            tc::mbar_init(bars + B_PF + x, 4);
-            tc::mbar_init(bars + B_PV + x, 1);
+        for (int z = 0; z < 4; ++z) {
+            tc::mbar_init(bars + B_SF + z, 1);
+            tc::mbar_init(bars + B_PF + z, 4);
+            tc::mbar_init(bars + B_OD + z, 1);
         }
         *abort_flag = 0;
         tc::fence_mbar_init();
@@ -197,7 +196,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
         tc::tma_prefetch_desc(&p.mapK);
         tc::tma_prefetch_desc(&p.mapV);
     }
-    if (warp == 9) {
+    if (warp == SOFT + 1) {
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
     }
@@ -217,7 +216,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
     };
     Item it;
 
-    if (warp == 8) {
+    if (warp == SOFT) {
         // ---------------- TMA producer: the item's Q tiles, then its K and V tiles through the ring
         if (tc::elect_one()) {
             int gkv = 0, n = 0;
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
             }
             if (!ok) give_up();
         }
-    } else if (warp == 11) {
+    } else if (warp == SOFT + 3) {
         // ---------------- value screen: lane takes rows lane, lane + 32, ...; a row's 128 bytes are contiguous
         // (the swizzle permutes its 16-byte chunks), chunks taken in a rotated order for the banks
         int gkv = 0;
@@ -293,30 +292,16 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
             }
         }
         if (!ok && lane == 0) give_up();
-    } else if (warp >= 9) {
-        // ---------------- MMA issuers, one per tile.  Step n = the tile's n-th key tile; the issuer of X issues
-        // S_X of step n (once its group has read S_X of the step before), then P_X V of step n - 1.
-        const int X = warp - 9;
+    } else if (warp > SOFT) {
+        // ---------------- MMA issuers, one per tile X; its two streams in turn: P V of the stream's last half tile,
+        // once P lies in S's place, and the S of its next one in order behind it
+        const int X = warp - SOFT - 1;
         if (tc::elect_one()) {
-            constexpr uint32_t ID_S = tc::instr_desc(1, BQ, BKV, 0, 0);      // bf16, both K-major
-            constexpr uint32_t ID_SN = tc::instr_desc(1, BQ, NARROW, 0, 0);
+            constexpr uint32_t ID_S = tc::instr_desc(1, BQ, HALF, 0, 0);     // bf16, both K-major
             constexpr uint32_t ID_PV = tc::instr_desc(1, BQ, DH, 0, 1);      // bf16, A in tensor memory, V MN-major
             const uint64_t dQ = kmajor_desc(sm + OFF_Q + X * TILE);
-            int gkv = 0, gs = 0, n = 0;
+            int gkv = 0, gs[2] = {0, 0}, n = 0;
             bool ok = true;
-            // P_X V of step gs - 1, whose values lie in stage s
-            auto pv = [&](int s, bool accumulate, bool narrow) {
-                if (!tc::mbar_wait(bars + B_PF + X, (gs - 1) & 1, abort_flag)) return false;
-                tc::tc_fence_after();
-                const uint64_t dV = mnmajor_desc(sm + OFF_KV + s * 2 * TILE + TILE);
-                const int steps = narrow ? NARROW / 16 : BKV / 16;
-                for (int kk = 0; kk < steps; ++kk)
-                    tc::mma_f16_ts(tm + TM_O + 64 * X, tm + TM_P + 64 * X + 8 * kk, dV + (uint64_t)(kk * 128), ID_PV,
-                                   (accumulate || kk > 0) ? 1u : 0u);
-                tc::mma_commit(bars + B_PV + X);
-                tc::mma_commit(bars + B_KVE + s);
-                return true;
-            };
             for (int k = 0; ok; ++k) {
                 const int w = items.take(k);
                 if (w < 0) {
@@ -326,159 +311,172 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
                 it.load(p.w, w);
                 int a, b;
                 it.range(p.w, X, a, b);
-                const int steps = (it.rows > BQ * X ? it.ns : 0) + b - a;
                 if (!tc::mbar_wait(bars + B_QF, n & 1, abort_flag)) { ok = false; break; }
                 ++n;
                 tc::tc_fence_after();
-                if (steps == 0) tc::mbar_arrive(bars + B_QE);
-                int done = 0, prev = -1;
-                bool prev_narrow = false;
+                int pending[2] = {-1, -1};   // the stage whose P V is to come
+                bool more[2] = {false, false};
+                auto pv = [&](int y) {
+                    const int s = pending[y];
+                    if (!tc::mbar_wait(bars + B_PF + 2 * X + y, gs[y] & 1, abort_flag)) return false;
+                    ++gs[y];
+                    tc::tc_fence_after();
+                    const uint32_t tS = tm + TM_X * X + HALF * y;
+                    const uint64_t dV = mnmajor_desc(sm + OFF_KV + s * 2 * TILE + TILE + y * (TILE / 2));
+#pragma unroll
+                    for (int kk = 0; kk < HALF / 16; ++kk)
+                        tc::mma_f16_ts(tS + TM_O, tS + 8 * kk, dV + (uint64_t)(kk * 128), ID_PV, (more[y] || kk > 0) ? 1u : 0u);
+                    more[y] = true;
+                    tc::mma_commit(bars + B_KVE + s);
+                    return true;
+                };
                 for (int j = 0; j < it.nt && ok; ++j, ++gkv) {
                     const int s = gkv % NST, use = gkv / NST;
+                    // (also where a half is not seen: the arrival then counts for this use of the stage)
                     if (!tc::mbar_wait(bars + B_KF + s, use & 1, abort_flag)) { ok = false; break; }
-                    if (!it.sees(X, j, a, b)) {
-                        tc::mbar_arrive(bars + B_KVE + s);
-                        continue;
-                    }
-                    if (gs > 0 && !tc::mbar_wait(bars + B_SR + X, (gs - 1) & 1, abort_flag)) { ok = false; break; }
                     tc::tc_fence_after();
-                    const bool narrow = it.narrow && j == 0;
-                    const uint64_t dK = kmajor_desc(sm + OFF_KV + s * 2 * TILE);
-                    const uint32_t id = narrow ? ID_SN : ID_S;
 #pragma unroll
-                    for (int kk = 0; kk < DH / 16; ++kk)
-                        tc::mma_f16_ss(tm + TM_S + 128 * X, dQ + 2 * kk, dK + 2 * kk, id, kk > 0);
-                    tc::mma_commit(bars + B_SF + X);
-                    if (done == steps - 1) tc::mma_commit(bars + B_QE);
-                    if (prev >= 0 && !pv(prev, done > 1, prev_narrow)) { ok = false; break; }
-                    ++gs;
-                    ++done;
-                    prev = s;
-                    prev_narrow = narrow;
+                    for (int y = 0; y < 2; ++y) {
+                        if (pending[y] >= 0 && !pv(y)) { ok = false; break; }
+                        pending[y] = -1;
+                        if (!it.sees(X, j, y, a, b)) {
+                            tc::mbar_arrive(bars + B_KVE + s);
+                            continue;
+                        }
+                        const uint64_t dK = kmajor_desc(sm + OFF_KV + s * 2 * TILE + y * (TILE / 2));
+#pragma unroll
+                        for (int kk = 0; kk < DH / 16; ++kk)
+                            tc::mma_f16_ss(tm + TM_X * X + HALF * y, dQ + 2 * kk, dK + 2 * kk, ID_S, kk > 0);
+                        tc::mma_commit(bars + B_SF + 2 * X + y);
+                        pending[y] = s;
+                    }
                 }
-                if (ok && prev >= 0 && !pv(prev, done > 1, prev_narrow)) ok = false;
+                if (ok) tc::mma_commit(bars + B_QE);
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    if (ok && pending[y] >= 0) ok = pv(y);
+                    if (ok && more[y]) tc::mma_commit(bars + B_OD + 2 * X + y);
+                }
             }
             if (!ok) give_up();
         }
     } else {
-        // ---------------- softmax groups: warps 0-3 tile A, 4-7 tile B; thread = query row r of its tile
-        const int X = warp >> 2, qd = warp & 3, r = 32 * qd + lane;
-        const uint32_t lanes = (uint32_t)(32 * qd) << 16;
-        const uint32_t tS = tm + lanes + TM_S + 128 * X, tO = tm + lanes + TM_O + 64 * X, tP = tm + lanes + TM_P + 64 * X;
+        // ---------------- softmax groups: thread = query row r of tile X, half y of each key tile
+        const int X = warp / (SOFT / 2), y = (warp >> 2) & 1, z = 2 * X + y, qd = warp & 3, r = 32 * qd + lane;
+        const uint32_t lanes = (uint32_t)(32 * qd) << 16, tX = tm + lanes + TM_X * X, tS = tX + HALF * y, tO = tS + TM_O;
+        float2* ml = reinterpret_cast<float2*>(sm + OFF_ML) + 256 * X;
         const float c = p.c;
-        int gs = 0, gkv = 0, nonfinite = 0;
+        int gs = 0, gkv = 0, nonfinite = 0, complete[2] = {0, 0};
         bool ok = true;
         // every branch below is uniform over the warp (the item, the key tile, the waits' outcome)
         auto wait_all = [&](uint64_t* bar, uint32_t parity) {
             const bool got = tc::mbar_wait(bar, parity, abort_flag);
             return __all_sync(0xffffffffu, got);
         };
-        for (int k = 0; ok; ++k) {
-            const int w = items.take_warp(k);
-            if (w < 0) {
-                ok = w == -1;
-                break;
+        for (int k = 0;; ++k) {
+            // the two halves of a row go on or stop together: they meet at barriers below
+            int w = ok ? items.take_warp(k) : -2;
+            if (w == -2) {
+                ok = false;
+                w = -1;
             }
+            if (tc::bar_sync_or(1 + X, 256, w < 0)) break;
             it.load(p.w, w);
             int a, b;
             it.range(p.w, X, a, b);
             const int pos = it.pos0 + BQ * X + r;
             RowState st{-INFINITY, 0.f, true};
-            // one key tile of NC keys: softmax, the screen's verdict, O's rescaling, P to tensor memory
-            auto step = [&](auto width, int j) {
-                constexpr int NC = decltype(width)::value;
-                // the keys of this tile that the row sees, as bits
-                const int t0 = it.start(j);
+            for (int j = 0; j < it.nt && ok; ++j, ++gkv) {
+                if (!it.sees(X, j, y, a, b)) continue;
+                // the keys of this half that the row sees, as bits
+                const int t0 = it.start(j) + HALF * y;
                 int lo = 0, hi = it.r.sk - t0, sk = 0;
                 if (j >= it.ns) {
                     lo = pos - p.w.left - t0;
                     hi = min(pos + p.w.right + 1, it.nk) - t0;
                     sk = p.w.sinks - t0;
                 }
-                const bool whole = __all_sync(0xffffffffu, hi >= NC && lo <= 0);
-                if (!wait_all(bars + B_SF + X, gs & 1)) return false;
+                const bool whole = __all_sync(0xffffffffu, hi >= HALF && lo <= 0);
+                if (!wait_all(bars + B_SF + z, gs & 1)) { ok = false; break; }
                 tc::tc_fence_after();
-                uint32_t s[NC];
-#pragma unroll
-                for (int k = 0; k < NC; k += 32) tc::tmem_ld_32x32b_x32(tS + k, *reinterpret_cast<uint32_t(*)[32]>(s + k));
+                uint32_t s[HALF];
+                tc::tmem_ld_32x32b_x32(tS, *reinterpret_cast<uint32_t(*)[32]>(s));
+                tc::tmem_ld_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
                 tc::tmem_wait_ld();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bars + B_SR + X);   // S_X may be overwritten
                 if (!whole) {
 #pragma unroll
-                    for (int i = 0; i < NC / 32; ++i) {
+                    for (int i = 0; i < HALF / 32; ++i) {
                         const uint32_t vis = visible(lo, hi, sk, i);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) s[32 * i + k] = (vis >> k) & 1u ? s[32 * i + k] : 0xff800000u;   // -inf
+                        for (int e = 0; e < 32; ++e) s[32 * i + e] = (vis >> e) & 1u ? s[32 * i + e] : 0xff800000u;   // -inf
                     }
                 }
-                const float f = softmax_tile<NC>(s, c, st);
+                const float f = softmax_tile<HALF>(s, c, st);
                 // the screened values: a row that sees one that is not finite becomes NaN
                 const int stage = gkv % NST;
-                if (!wait_all(bars + B_VS + stage, (gkv / NST) & 1)) return false;
-                const uint4 bad = bad_rows[stage];
-                if (bad.x | bad.y | bad.z | bad.w) {
-                    if ((bad.x & visible(lo, hi, sk, 0)) | (bad.y & visible(lo, hi, sk, 1)) | (bad.z & visible(lo, hi, sk, 2)) |
-                        (bad.w & visible(lo, hi, sk, 3)))
-                        st.l = NAN;
+                if (!wait_all(bars + B_VS + stage, (gkv / NST) & 1)) { ok = false; break; }
+                const uint2 bad = reinterpret_cast<const uint2*>(bad_rows + stage)[y];
+                if (bad.x | bad.y) {
+                    if ((bad.x & visible(lo, hi, sk, 0)) | (bad.y & visible(lo, hi, sk, 1))) st.l = NAN;
                 }
-                // the previous step's P V is done: P_X may be rewritten and O_X is stable
-                if (gs > 0) {
-                    if (!wait_all(bars + B_PV + X, (gs - 1) & 1)) return false;
-                    tc::tc_fence_after();
-                }
-                if (__any_sync(0xffffffffu, f != 1.f && !st.first)) {
-                    uint32_t o[32];
+                if (__any_sync(0xffffffffu, f != 1.f && !st.first)) {   // S's arrival says that O is stable
+                    uint32_t o[16];
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        tc::tmem_ld_32x32b_x32(tO + 32 * half, o);
+                    for (int q = 0; q < DH / 16; ++q) {
+                        tc::tmem_ld_32x32b_x16(tO + 16 * q, o);
                         tc::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tc::tmem_st_32x32b_x32(tO + 32 * half, o);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tc::tmem_st_32x32b_x16(tO + 16 * q, o);
                     }
                 }
                 st.first = false;
-                if constexpr (NC == NARROW) {
-                    tc::tmem_st_32x32b_x16(tP, *reinterpret_cast<uint32_t(*)[16]>(s));
-                } else {
-                    tc::tmem_st_32x32b_x32(tP + 0, *reinterpret_cast<uint32_t(*)[32]>(s + 0));
-                    tc::tmem_st_32x32b_x32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(s + 32));
-                }
+                tc::tmem_st_32x32b_x32(tS, *reinterpret_cast<uint32_t(*)[32]>(s));
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bars + B_PF + X);
+                if (lane == 0) tc::mbar_arrive(bars + B_PF + z);
                 ++gs;
-                return true;
-            };
-            for (int j = 0; j < it.nt && ok; ++j, ++gkv) {
-                if (!it.sees(X, j, a, b)) continue;
-                ok = it.narrow && j == 0 ? step(std::integral_constant<int, NARROW>{}, j)
-                                               : step(std::integral_constant<int, BKV>{}, j);
             }
-            if (!ok) break;
-            // ---- epilogue: O_X / l (+ residual) as bf16, the row's log-sum-exp
-            if (!st.first) {
-                if (!wait_all(bars + B_PV + X, (gs - 1) & 1)) { ok = false; break; }
-                tc::tc_fence_after();
+            // ---- epilogue: the halves' O joined, / l (+ residual) as bf16, 32 columns a thread; log-sum-exp
+            ml[128 * y + r] = make_float2(st.m, st.first ? -1.f : st.l);   // (no step: a sum of -1)
+            if (tc::bar_sync_or(1 + X, 256, !ok)) {
+                ok = false;
+                continue;
             }
-            uint32_t o[64];   // without a key tile what was there before: not used
-            tc::tmem_ld_32x32b_x32(tO + 0, *reinterpret_cast<uint32_t(*)[32]>(o + 0));
-            tc::tmem_ld_32x32b_x32(tO + 32, *reinterpret_cast<uint32_t(*)[32]>(o + 32));
+            const bool has[2] = {ml[r].y != -1.f, ml[128 + r].y != -1.f};   // (the same for every row)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (has[q]) ok = wait_all(bars + B_OD + 2 * X + q, complete[q]++ & 1) && ok;
+            }
+            if (!ok) continue;
+            tc::tc_fence_after();
+            float2 ml0 = ml[r], ml1 = ml[128 + r];
+            if (!has[0]) ml0.y = 0.f;
+            if (!has[1]) ml1.y = 0.f;
+            const float m = fmaxf(ml0.x, ml1.x), ref = m == -INFINITY ? 0.f : m;
+            const float f0 = ex2(ml0.x - ref), f1 = ex2(ml1.x - ref), l = ml0.y * f0 + ml1.y * f1;
+            // NaN sums stay (a half whose maximum is -infinity has factor 0 and, unless it saw a NaN, a finite sum)
+            const bool empty = m == -INFINITY && ml0.y == ml0.y && ml1.y == ml1.y;
+            const float inv = 1.0f / l, g0 = f0 * inv, g1 = f1 * inv;
+            uint32_t o0[32], o1[32];
+            tc::tmem_ld_32x32b_x32(tX + TM_O + 32 * y, o0);
+            tc::tmem_ld_32x32b_x32(tX + TM_O + HALF + 32 * y, o1);
             tc::tmem_wait_ld();
+            tc::tc_fence_before();
             if (BQ * X + r < it.rows) {
-                const bool empty = st.first || (st.m == -INFINITY && st.l == st.l);
-                const float inv = 1.0f / st.l;
-                const long long t = it.q_lo + BQ * X + r, col = (long long)it.h * DH;
+                const long long t = it.q_lo + BQ * X + r, col = (long long)it.h * DH + 32 * y;
                 const uint4* xr = p.w.Xres ? reinterpret_cast<const uint4*>(p.w.Xres + t * p.w.ld_out + col) : nullptr;
                 uint4* dst = reinterpret_cast<uint4*>(p.w.Out + t * p.w.ld_out + col);
 #pragma unroll
-                for (int c8 = 0; c8 < DH / 8; ++c8) {
+                for (int c8 = 0; c8 < 4; ++c8) {
                     float v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = empty ? 0.f : __uint_as_float(o[8 * c8 + e]) * inv;
+                    for (int e = 0; e < 8; ++e) {   // what a half without a step left in tensor memory is not used
+                        const float a0 = has[0] ? __uint_as_float(o0[8 * c8 + e]) * g0 : 0.f;
+                        const float a1 = has[1] ? __uint_as_float(o1[8 * c8 + e]) * g1 : 0.f;
+                        v[e] = empty ? 0.f : l == l ? a0 + a1 : l;
+                    }
                     if (xr) {
                         const uint4 xv = xr[c8];
                         const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
@@ -494,10 +492,10 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
                     dst[c8] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                                          pack_bf16(v[6], v[7]));
                 }
-                if (p.w.Lse)
-                    p.w.Lse[(long long)it.h * p.w.Tq + t] =
-                        empty ? -INFINITY : (st.m == -INFINITY ? 0.f : st.m) * 0.69314718055994531f + logf(st.l);
+                if (p.w.Lse && y == 0)
+                    p.w.Lse[(long long)it.h * p.w.Tq + t] = empty ? -INFINITY : ref * 0.69314718055994531f + logf(l);
             }
+            // (the next item's first barrier keeps both halves from each other's O until it has been read)
         }
         if (!ok) {
             if (lane == 0) give_up();
@@ -512,7 +510,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == SOFT + 1) {
         tc::tc_fence_after();
         tc::tmem_dealloc(tm, 512);
     }

@@ -9,10 +9,10 @@
 // a tile each: a thread holds 32 scores and 32 products of its key.  The rows' lse and delta lie in shared
 // memory beside the tile.
 //
-// Roles (640 threads): warps 0-7 queries 0..63 of a tile, 8-15 queries 64..127, warp 16 the TMA producer, warps 17
-// and 18 the MMA issuers of the two halves, warp 19 loads lse and delta and zeroes rows that are not finite.
-// Tensor memory (512 columns), half X: S 256 X, dP 256 X + 64 (P and dS, as bf16 pairs, in the first 16 columns of
-// every 32 of theirs); dV 256 X + 128, dK 256 X + 192.  The halves' sums are added in the end.
+// Roles (608 threads): warps 0-7 queries 0..63 of a tile, 8-15 queries 64..127, warp 16 the TMA producer, warp 17
+// the MMA issuer (one, so that the sums' order is fixed), warp 18 loads lse and delta and zeroes rows that are not
+// finite.
+// Tensor memory (512 columns), half X: S 192 X, dP 192 X + 64, P 192 X + 128, dS 192 X + 160; dV 384, dK 448.
 // Per tile of 128 x 128 scores the tensor cores have 4 products of 2.1 MFLOP and the exponential unit 14,336
 // results (1,024 and 896 cycles).  Every wait is bounded, as in the forward kernel.
 #include "window_bwd.cuh"
@@ -28,17 +28,20 @@ constexpr int OFF_Q = 4 * TILE;                       // stage s: Q at OFF_Q + 2
 constexpr int OFF_STAT = OFF_Q + NST * 2 * TILE;      // stage s: 128 x -lse2, 128 x -delta
 constexpr int OFF_BAR = OFF_STAT + NST * 1024;
 constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
-constexpr uint32_t TM_X = 256, TM_S = 0, TM_DP = 64, TM_DV = 128, TM_DK = 192;   // P and dS lie where S and dP were
+constexpr int KV_THREADS = THREADS - 32;
+constexpr uint32_t TM_X = 192, TM_S = 0, TM_DP = 64, TM_P = 128, TM_DS = 160, TM_DV = 384, TM_DK = 448;
 
 enum : int {
     B_KVF = 0,             // [2] the item's K and V landed
     B_KVE = 2,             // [2] its S and dP products are done
     B_QF = 4,              // [NST] Q and dO landed
     B_ST = 4 + NST,        // [NST] lse and delta written, rows that must not take part zeroed
-    B_QE = 4 + 2 * NST,    // [NST] stage free (2 commits and 16 warps)
+    B_QE = 4 + 2 * NST,    // [NST] stage free (a commit and 16 warps)
     B_SF = 4 + 3 * NST,    // [2] S_X and dP_X in tensor memory
-    B_PF = B_SF + 2,       // [2] P_X and dS_X written in their place (8 warps)
-    B_AF = B_PF + 2,       // the item's dV and dK are complete (2 commits)
+    B_SR = B_SF + 2,       // [2] the group has read them (8 warps)
+    B_PF = B_SR + 2,       // [2] P_X and dS_X written (8 warps)
+    B_PV = B_PF + 2,       // [2] their products are done
+    B_AF = B_PV + 2,       // the item's dV and dK are complete
     B_AE = B_AF + 1,       // and read (16 warps)
     B_SLOT = B_AE + 1,
     B_BAD = 36,            // [NST] 16 bytes: bits of the stage's query rows that are not finite
@@ -123,7 +126,7 @@ struct Item {
     __device__ __forceinline__ int tiles() const { return (i1 - i0 + BT - 1) / BT; }
 };
 
-__global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_constant__ KvArgs p) {
+__global__ void __launch_bounds__(KV_THREADS, 1) window_dkv_kernel(const __grid_constant__ KvArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = smem_raw + (-tc::smem_u32(smem_raw) & 1023u);   // (an offset: the pointer stays known as shared)
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
@@ -135,19 +138,21 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
     const win::ItemQueue items{bars + B_IF, bars + B_IE, reinterpret_cast<volatile int*>(bars + B_ITEM), abort_flag};
 
     if (tid == 0) {
-        items.init(2 + 1 + SOFT);   // MMA issuers, side warps, softmax warps
+        items.init(1 + 1 + SOFT);   // MMA issuers, side warps, softmax warps
         for (int x = 0; x < 2; ++x) {
             tc::mbar_init(bars + B_KVF + x, 1);
-            tc::mbar_init(bars + B_KVE + x, 2);
+            tc::mbar_init(bars + B_KVE + x, 1);
             tc::mbar_init(bars + B_SF + x, 1);
+            tc::mbar_init(bars + B_SR + x, SOFT / 2);
             tc::mbar_init(bars + B_PF + x, SOFT / 2);
+            tc::mbar_init(bars + B_PV + x, 1);
         }
         for (int s = 0; s < NST; ++s) {
             tc::mbar_init(bars + B_QF + s, 1);
             tc::mbar_init(bars + B_ST + s, 1);
-            tc::mbar_init(bars + B_QE + s, 2 + SOFT);
+            tc::mbar_init(bars + B_QE + s, 1 + SOFT);
         }
-        tc::mbar_init(bars + B_AF, 2);
+        tc::mbar_init(bars + B_AF, 1);
         tc::mbar_init(bars + B_AE, SOFT);
         *abort_flag = 0;
         tc::fence_mbar_init();
@@ -209,15 +214,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
             }
             if (!ok) give_up();
         }
-    } else if (warp == SOFT + 1 || warp == SOFT + 2) {
-        // ---------------- MMA issuers, one per half of the queries, each with sums of its own (so that neither's
-        // order depends on the other): S and dP of a tile, then the products of P and dS, which the softmax has put
-        // in their place.  One half's products run while the other's scores are worked on.
-        const int X = warp - SOFT - 1;
+    } else if (warp == SOFT + 1) {
+        // ---------------- MMA issuer.  In turn: the scores of half 0 of the next tile, the products of half 1 of the
+        // tile before, the scores of half 1, the products of half 0: the order in which the two halves' softmax
+        // reaches them, half a tile apart, so that scores are always there and neither waits for products.
         if (tc::elect_one()) {
             constexpr uint32_t ID_S = tc::instr_desc(1, BT, HALF, 0, 0);   // both K-major
             constexpr uint32_t ID_A = tc::instr_desc(1, BT, DH, 0, 1);     // A in tensor memory, B MN-major
-            const uint32_t tX = tm + TM_X * X;
             int g = 0, n = 0;
             bool ok = true;
             for (int k = 0; ok; ++k) {
@@ -231,37 +234,52 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
                 const int kv = n & 1, steps = it.heads * it.tiles();
                 if (!tc::mbar_wait(bars + B_KVF + kv, (n >> 1) & 1, abort_flag)) { ok = false; break; }
                 const uint64_t dK = kmajor_desc(sm + OFF_KV + kv * 2 * TILE), dV = kmajor_desc(sm + OFF_KV + kv * 2 * TILE + TILE);
-                for (int t = 0; t < steps; ++t, ++g) {
-                    const int s = g % NST;
-                    if (!tc::mbar_wait(bars + B_QF + s, (g / NST) & 1, abort_flag)) { ok = false; break; }
+                auto scores = [&](int X, int t) {
+                    const int gt = g + t, s = gt % NST;
+                    if (X == 0 && !tc::mbar_wait(bars + B_QF + s, (gt / NST) & 1, abort_flag)) return false;
+                    if (gt > 0 && !tc::mbar_wait(bars + B_SR + X, (gt - 1) & 1, abort_flag)) return false;
                     tc::tc_fence_after();
-                    const uint8_t *qt = sm + OFF_Q + s * 2 * TILE + X * (TILE / 2), *ot = qt + TILE;
-                    const uint64_t dQ = kmajor_desc(qt), dO = kmajor_desc(ot);
+                    const uint8_t* qt = sm + OFF_Q + s * 2 * TILE + X * (TILE / 2);
+                    const uint64_t dQ = kmajor_desc(qt), dO = kmajor_desc(qt + TILE);
 #pragma unroll
-                    for (int kk = 0; kk < DH / 16; ++kk) tc::mma_f16_ss(tX + TM_S, dK + 2 * kk, dQ + 2 * kk, ID_S, kk > 0);
+                    for (int kk = 0; kk < DH / 16; ++kk) tc::mma_f16_ss(tm + TM_X * X + TM_S, dK + 2 * kk, dQ + 2 * kk, ID_S, kk > 0);
 #pragma unroll
-                    for (int kk = 0; kk < DH / 16; ++kk) tc::mma_f16_ss(tX + TM_DP, dV + 2 * kk, dO + 2 * kk, ID_S, kk > 0);
+                    for (int kk = 0; kk < DH / 16; ++kk) tc::mma_f16_ss(tm + TM_X * X + TM_DP, dV + 2 * kk, dO + 2 * kk, ID_S, kk > 0);
                     tc::mma_commit(bars + B_SF + X);
-                    if (t == steps - 1) tc::mma_commit(bars + B_KVE + kv);
-                    // the item before has left the sums
-                    if (t == 0 && n > 0 && !tc::mbar_wait(bars + B_AE, (n - 1) & 1, abort_flag)) { ok = false; break; }
-                    if (!tc::mbar_wait(bars + B_PF + X, g & 1, abort_flag)) { ok = false; break; }
+                    if (X == 1 && t == steps - 1) tc::mma_commit(bars + B_KVE + kv);
+                    return true;
+                };
+                auto products = [&](int X, int t) {
+                    const int gt = g + t, s = gt % NST;
+                    if (!tc::mbar_wait(bars + B_PF + X, gt & 1, abort_flag)) return false;
                     tc::tc_fence_after();
-                    const uint64_t mQ = mnmajor_desc(qt), mO = mnmajor_desc(ot);
-#pragma unroll
-                    for (int kk = 0; kk < HALF / 16; ++kk)   // 16 queries: 8 columns, 32 queries' columns begin 32 apart
-                        tc::mma_f16_ts(tX + TM_DV, tX + TM_S + 8 * kk + 16 * (kk / 2), mO + (uint64_t)(kk * 128), ID_A, t > 0 || kk > 0);
+                    const uint8_t* qt = sm + OFF_Q + s * 2 * TILE + X * (TILE / 2);
+                    const uint64_t mQ = mnmajor_desc(qt), mO = mnmajor_desc(qt + TILE);
+                    const uint32_t more = t > 0 || X > 0;
 #pragma unroll
                     for (int kk = 0; kk < HALF / 16; ++kk)
-                        tc::mma_f16_ts(tX + TM_DK, tX + TM_DP + 8 * kk + 16 * (kk / 2), mQ + (uint64_t)(kk * 128), ID_A, t > 0 || kk > 0);
-                    tc::mma_commit(bars + B_QE + s);
-                }
+                        tc::mma_f16_ts(tm + TM_DV, tm + TM_X * X + TM_P + 8 * kk, mO + (uint64_t)(kk * 128), ID_A, more | (kk > 0));
+#pragma unroll
+                    for (int kk = 0; kk < HALF / 16; ++kk)
+                        tc::mma_f16_ts(tm + TM_DK, tm + TM_X * X + TM_DS + 8 * kk, mQ + (uint64_t)(kk * 128), ID_A, more | (kk > 0));
+                    tc::mma_commit(bars + B_PV + X);
+                    if (X == 1) tc::mma_commit(bars + B_QE + s);
+                    return true;
+                };
+                ok = scores(0, 0) && scores(1, 0);
+                // the item before has left the sums
+                if (ok && n > 0) ok = tc::mbar_wait(bars + B_AE, (n - 1) & 1, abort_flag);
+                for (int t = 0; t < steps && ok; ++t)
+                    ok = (t + 1 == steps || scores(0, t + 1)) && (t == 0 || products(1, t - 1)) &&
+                         (t + 1 == steps || scores(1, t + 1)) && products(0, t);
+                ok = ok && products(1, steps - 1);
                 if (ok) tc::mma_commit(bars + B_AF);
+                g += steps;
                 ++n;
             }
             if (!ok) give_up();
         }
-    } else if (warp > SOFT) {
+    } else if (warp == SOFT + 2) {
         // ---------------- lse and delta of the tile's rows; rows of Q and dO that are not finite (delta says so), or
         // behind the sequence's last query, are zeroed
         int g = 0;
@@ -311,7 +329,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
             }
         }
         if (!ok && lane == 0) give_up();
-    } else {
+    } else if (warp < SOFT) {
         // ---------------- softmax groups: thread = key r of the block, queries 64 X + 32 y ... + 31 of each tile
         const int X = warp / (SOFT / 2), y = (warp >> 2) & 1, qd = warp & 3, r = 32 * qd + lane;
         const uint32_t lanes = (uint32_t)(32 * qd) << 16, tX = tm + lanes + TM_X * X;
@@ -328,9 +346,17 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
             const int tiles = it.tiles(), steps = it.heads * tiles, u = it.u0 + r;
             // queries (as indices) that see key u, cut to the item's
             const int lo_i = max(u - p.w.right - it.first, it.i0), hi_i = u < p.w.sinks ? it.i1 : min(u + p.w.left + 1 - it.first, it.i1);
-            for (int t = 0; t < steps; ++t, ++g) {
+            int lo = 0, hi = 0;   // of the part's first query
+            for (int t = 0, ti = 0; t < steps; ++t, ++g) {
                 const int s = g % NST, use = g / NST;
-                const int base = it.i0 + (t % tiles) * BT + HALF * X + COLS * y, lo = lo_i - base, hi = hi_i - base;
+                if (ti == 0) {
+                    lo = lo_i - it.i0 - HALF * X - COLS * y;
+                    hi = hi_i - it.i0 - HALF * X - COLS * y;
+                } else {
+                    lo -= BT;
+                    hi -= BT;
+                }
+                if (++ti == tiles) ti = 0;
                 const bool whole = __all_sync(0xffffffffu, lo <= 0 && hi >= COLS);
                 const uint32_t vis = win::low_bits(hi) & ~win::low_bits(lo);
                 if (!wait_all(bars + B_ST + s, use & 1) || !wait_all(bars + B_SF + X, g & 1)) { ok = false; break; }
@@ -340,6 +366,9 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
                 tc::tmem_ld_32x32b_x32(tX + TM_S + COLS * y, sc);
                 tc::tmem_ld_32x32b_x32(tX + TM_DP + COLS * y, dp);
                 tc::tmem_wait_ld();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bars + B_SR + X);
                 const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(sm + OFF_STAT + s * 1024) + HALF / 4 * X + COLS / 4 * y;
                 auto neg = [&](int k4, uint64_t& l0, uint64_t& l1, uint64_t& d0, uint64_t& d1) {
                     const ulonglong2 l = nl[k4], d = nl[BT / 4 + k4];
@@ -352,8 +381,12 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
                 else grad_scores<false, true>(sc, dp, c, vis, bad, neg);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bars + B_QE + s);   // the statistics have been read
-                tc::tmem_st_32x32b_x16(tX + TM_S + COLS * y, *reinterpret_cast<uint32_t(*)[16]>(sc));
-                tc::tmem_st_32x32b_x16(tX + TM_DP + COLS * y, *reinterpret_cast<uint32_t(*)[16]>(dp));
+                if (g > 0) {
+                    if (!wait_all(bars + B_PV + X, (g - 1) & 1)) { ok = false; break; }
+                    tc::tc_fence_after();
+                }
+                tc::tmem_st_32x32b_x16(tX + TM_P + COLS / 2 * y, *reinterpret_cast<uint32_t(*)[16]>(sc));
+                tc::tmem_st_32x32b_x16(tX + TM_DS + COLS / 2 * y, *reinterpret_cast<uint32_t(*)[16]>(dp));
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 __syncwarp();
@@ -366,12 +399,9 @@ __global__ void __launch_bounds__(THREADS, 1) window_dkv_kernel(const __grid_con
                 tc::tc_fence_after();
                 ++n;
             }
-            uint32_t o[COLS], o1[COLS];
+            uint32_t o[COLS];
             tc::tmem_ld_32x32b_x32(tm + lanes + (X ? TM_DK : TM_DV) + COLS * y, o);
-            tc::tmem_ld_32x32b_x32(tm + lanes + TM_X + (X ? TM_DK : TM_DV) + COLS * y, o1);
             tc::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < COLS; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) + __uint_as_float(o1[e]));
             if (steps > 0) {
                 tc::tc_fence_before();
                 __syncwarp();
@@ -464,7 +494,7 @@ cudaError_t launch_window_dkv(const WindowArgs& a, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     {
         LaunchScope scope("window_dkv", s);
-        window_dkv_kernel<<<(unsigned)(p.n_items < sms ? p.n_items : sms), THREADS, SMEM_BYTES, s>>>(p);
+        window_dkv_kernel<<<(unsigned)(p.n_items < sms ? p.n_items : sms), KV_THREADS, SMEM_BYTES, s>>>(p);
     }
     if (p.cut) {
         LaunchScope scope("window_sink_sum", s);
