@@ -43,7 +43,7 @@ constexpr int OFF_ML = OFF_BAR + 512;             // [2][2][128] float2: a row's
 constexpr int SMEM_BYTES = OFF_ML + 4096 + 1024;
 constexpr uint32_t TM_X = 256, TM_O = 128;        // tile X's S at TM_X X + 64 y, its O at TM_X X + TM_O + 64 y
 constexpr float kLazy = 8.0f;                     // log2 of the largest unscaled exponential
-constexpr int EMU = 1;                            // pairs of every 8 whose 2^x runs on the FMA pipe
+constexpr int EMU = 2;                            // pairs of every 8 whose 2^x runs on the FMA pipe
 
 // Barrier slots (8 bytes each) from OFF_BAR.
 enum : int {

@@ -562,8 +562,8 @@ def _ask(ok: bool, what: str) -> None:
 
 def _rows(x, shape, dtype, device, name) -> int:
     """Row stride of a tensor of `shape` whose rows are dense (checked with its type and device)."""
-    if x.dtype is not dtype or x.device != device:
-        raise ValueError(f"{name}: {x.dtype} on {x.device}, wanted {dtype} on {device}")
+    if x.dtype is not dtype or x.get_device() != device:
+        raise ValueError(f"{name}: {x.dtype} on {x.device}, wanted {dtype} on GPU {device}")
     if x.shape != shape:
         raise ValueError(f"{name}: shape {tuple(x.shape)}, wanted {tuple(shape)}")
     strides = x.stride()
@@ -581,24 +581,26 @@ def _rows(x, shape, dtype, device, name) -> int:
 def _offsets(cu, device, name):
     if cu is None:
         return 1
-    if not (cu.dtype is torch.int32 and cu.device == device and cu.dim() == 1 and cu.numel() >= 2 and cu.is_contiguous()):
-        raise ValueError(f"{name}: a dense int32 vector of n_seq + 1 offsets on {device} is wanted")
+    if not (cu.dtype is torch.int32 and cu.get_device() == device and cu.dim() == 1 and cu.numel() >= 2 and cu.is_contiguous()):
+        raise ValueError(f"{name}: a dense int32 vector of n_seq + 1 offsets on GPU {device} is wanted")
     return cu.numel() - 1
 
 
 def _dense(x, shape, dtype, device, name):
-    if not (x.dtype is dtype and x.device == device and x.shape == shape and x.is_contiguous()):
-        raise ValueError(f"{name}: a dense {dtype} tensor of shape {tuple(shape)} on {device} is wanted")
+    if not (x.dtype is dtype and x.get_device() == device and x.shape == shape and x.is_contiguous()):
+        raise ValueError(f"{name}: a dense {dtype} tensor of shape {tuple(shape)} on GPU {device} is wanted")
     return x
 
 
-def _space(workspace, n, device):
-    if n == 0:
-        raise TTTError(TTT_ERR_INVALID_ARG, "workspace size")
+def _space(workspace, size, device):
+    """The given workspace (the call checks its size), or a new one of size() bytes."""
     if workspace is None:
+        n = size()
+        if n == 0:
+            raise TTTError(TTT_ERR_INVALID_ARG, "workspace size")
         return torch.empty(n, dtype=torch.uint8, device=device)
-    if workspace.device != device:
-        raise ValueError(f"workspace on {workspace.device}, wanted {device}")
+    if workspace.get_device() != device:
+        raise ValueError(f"workspace on {workspace.device}, wanted GPU {device}")
     return workspace
 
 
@@ -609,17 +611,27 @@ def _dtype_code(x, name) -> int:
 
 
 _ROPE_KEYS = {"kind", "factor", "length", "low", "high", "amplitude"}
-# descriptors by their sizes: building one costs as much as a launch
+# Descriptors by their sizes, with a reference for the call: building one costs as much as a launch.
+def _descriptor(_type, *args):
+    desc = _type(*args)
+    desc.ref = ctypes.byref(desc)
+    return desc
+
+
 _rope_desc, _window_sizes, _decode_sizes, _gated_sizes = (
-    functools.lru_cache(maxsize=256)(lambda *args, _type=c: _type(*args))
+    functools.lru_cache(maxsize=256)(functools.partial(_descriptor, c))
     for c in (ttt_rope_desc, ttt_window_desc, ttt_window_decode_desc, ttt_gated_scan_desc))
+
+
+def _at(x):
+    return None if x is None else x.data_ptr()
 
 
 def rope(x, positions=None, *, pos0: int = 0, rot: int | None = None, layout: str = "half", base: float = 10000.0,
          scaling: dict | None = None, inverse: bool = False, out=None, stream=None):
     """Rotary positions of x [T, H, d] (ttt_rope).  `scaling`: {"kind": "linear" | "base", "factor": f} or
     {"kind": "ramp", "factor": f, "length": n, "low": l, "high": h}, with "amplitude" optional.  `out` may be x."""
-    code, shape, dev = _dtype_code(x, "x"), x.shape, x.device
+    code, shape, dev = _dtype_code(x, "x"), x.shape, x.get_device()
     T, H, d = shape
     sc = scaling or {}
     if not (_ROPE_KEYS >= sc.keys() and sc.get("kind", "none") in TTT_ROPE_SCALINGS):
@@ -632,8 +644,9 @@ def rope(x, positions=None, *, pos0: int = 0, rot: int | None = None, layout: st
     with _Place(x, stream):
         if out is None:
             out = torch.empty(shape, dtype=x.dtype, device=dev)
-        check(ttt_rope(desc, x, _rows(x, shape, x.dtype, dev, "x"), out, _rows(out, shape, x.dtype, dev, "out"),
-                       positions, pos0, inverse, stream), "ttt_rope")
+        check(lib().ttt_rope(desc.ref, x.data_ptr(), _rows(x, shape, x.dtype, dev, "x"), out.data_ptr(),
+                             _rows(out, shape, x.dtype, dev, "out"), _at(positions), pos0, int(inverse), _stream(stream)),
+              "ttt_rope")
     return out
 
 
@@ -646,22 +659,22 @@ def _window_desc(q, k, n_seq, left, right, sinks, scale):
 def window_attention_workspace(q, k, n_seq: int = 1, backward: bool = False) -> torch.Tensor:
     """A workspace that window_attention (and, with backward, window_attention_backward) can use."""
     desc = _window_desc(q, k, n_seq, 0, 0, 0, None)
-    n = (ttt_window_attention_backward_workspace_size if backward else ttt_window_attention_workspace_size)(desc)
-    return _space(None, n, q.device)
+    size = ttt_window_attention_backward_workspace_size if backward else ttt_window_attention_workspace_size
+    return _space(None, lambda: size(desc), q.get_device())
 
 
 def window_attention(q, k, v, *, left: int, right: int = 0, sinks: int = 0, cu_q=None, cu_k=None, scale=None,
                      residual=None, out=None, lse=None, want_lse: bool = False, workspace=None,
                      check_status: bool = True, stream=None) -> dict:
     """Window attention of q [Tq, Hq, 64] on k, v [Tk, Hk, 64] (ttt_window_attention)."""
-    dev, bf = q.device, torch.bfloat16
+    dev, bf = q.get_device(), torch.bfloat16
     n_seq = _offsets(cu_q, dev, "cu_q")
     _ask((cu_q is None) == (cu_k is None) and _offsets(cu_k, dev, "cu_k") == n_seq,
          "cu_q and cu_k: both or neither, of the same length")
     desc = _window_desc(q, k, n_seq, left, right, sinks, scale)
     lds = [_rows(q, q.shape, bf, dev, "q"), _rows(k, k.shape, bf, dev, "k"), _rows(v, k.shape, bf, dev, "v")]
     with _Place(q, stream):
-        ws = _space(workspace, ttt_window_attention_workspace_size(desc), dev)
+        ws = _space(workspace, lambda: ttt_window_attention_workspace_size(desc), dev)
         if out is None:   # rows outside the sequences are not written: they start as zeros
             out = (torch.empty if cu_q is None else torch.zeros)(q.shape, dtype=bf, device=dev)
         if lse is None and want_lse:
@@ -671,8 +684,9 @@ def window_attention(q, k, v, *, left: int, right: int = 0, sinks: int = 0, cu_q
         ld_out = _rows(out, q.shape, bf, dev, "out")
         if residual is not None:
             _ask(_rows(residual, q.shape, bf, dev, "residual") == ld_out, "residual and out need the same row stride")
-        check(ttt_window_attention(desc, cu_q, cu_k, q, lds[0], k, lds[1], v, lds[2], residual, out, ld_out, lse, ws,
-                                   ws.numel(), stream), "ttt_window_attention")
+        check(lib().ttt_window_attention(desc.ref, _at(cu_q), _at(cu_k), q.data_ptr(), lds[0], k.data_ptr(), lds[1],
+                                         v.data_ptr(), lds[2], _at(residual), out.data_ptr(), ld_out, _at(lse),
+                                         ws.data_ptr(), ws.numel(), _stream(stream)), "ttt_window_attention")
         if check_status:
             check(ttt_mlp_status(ws, stream), "ttt_mlp_status")
     return {"out": out, "lse": lse, "workspace": ws}
@@ -682,23 +696,25 @@ def window_attention_backward(q, k, v, out, lse, dout, *, left: int, right: int 
                               cu_k=None, scale=None, dq=None, dk=None, dv=None, workspace=None,
                               check_status: bool = True, stream=None) -> dict:
     """Gradients of window_attention (without a residual) from its out and lse (ttt_window_attention_backward)."""
-    dev, bf = q.device, torch.bfloat16
+    dev, bf = q.get_device(), torch.bfloat16
     n_seq = _offsets(cu_q, dev, "cu_q")
     _ask((cu_q is None) == (cu_k is None) and _offsets(cu_k, dev, "cu_k") == n_seq,
          "cu_q and cu_k: both or neither, of the same length")
     desc = _window_desc(q, k, n_seq, left, right, sinks, scale)
     _dense(lse, (q.shape[1], q.shape[0]), torch.float32, dev, "lse")
     with _Place(q, stream):
-        ws = _space(workspace, ttt_window_attention_backward_workspace_size(desc), dev)
+        ws = _space(workspace, lambda: ttt_window_attention_backward_workspace_size(desc), dev)
         new = torch.empty if cu_q is None else torch.zeros
         dq = new(q.shape, dtype=bf, device=dev) if dq is None else dq
         dk = new(k.shape, dtype=bf, device=dev) if dk is None else dk
         dv = new(k.shape, dtype=bf, device=dev) if dv is None else dv
-        ld = {n: _rows(t, (q if n in ("q", "out", "dout", "dq") else k).shape, bf, dev, n)
-              for n, t in dict(q=q, k=k, v=v, out=out, dout=dout, dq=dq, dk=dk, dv=dv).items()}
-        check(ttt_window_attention_backward(desc, cu_q, cu_k, q, ld["q"], k, ld["k"], v, ld["v"], out, ld["out"], lse,
-                                            dout, ld["dout"], dq, ld["dq"], dk, ld["dk"], dv, ld["dv"], ws,
-                                            ws.numel(), stream), "ttt_window_attention_backward")
+        sq, sk = q.shape, k.shape
+        check(lib().ttt_window_attention_backward(
+            desc.ref, _at(cu_q), _at(cu_k), q.data_ptr(), _rows(q, sq, bf, dev, "q"), k.data_ptr(),
+            _rows(k, sk, bf, dev, "k"), v.data_ptr(), _rows(v, sk, bf, dev, "v"), out.data_ptr(),
+            _rows(out, sq, bf, dev, "out"), lse.data_ptr(), dout.data_ptr(), _rows(dout, sq, bf, dev, "dout"),
+            dq.data_ptr(), _rows(dq, sq, bf, dev, "dq"), dk.data_ptr(), _rows(dk, sk, bf, dev, "dk"), dv.data_ptr(),
+            _rows(dv, sk, bf, dev, "dv"), ws.data_ptr(), ws.numel(), _stream(stream)), "ttt_window_attention_backward")
         if check_status:
             check(ttt_mlp_status(ws, stream), "ttt_mlp_status")
     return {"dq": dq, "dk": dk, "dv": dv, "workspace": ws}
@@ -716,8 +732,8 @@ def _decode_desc(q, cache, left, sinks, scale):
 
 def window_attention_decode_workspace(q, cache) -> torch.Tensor:
     """A zeroed workspace for window_attention_decode."""
-    n = ttt_window_attention_decode_workspace_size(_decode_desc(q, cache, 0, 0, None))
-    return _space(None, n, q.device).zero_()
+    desc = _decode_desc(q, cache, 0, 0, None)
+    return _space(None, lambda: ttt_window_attention_decode_workspace_size(desc), q.get_device()).zero_()
 
 
 def window_attention_decode(q, cache_k, cache_v, lens, *, left: int, sinks: int = 0, scale=None, k_new=None,
@@ -725,11 +741,11 @@ def window_attention_decode(q, cache_k, cache_v, lens, *, left: int, sinks: int 
     """One token of each request on its cache (ttt_window_attention_decode): q [B, Hq, 64], caches
     [B, slots, Hk, 64] with any strides, lens int32 [B]; k_new, v_new [B, Hk, 64] are stored first.
     A given workspace must have been zeroed once (window_attention_decode_workspace)."""
-    dev, bf = q.device, torch.bfloat16
+    dev, bf = q.get_device(), torch.bfloat16
     desc = _decode_desc(q, cache_k, left, sinks, scale)
-    if not (cache_k.dtype is bf and cache_v.dtype is bf and cache_k.device == dev and cache_v.device == dev and
+    if not (cache_k.dtype is bf and cache_v.dtype is bf and cache_k.get_device() == dev and cache_v.get_device() == dev and
             cache_k.shape == cache_v.shape and cache_k.stride() == cache_v.stride()):
-        raise ValueError(f"the caches: bfloat16 on {dev}, of the same shape and strides")
+        raise ValueError(f"the caches: bfloat16 on GPU {dev}, of the same shape and strides")
     _dense(lens, (q.shape[0],), torch.int32, dev, "lens")
     ld_q = _rows(q, q.shape, bf, dev, "q")
     ld_new = 0
@@ -740,12 +756,13 @@ def window_attention_decode(q, cache_k, cache_v, lens, *, left: int, sinks: int 
         _ask(_rows(v_new, shape, bf, dev, "v_new") == ld_new, "k_new and v_new need the same row stride")
     with _Place(q, stream):
         if workspace is None:
-            workspace = _space(None, ttt_window_attention_decode_workspace_size(desc), dev).zero_()
+            workspace = _space(None, lambda: ttt_window_attention_decode_workspace_size(desc), dev).zero_()
         if out is None:
             out = torch.empty(q.shape, dtype=bf, device=dev)
-        check(ttt_window_attention_decode(desc, q, ld_q, k_new, v_new, ld_new, cache_k, cache_v, lens, out,
-                                          _rows(out, q.shape, bf, dev, "out"), workspace, workspace.numel(), stream),
-              "ttt_window_attention_decode")
+        check(lib().ttt_window_attention_decode(
+            desc.ref, q.data_ptr(), ld_q, _at(k_new), _at(v_new), ld_new, cache_k.data_ptr(), cache_v.data_ptr(),
+            lens.data_ptr(), out.data_ptr(), _rows(out, q.shape, bf, dev, "out"), workspace.data_ptr(),
+            workspace.numel(), _stream(stream)), "ttt_window_attention_decode")
         if check_status:
             check(ttt_mlp_status(workspace, stream), "ttt_mlp_status")
     return {"out": out, "workspace": workspace}
@@ -759,34 +776,36 @@ def _gated_desc(x, n_seq, form, dirs):
 
 def gated_scan_workspace(x, n_seq: int = 1) -> torch.Tensor:
     """A workspace for gated_scan and gated_scan_backward on tensors of x's shape and type."""
-    return _space(None, ttt_gated_scan_workspace_size(_gated_desc(x, n_seq, "sum", "fwd")), x.device)
+    desc = _gated_desc(x, n_seq, "sum", "fwd")
+    return _space(None, lambda: ttt_gated_scan_workspace_size(desc), x.get_device())
 
 
 def gated_scan(f, x, *, form: str = "convex", dirs: str = "fwd", cu=None, h0=None, y=None, h_T=None,
                want_state: bool = False, want_chunk_states: bool = False, chunk_states=None, workspace=None,
                check_status: bool = True, stream=None) -> dict:
     """Gated linear recurrence of the gate logits f and inputs x [T, D] (ttt_gated_scan)."""
-    dev, n_seq = x.device, _offsets(cu, x.device, "cu")
+    dev = x.get_device()
+    n_seq = _offsets(cu, dev, "cu")
     desc = _gated_desc(x, n_seq, form, dirs)
     ld_f, ld_x = _rows(f, x.shape, x.dtype, dev, "f"), _rows(x, x.shape, x.dtype, dev, "x")
     state = (n_seq, x.shape[1])
     if h0 is not None:
         _dense(h0, state, torch.float32, dev, "h0")
     with _Place(x, stream):
-        ws = _space(workspace, ttt_gated_scan_workspace_size(desc), dev)
+        ws = _space(workspace, lambda: ttt_gated_scan_workspace_size(desc), dev)
         if y is None:
             y = (torch.empty if cu is None else torch.zeros)(x.shape, dtype=x.dtype, device=dev)
         if h_T is None and want_state:
             h_T = torch.empty(state, device=dev)
         if h_T is not None:
             _dense(h_T, state, torch.float32, dev, "h_T")
-        n = ttt_gated_scan_chunk_states_size(desc)
-        if chunk_states is None and want_chunk_states:
-            chunk_states = torch.empty(n // 4, device=dev)
         if chunk_states is not None:
-            _dense(chunk_states, (n // 4,), torch.float32, dev, "chunk_states")
-        check(ttt_gated_scan(desc, cu, f, ld_f, x, ld_x, h0, y, _rows(y, x.shape, x.dtype, dev, "y"), h_T,
-                             chunk_states, ws, ws.numel(), stream), "ttt_gated_scan")
+            _dense(chunk_states, (ttt_gated_scan_chunk_states_size(desc) // 4,), torch.float32, dev, "chunk_states")
+        elif want_chunk_states:
+            chunk_states = torch.empty(ttt_gated_scan_chunk_states_size(desc) // 4, device=dev)
+        check(lib().ttt_gated_scan(desc.ref, _at(cu), f.data_ptr(), ld_f, x.data_ptr(), ld_x, _at(h0), y.data_ptr(),
+                                   _rows(y, x.shape, x.dtype, dev, "y"), _at(h_T), _at(chunk_states), ws.data_ptr(),
+                                   ws.numel(), _stream(stream)), "ttt_gated_scan")
         if check_status:
             check(ttt_mlp_status(ws, stream), "ttt_mlp_status")
     return {"y": y, "h_T": h_T, "chunk_states": chunk_states, "workspace": ws}
@@ -796,7 +815,8 @@ def gated_scan_backward(f, x, dy, chunk_states, *, form: str = "convex", dirs: s
                         dh_T=None, df=None, dx=None, dh0=None, want_dh0: bool = False, workspace=None,
                         check_status: bool = True, stream=None) -> dict:
     """Gradients of gated_scan from its inputs and chunk states (ttt_gated_scan_backward)."""
-    dev, n_seq = x.device, _offsets(cu, x.device, "cu")
+    dev = x.get_device()
+    n_seq = _offsets(cu, dev, "cu")
     desc = _gated_desc(x, n_seq, form, dirs)
     state = (n_seq, x.shape[1])
     _dense(chunk_states, (ttt_gated_scan_chunk_states_size(desc) // 4,), torch.float32, dev, "chunk_states")
@@ -804,7 +824,7 @@ def gated_scan_backward(f, x, dy, chunk_states, *, form: str = "convex", dirs: s
         if t is not None:
             _dense(t, state, torch.float32, dev, name)
     with _Place(x, stream):
-        ws = _space(workspace, ttt_gated_scan_workspace_size(desc), dev)
+        ws = _space(workspace, lambda: ttt_gated_scan_workspace_size(desc), dev)
         new = torch.empty if cu is None else torch.zeros
         df = new(x.shape, dtype=x.dtype, device=dev) if df is None else df
         dx = new(x.shape, dtype=x.dtype, device=dev) if dx is None else dx
@@ -812,10 +832,12 @@ def gated_scan_backward(f, x, dy, chunk_states, *, form: str = "convex", dirs: s
             dh0 = torch.empty(state, device=dev)
         if dh0 is not None:
             _dense(dh0, state, torch.float32, dev, "dh0")
-        ld = {n: _rows(t, x.shape, x.dtype, dev, n) for n, t in dict(f=f, x=x, dy=dy, df=df, dx=dx).items()}
-        check(ttt_gated_scan_backward(desc, cu, f, ld["f"], x, ld["x"], h0, chunk_states, dy, ld["dy"], dh_T, df,
-                                      ld["df"], dx, ld["dx"], dh0, ws, ws.numel(), stream),
-              "ttt_gated_scan_backward")
+        dt, sx = x.dtype, x.shape
+        check(lib().ttt_gated_scan_backward(
+            desc.ref, _at(cu), f.data_ptr(), _rows(f, sx, dt, dev, "f"), x.data_ptr(), _rows(x, sx, dt, dev, "x"),
+            _at(h0), chunk_states.data_ptr(), dy.data_ptr(), _rows(dy, sx, dt, dev, "dy"), _at(dh_T), df.data_ptr(),
+            _rows(df, sx, dt, dev, "df"), dx.data_ptr(), _rows(dx, sx, dt, dev, "dx"), _at(dh0), ws.data_ptr(),
+            ws.numel(), _stream(stream)), "ttt_gated_scan_backward")
         if check_status:
             check(ttt_mlp_status(ws, stream), "ttt_mlp_status")
     return {"df": df, "dx": dx, "dh0": dh0, "workspace": ws}
@@ -823,13 +845,14 @@ def gated_scan_backward(f, x, dy, chunk_states, *, form: str = "convex", dirs: s
 
 def gated_scan_step(f, x, h, *, form: str = "convex", y=None, h_out=None, stream=None):
     """One token of each row: returns (y, h_out) for f, x [B, D] and the state h fp32 [B, D] (h_out may be h)."""
-    dev, code = x.device, _dtype_code(x, "x")
+    dev, code = x.get_device(), _dtype_code(x, "x")
     B, D = x.shape
     _dense(h, (B, D), torch.float32, dev, "h")
     with _Place(x, stream):
         y = torch.empty((B, D), dtype=x.dtype, device=dev) if y is None else y
         h_out = torch.empty_like(h) if h_out is None else _dense(h_out, (B, D), torch.float32, dev, "h_out")
-        check(ttt_gated_scan_step(B, D, TTT_GATE_FORMS[form], code, f, _rows(f, x.shape, x.dtype, dev, "f"), x,
-                                  _rows(x, x.shape, x.dtype, dev, "x"), h, h_out, y,
-                                  _rows(y, x.shape, x.dtype, dev, "y"), stream), "ttt_gated_scan_step")
+        check(lib().ttt_gated_scan_step(
+            B, D, TTT_GATE_FORMS[form], code, f.data_ptr(), _rows(f, x.shape, x.dtype, dev, "f"), x.data_ptr(),
+            _rows(x, x.shape, x.dtype, dev, "x"), h.data_ptr(), h_out.data_ptr(), y.data_ptr(),
+            _rows(y, x.shape, x.dtype, dev, "y"), _stream(stream)), "ttt_gated_scan_step")
     return y, h_out
