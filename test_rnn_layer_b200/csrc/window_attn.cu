@@ -43,7 +43,7 @@ constexpr int OFF_ML = OFF_BAR + 512;             // [2][2][128] float2: a row's
 constexpr int SMEM_BYTES = OFF_ML + 4096 + 1024;
 constexpr uint32_t TM_X = 256, TM_O = 128;        // tile X's S at TM_X X + 64 y, its O at TM_X X + TM_O + 64 y
 constexpr float kLazy = 8.0f;                     // log2 of the largest unscaled exponential
-constexpr int EMU = 2;                            // pairs of every 8 whose 2^x runs on the FMA pipe
+constexpr int EMU = 1;                            // pairs of every 8 whose 2^x runs on the FMA pipe
 
 // Barrier slots (8 bytes each) from OFF_BAR.
 enum : int {
@@ -148,7 +148,7 @@ __device__ __forceinline__ float softmax_tile(uint32_t (&s)[NC], float c, RowSta
         const uint64_t x = f2_fma(f2(__uint_as_float(s[2 * k2]), __uint_as_float(s[2 * k2 + 1])), c2, nm2);
         float p0, p1;
         if ((k2 & 7) >= 8 - EMU) {
-            ex2_poly2(x, p0, p1);
+            ex2_poly2_fine(x, p0, p1);   // (a cubic's 7.6e-5 would show in the log-sum-exp of a few keys)
         } else {
             float x0, x1;
             f2_split(x, x0, x1);
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
                 next = gridDim.x + atomicAdd(p.w.status + kTicket, 1);
                 if (!it.load(p.w, w)) continue;
                 if (!items.put(k++, w)) { ok = false; break; }
-                if (n > 0 && !tc::mbar_wait(bars + B_QE, (n - 1) & 1, abort_flag)) { ok = false; break; }
+                if (n > 0 && !tc::mbar_wait(bars + B_QE, (n - 1) & 1, abort_flag, win::kItemWait)) { ok = false; break; }
                 ++n;
                 const int xq = it.h * DH, xk = it.hk * DH;
                 tc::mbar_arrive_expect_tx(bars + B_QF, 2 * TILE);
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
                 it.load(p.w, w);
                 int a, b;
                 it.range(p.w, X, a, b);
-                if (!tc::mbar_wait(bars + B_QF, n & 1, abort_flag)) { ok = false; break; }
+                if (!tc::mbar_wait(bars + B_QF, n & 1, abort_flag, win::kItemWait)) { ok = false; break; }
                 ++n;
                 tc::tc_fence_after();
                 int pending[2] = {-1, -1};   // the stage whose P V is to come

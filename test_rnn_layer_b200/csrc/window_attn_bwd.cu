@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
                 next = gridDim.x + atomicAdd(p.w.status + kTicket, 1);
                 if (!it.load(p.w, w)) continue;
                 if (!items.put(k++, w)) { ok = false; break; }
-                if (n > 0 && !tc::mbar_wait(bars + B_QE, (n - 1) & 1, abort_flag)) { ok = false; break; }
+                if (n > 0 && !tc::mbar_wait(bars + B_QE, (n - 1) & 1, abort_flag, win::kItemWait)) { ok = false; break; }
                 ++n;
                 const int xq = it.h * DH, xk = it.hk * DH;
                 // tile B past the last row: tile A's rows again (its results are never stored)
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
                 it.load(p.w, w);
                 int a, b;
                 it.range(p.w, X, a, b);
-                if (!tc::mbar_wait(bars + B_QF, n & 1, abort_flag)) { ok = false; break; }
+                if (!tc::mbar_wait(bars + B_QF, n & 1, abort_flag, win::kItemWait)) { ok = false; break; }
                 ++n;
                 tc::tc_fence_after();
                 int done = 0, ps = -1, ph = 0;

@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(KV_THREADS, 1) window_dkv_kernel(const __grid_
                 if (!items.put(k++, w)) { ok = false; break; }
                 if (it.tiles() == 0) continue;
                 const int kv = n & 1, xk = it.hk * DH, tiles = it.tiles();
-                if (n >= 2 && !tc::mbar_wait(bars + B_KVE + kv, ((n >> 1) - 1) & 1, abort_flag)) { ok = false; break; }
+                if (n >= 2 && !tc::mbar_wait(bars + B_KVE + kv, ((n >> 1) - 1) & 1, abort_flag, win::kItemWait)) { ok = false; break; }
                 uint8_t* kt = sm + OFF_KV + kv * 2 * TILE;
                 tc::mbar_arrive_expect_tx(bars + B_KVF + kv, 2 * TILE);
                 tc::tma_load_2d(kt, &p.mapK, xk, it.k_lo, bars + B_KVF + kv);
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(KV_THREADS, 1) window_dkv_kernel(const __grid_
                 it.load(p, w);
                 if (it.tiles() == 0) continue;
                 const int kv = n & 1, steps = it.heads * it.tiles();
-                if (!tc::mbar_wait(bars + B_KVF + kv, (n >> 1) & 1, abort_flag)) { ok = false; break; }
+                if (!tc::mbar_wait(bars + B_KVF + kv, (n >> 1) & 1, abort_flag, win::kItemWait)) { ok = false; break; }
                 const uint64_t dK = kmajor_desc(sm + OFF_KV + kv * 2 * TILE), dV = kmajor_desc(sm + OFF_KV + kv * 2 * TILE + TILE);
                 auto scores = [&](int X, int t) {
                     const int gt = g + t, s = gt % NST;

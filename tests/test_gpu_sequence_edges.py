@@ -1,0 +1,273 @@
+"""The sequence operators where their kernels' tiles, strips, chunks and shares end, and what must not reach from
+one row, sequence, call or stream into another.  Bounds as in oracle/sequence_ops.py."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import sequence_ops as S
+from test_rnn_layer_b200 import tttmlp as L
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+NAN = float("nan")
+
+
+def _rand(seed, *shape, dtype=torch.float32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def _within(got, want, tol, name):
+    g = _np(got)
+    has = ~np.isnan(want)
+    with np.errstate(invalid="ignore"):
+        off = np.where(has & (g != want), np.abs(g - want), 0.0)
+    over = float(np.where(has, off - tol, 0.0).max(initial=0.0))
+    assert np.all(np.isfinite(g[has & np.isfinite(want)])), f"{name}: non-finite values"
+    assert over <= 0, f"{name}: {over} beyond the bound"
+
+
+# ---------------------------------------------------------------- rotary positions
+@pytest.mark.parametrize("T,H,d,rot,layout,dtype", [
+    (9, 3, 64, 24, "interleaved", "bf16"),      # three 16-byte pieces: the last has no second
+    (9, 3, 64, 12, "interleaved", "f32"),
+    (5, 2, 64, 4, "interleaved", "bf16"),       # no whole piece: pair by pair
+    (5, 2, 24, 8, "interleaved", "bf16"),       # one piece
+    (2000, 1, 64, 32, "half", "bf16"),          # several rows a block, part of the head
+    (1999, 2, 128, 64, "half", "f32"),
+    (700, 40, 64, 64, "half", "f32"),
+    (1, 200, 64, 64, "interleaved", "bf16"),    # one row, more heads than one batch of loads
+    (3, 300, 256, 256, "half", "bf16"),
+])
+@pytest.mark.parametrize("place", ["new", "in place", "strided"])
+def test_rope_pieces(T, H, d, rot, layout, dtype, place):
+    dt = BF if dtype == "bf16" else torch.float32
+    wide = _rand(T + rot, T, H + 2, d, dtype=dt)
+    x = wide[:, 1:H + 1] if place == "strided" else wide[:, :H].contiguous()
+    want, tol = S.rope(_np(x), 5 + np.arange(T), rot, layout, dtype=dtype)
+    keep = wide.clone()
+    y = L.rope(x, pos0=5, rot=rot, layout=layout, out=x if place != "new" else None)
+    _within(y, want, tol, "rope")
+    if place == "strided":      # the heads on both sides were left alone
+        assert torch.equal(wide[:, 0], keep[:, 0]) and torch.equal(wide[:, H + 1], keep[:, H + 1])
+
+
+# ---------------------------------------------------------------- window attention
+LONG = [   # cu_q, cu_k, Hq, Hk, left, right, sinks
+    ([0, 5000], [0, 5000], 4, 2, 100, 0, 130),                 # sinks in two key blocks, their queries in three chunks
+    ([0, 2048, 4097, 4099], [0, 2048, 4097, 4099], 2, 1, 50, 0, 1),   # chunks that end with a sequence
+    ([0, 300, 4600], [0, 2500, 7000], 2, 2, 64, 10, 20),       # behind cached tokens, both sides
+    ([0, 3000], [0, 3000], 1, 1, 3000, 0, 4),                  # causal: nothing behind the window
+    ([0, 2600], [0, 2600], 1, 1, 20, 0, 300),                  # more sinks than are cut up
+    ([0, 2500], [0, 40], 2, 1, 10, 0, 3),                      # fewer keys than queries
+]
+
+
+@pytest.mark.parametrize("cu_q,cu_k,Hq,Hk,left,right,sinks", LONG)
+def test_window_long_lists_of_queries(cu_q, cu_k, Hq, Hk, left, right, sinks):
+    Tq, Tk = cu_q[-1], cu_k[-1]
+    q, k, v, g = (_rand(i, T, H, 64, dtype=BF) for i, (T, H) in enumerate(((Tq, Hq), (Tk, Hk), (Tk, Hk), (Tq, Hq))))
+    mask = dict(left=left, right=right, sinks=sinks, cu_q=_ints(cu_q), cu_k=_ints(cu_k))
+    ref = S.window_attention(_np(q), _np(k), _np(v), left, right, sinks, cu_q, cu_k, grad_out=_np(g))
+    r = L.window_attention(q, k, v, want_lse=True, **mask)
+    _within(r["out"], ref["out"], ref["out_tol"], "out")
+    _within(r["lse"], ref["lse"], 2.0 ** -16 + 2.0 ** -17 * np.abs(np.nan_to_num(ref["lse"], neginf=0.0)), "lse")
+    b = L.window_attention_backward(q, k, v, r["out"], r["lse"], g, **mask)
+    for n in ("dq", "dk", "dv"):
+        _within(b[n], ref[n], ref[n + "_tol"] + 1e-7, n)
+    again = L.window_attention_backward(q, k, v, r["out"], r["lse"], g, **mask)
+    assert all(torch.equal(again[n], b[n]) for n in ("dq", "dk", "dv"))
+
+
+@pytest.mark.parametrize("left", [0, 1, 40])
+def test_window_log_sum_exp_of_few_keys(left):
+    """The sum is held in fp32: with one key its logarithm is the score, to fp32's last bits."""
+    T = 300
+    q, k, v = (_rand(7 + i, T, 1, 64, dtype=BF) for i in range(3))
+    r = L.window_attention(q, k, v, left=left, want_lse=True)
+    ref = S.window_attention(_np(q), _np(k), _np(v), left, 0, 0)["lse"]
+    # 64 additions in fp32 (64 2^-24 of the sum of the products' sizes, which times the scale is below 16 here), an
+    # exponential good to 2^-18
+    assert np.abs(_np(r["lse"]) - ref).max() < 2.0 ** -18 * 16 + 2.0 ** -18
+
+
+@pytest.mark.parametrize("value", [NAN, math.inf])
+@pytest.mark.parametrize("which", ["q", "k", "v", "g"])
+def test_window_backward_keeps_non_finite_values_to_those_that_meet_them(which, value):
+    T, left, sinks, at = 700, 90, 2, 333
+    q, k, v, g = (_rand(30 + i, T, 2, 64, dtype=BF) for i in range(4))
+    r = L.window_attention(q, k, v, left=left, sinks=sinks, want_lse=True)
+    clean = L.window_attention_backward(q, k, v, r["out"], r["lse"], g, left=left, sinks=sinks)
+    t = dict(q=q, k=k, v=v, g=g)
+    t[which][at, 0, 9] = value
+    f = L.window_attention(q, k, v, left=left, sinks=sinks, want_lse=True, check_status=False)
+    b = L.window_attention_backward(q, k, v, f["out"], f["lse"], g, left=left, sinks=sinks, check_status=False)
+    assert L.ttt_mlp_status(b["workspace"]) == L.TTT_ERR_NONFINITE
+    i = torch.arange(T, device="cuda")
+    # query rows that meet it, and the keys that those rows see
+    rows = (i >= at) & (i <= at + left) if which in "kv" else i == at
+    first, last = int(rows.nonzero().min()), int(rows.nonzero().max())
+    keys = ((i >= first - left) & (i <= last)) | (i < sinks)
+    for n, touched in (("dq", rows), ("dk", keys), ("dv", keys)):
+        assert torch.equal(b[n][~touched], clean[n][~touched]), n
+        assert torch.equal(b[n][:, 1], clean[n][:, 1]), n          # the other head
+    assert not torch.isfinite(b["dq"][rows, 0].float()).all()
+
+
+def test_window_unseen_keys_get_zeros_whatever_they_hold():
+    Tq, Tk, left = 50, 600, 30
+    q, k, v, g = _rand(1, Tq, 1, 64, dtype=BF), _rand(2, Tk, 1, 64, dtype=BF), _rand(3, Tk, 1, 64, dtype=BF), _rand(4, Tq, 1, 64, dtype=BF)
+    k[:400], v[:400] = NAN, math.inf
+    r = L.window_attention(q, k, v, left=left, want_lse=True)
+    b = L.window_attention_backward(q, k, v, r["out"], r["lse"], g, left=left)
+    assert torch.all(b["dk"][:520] == 0) and torch.all(b["dv"][:520] == 0) and torch.isfinite(b["dq"].float()).all()
+
+
+def test_two_window_calls_at_once():
+    """Two streams, a workspace each, many items: the calls share nothing."""
+    T = 3000
+    a = [_rand(i, T, 4, 64, dtype=BF) for i in range(4)]
+    c = [_rand(10 + i, T, 4, 64, dtype=BF) for i in range(4)]
+
+    def step(q, k, v, g, ws=None, stream=None):
+        r = L.window_attention(q, k, v, left=200, sinks=3, want_lse=True, workspace=ws, check_status=False, stream=stream)
+        return r["out"], L.window_attention_backward(q, k, v, r["out"], r["lse"], g, left=200, sinks=3, workspace=ws,
+                                                     check_status=False, stream=stream)
+
+    alone = [step(*t) for t in (a, c)]
+    torch.cuda.synchronize()
+    ws = [L.window_attention_workspace(t[0], t[1], 1, backward=True) for t in (a, c)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        both = [step(*t, ws=w, stream=s) for t, w, s in zip((a, c), ws, streams)]
+        torch.cuda.synchronize()
+        for (o, b), (o1, b1) in zip(both, alone):
+            assert torch.equal(o, o1) and all(torch.equal(b[n], b1[n]) for n in ("dq", "dk", "dv"))
+
+
+# ---------------------------------------------------------------- decode
+def test_decode_one_token_at_every_length_around_tiles_and_the_ring():
+    Hq, Hk, sinks, left = 6, 2, 3, 130
+    slots = sinks + left + 1
+    lens = list(range(0, 140)) + [slots - 1, slots, slots + 1, 2 * slots, 1000, 2 ** 30]
+    B = len(lens)
+    ck, cv, q = (_rand(i, B, n, h, 64, dtype=BF) for i, (n, h) in enumerate(((slots, Hk), (slots, Hk), (1, Hq))))
+    r = L.window_attention_decode(q[:, 0], ck, cv, _ints(lens), left=left, sinks=sinks)
+    K, V = _np(ck), _np(cv)
+    small = [i for i, n in enumerate(lens) if n < 2 ** 20]
+    want, tol = S.window_decode(_np(q[:, 0])[small], lambda b, u: K[small[b], S.cache_slot(u, slots, sinks)],
+                                lambda b, u: V[small[b], S.cache_slot(u, slots, sinks)], [lens[i] for i in small], left, sinks, slots)
+    _within(r["out"][small], want, tol, "decode")
+    # a far position sees every slot of a ring of exactly its window, whatever their order
+    s = torch.einsum("hd,chd->hc", q[-1, 0].double(), ck[-1].double().repeat_interleave(Hq // Hk, 1)) / 8
+    far = torch.einsum("hc,chd->hd", s.softmax(-1), cv[-1].double().repeat_interleave(Hq // Hk, 1))
+    assert (r["out"][-1].double() - far).abs().max() < 2.0 ** -6
+
+
+# ---------------------------------------------------------------- gated recurrence
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dirs", ["fwd", "rev"])
+@pytest.mark.parametrize("T,D", [
+    (1, 8), (7, 16), (8, 40), (56, 8), (57, 72), (449, 200),     # narrow strips, less than a tile, a tile and a row
+    (3000, 8), (2000, 520), (900, 1000), (700, 2048), (300, 5000),
+])
+def test_scan_strips_and_tiles(T, D, dirs, dtype):
+    dt = BF if dtype == "bf16" else torch.float32
+    f, x, dy = (_rand(1, T, D) + 3).to(dt), _rand(2, T, D, dtype=dt), _rand(3, T, D, dtype=dt)
+    h0, dhT = _rand(4, 1, D), _rand(5, 1, D)
+    ref = S.gated_scan(_np(f), _np(x), "unit", dirs == "rev", None, _np(h0), _np(dy), _np(dhT), dtype)
+    r = L.gated_scan(f, x, form="unit", dirs=dirs, h0=h0, want_state=True, want_chunk_states=True)
+    _within(r["y"], ref["y"], ref["y_tol"], "y")
+    _within(r["h_T"], ref["hT"], ref["hT_tol"], "h_T")
+    b = L.gated_scan_backward(f, x, dy, r["chunk_states"], form="unit", dirs=dirs, h0=h0, dh_T=dhT, want_dh0=True)
+    for n in ("df", "dx", "dh0"):
+        _within(b[n], ref[n], ref[n + "_tol"] + 1e-30, n)
+
+
+@pytest.mark.parametrize("dirs", ["fwd", "rev"])
+@pytest.mark.parametrize("D", [8, 24, 264])
+def test_scan_of_many_short_sequences(D, dirs):
+    lens = [(5 * i) % 7 for i in range(800)]
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    T = cu[-1]
+    f, x, dy = _rand(1, T, D) + 1, _rand(2, T, D), _rand(3, T, D)
+    h0, dhT = _rand(4, 800, D), _rand(5, 800, D)
+    ref = S.gated_scan(_np(f), _np(x), "convex", dirs == "rev", cu, _np(h0), _np(dy), _np(dhT))
+    how = dict(dirs=dirs, cu=_ints(cu), h0=h0)
+    r = L.gated_scan(f, x, want_state=True, want_chunk_states=True, **how)
+    _within(r["y"], ref["y"], ref["y_tol"], "y")
+    _within(r["h_T"], ref["hT"], ref["hT_tol"], "h_T")
+    b = L.gated_scan_backward(f, x, dy, r["chunk_states"], dh_T=dhT, want_dh0=True, **how)
+    for n in ("df", "dx", "dh0"):
+        _within(b[n], ref[n], ref[n + "_tol"] + 1e-30, n)
+
+
+@pytest.mark.parametrize("dirs", ["fwd", "rev"])
+@pytest.mark.parametrize("which", ["f", "x", "dy", "h0"])
+@pytest.mark.parametrize("value", [NAN, math.inf])
+def test_scan_keeps_non_finite_values_to_their_sequence_and_channel(which, value, dirs):
+    cu, D = [0, 300, 700, 1500], 72
+    T = cu[-1]
+    f, x, dy, h0 = _rand(1, T, D) + 4, _rand(2, T, D), _rand(3, T, D), _rand(4, 3, D)
+    how = dict(form="sum", dirs=dirs, cu=_ints(cu))
+
+    def both():
+        r = L.gated_scan(f, x, h0=h0, want_state=True, want_chunk_states=True, check_status=False, **how)
+        b = L.gated_scan_backward(f, x, dy, r["chunk_states"], h0=h0, want_dh0=True, check_status=False, **how)
+        return [r["y"], b["df"], b["dx"]], [r["h_T"], b["dh0"]], r["workspace"], b["workspace"]
+
+    rows0, states0, _, _ = both()
+    t = dict(f=f, x=x, dy=dy, h0=h0)[which]
+    t[1 if which == "h0" else 500, 5] = NAN if which == "f" else value
+    rows, states, w1, w2 = both()
+    assert L.TTT_ERR_NONFINITE in (L.ttt_mlp_status(w1), L.ttt_mlp_status(w2))
+    other = torch.ones(T, D, dtype=torch.bool, device="cuda")
+    other[cu[1]:cu[2], 5] = False
+    for a, c in zip(rows, rows0):
+        assert torch.equal(a[other], c[other])
+    keep = torch.ones(3, D, dtype=torch.bool, device="cuda")
+    keep[1, 5] = False
+    for a, c in zip(states, states0):
+        assert torch.equal(a[keep], c[keep])
+    if which != "dy":
+        assert not torch.isfinite(rows[0][cu[1]:cu[2], 5]).all()
+
+
+def test_two_scans_at_once():
+    T, D = 5000, 512
+    sets = [[_rand(10 * j + i, T, D, dtype=BF) for i in range(2)] for j in range(2)]
+    alone = [L.gated_scan(*s, want_state=True) for s in sets]
+    ws, streams = [L.gated_scan_workspace(s[1]) for s in sets], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        both = [L.gated_scan(*s, want_state=True, workspace=w, stream=st, check_status=False) for s, w, st in zip(sets, ws, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(both, alone):
+            assert torch.equal(a["y"], b["y"]) and torch.equal(a["h_T"], b["h_T"])
+
+
+def test_operators_refuse_tensors_of_the_wrong_place_or_size():
+    x = _rand(1, 16, 64)
+    r = L.gated_scan(x, x.clone(), want_chunk_states=True)
+    for call in (lambda: L.gated_scan_backward(x, x, x, r["chunk_states"][:-8]),
+                 lambda: L.gated_scan(x, x.cpu()),
+                 lambda: L.gated_scan(x, x.half()),
+                 lambda: L.gated_scan(x, x, h0=_rand(2, 2, 64)),
+                 lambda: L.rope(x.view(16, 1, 64), positions=torch.zeros(15, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
+    q = _rand(3, 8, 1, 64, dtype=BF)
+    with pytest.raises(L.TTTError):     # a workspace of the forward pass is too small for the backward pass
+        f = L.window_attention(q, q.clone(), q.clone(), left=3, want_lse=True)
+        L.window_attention_backward(q, q.clone(), q.clone(), f["out"], f["lse"], q.clone(), left=3, workspace=f["workspace"])
