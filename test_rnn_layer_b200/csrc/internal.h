@@ -205,6 +205,7 @@ struct WindowArgs {
 cudaError_t launch_window_attention(const WindowArgs& a, cudaStream_t s);
 cudaError_t launch_window_attention_backward(const WindowArgs& a, cudaStream_t s);
 cudaError_t launch_window_dkv(const WindowArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_window_sink_sum(const WindowArgs& a, cudaStream_t s);
 long long window_partial_floats(const WindowArgs& a);   // of Tq, n_seq, Hq and Hk alone
 
 struct WindowDecodeArgs {

@@ -371,6 +371,8 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
         tc::tc_fence_after();
         tc::tmem_dealloc(tm, 512);
     }
+    // this kernel may have begun before the one of dK and dV ended; what follows in the stream waits for both
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // delta[h, t] = sum of dO Out over the head's columns, NaN where the row's q is not finite (so that delta is finite
@@ -417,7 +419,8 @@ __global__ void __launch_bounds__(256) window_delta_kernel(const WindowArgs p, l
     if (t < rows && (lane & 7) == 0) p.delta[(long long)h * p.Tq + t] = sum;
 }
 
-cudaError_t launch_dq(const WindowArgs& a, int sms, cudaStream_t s) {
+// after_dkv: the launch before is the one of dK and dV, whose end need not be waited for
+cudaError_t launch_dq(const WindowArgs& a, int sms, bool after_dkv, cudaStream_t s) {
     QArgs p{};
     p.w = a;
     const bool k = a.Tk > 0;   // without keys the tiles are never loaded; any valid array serves the maps
@@ -429,9 +432,18 @@ cudaError_t launch_dq(const WindowArgs& a, int sms, cudaStream_t s) {
     p.n_items = win::block_numbers<ROWS>(a.Tq, a.n_seq) * a.Hq;
     cudaError_t e = cudaFuncSetAttribute(window_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.n_items < sms ? p.n_items : sms));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = after_dkv ? 1 : 0;
     LaunchScope scope("window_dq", s);
-    window_dq_kernel<<<(unsigned)(p.n_items < sms ? p.n_items : sms), THREADS, SMEM_BYTES, s>>>(p);
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, window_dq_kernel, p);
 }
 
 }  // namespace
@@ -447,7 +459,8 @@ cudaError_t launch_window_attention_backward(const WindowArgs& a, cudaStream_t s
     }
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && a.Tk) e = launch_window_dkv(a, sms, s);
-    if (e == cudaSuccess && a.Tq) e = launch_dq(a, sms, s);
+    if (e == cudaSuccess && a.Tq) e = launch_dq(a, sms, a.Tk > 0, s);
+    if (e == cudaSuccess && a.Tk) e = launch_window_sink_sum(a, s);
     return e;
 }
 

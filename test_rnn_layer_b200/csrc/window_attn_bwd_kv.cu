@@ -135,6 +135,9 @@ __global__ void __launch_bounds__(KV_THREADS, 1) window_dkv_kernel(const __grid_
     uint4* bad_rows = reinterpret_cast<uint4*>(bars + B_BAD);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    // dQ needs nothing of this kernel: its CTAs may take the SMs that this kernel's last items leave
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
     const win::ItemQueue items{bars + B_IF, bars + B_IE, reinterpret_cast<volatile int*>(bars + B_ITEM), abort_flag};
 
     if (tid == 0) {
@@ -496,10 +499,14 @@ cudaError_t launch_window_dkv(const WindowArgs& a, int sms, cudaStream_t s) {
         LaunchScope scope("window_dkv", s);
         window_dkv_kernel<<<(unsigned)(p.n_items < sms ? p.n_items : sms), KV_THREADS, SMEM_BYTES, s>>>(p);
     }
-    if (p.cut) {
-        LaunchScope scope("window_sink_sum", s);
-        window_sink_sum_kernel<<<dim3((unsigned)(a.n_seq * a.Hk), (a.sinks + BT - 1) / BT, SLOT / 4 / 256), 256, 0, s>>>(a);
-    }
+    return cudaGetLastError();
+}
+
+// The sums of the key blocks that were cut up, if there are any.
+cudaError_t launch_window_sink_sum(const WindowArgs& a, cudaStream_t s) {
+    if (!cuts_sinks(a)) return cudaSuccess;
+    LaunchScope scope("window_sink_sum", s);
+    window_sink_sum_kernel<<<dim3((unsigned)(a.n_seq * a.Hk), (a.sinks + BT - 1) / BT, SLOT / 4 / 256), 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 
