@@ -14,13 +14,13 @@ __global__ void __launch_bounds__(32 * (kWarpsF + 1), kPerSmF)
     extern __shared__ __align__(128) uint8_t stages[];
     const SeqOffsets c{p.cu, p.n_seq, p.T};
     const int cs = cluster_size(), rank = tc::cluster_ctarank(), chunks = (p.T + TILE - 1) / TILE, steps = (chunks + cs - 1) / cs;
-    const int strip = blockIdx.x / cs * LC * V;
+    const int strip = blockIdx.x / cs * LC * V, cols = min(LC, (p.D - strip) / V);
     empty_sequences(c, p.D, p.H_0, p.H_T, p.status);
     init_barriers(sh);
     bool ok = true;
     if (threadIdx.x >= 32 * W) {
         // stage s: TILE rows of the strip of F, then of X
-        ok = exchange<LC, V, W>(sh, steps, cs, rank, [&](int step) {
+        ok = exchange<LC, V, W>(sh, steps, cs, rank, cols, [&](int step) {
             const int chunk = step * cs + rank, s = step % kStages;
             if (step >= steps || chunk >= chunks) return;
             const int row = (p.reverse ? chunks - 1 - chunk : chunk) * TILE;
@@ -32,8 +32,7 @@ __global__ void __launch_bounds__(32 * (kWarpsF + 1), kPerSmF)
             }
         });
     } else {
-        const int col = threadIdx.x % LC, group = threadIdx.x / LC, dir = p.reverse ? -1 : 1, ch = strip + col * V;
-        const bool on = ch < p.D;
+        const int col = min((int)threadIdx.x % LC, cols - 1), group = threadIdx.x / LC, dir = p.reverse ? -1 : 1, ch = strip + col * V;
         using T = typename Elem<BF>::type;
         bool bad = false;
         int seq_b = 0, seq_e = 0;
@@ -82,24 +81,24 @@ __global__ void __launch_bounds__(32 * (kWarpsF + 1), kPerSmF)
                     Vec<V> ak, bk;
                     load(in + k * pitch_in, ak, bk);
                     if (r.start) {
-                        run = Run<V>{all<V>(kReset), fma(ak, state_of<V>(p.H_0, r.s, p.D, ch, on), bk)};
+                        run = Run<V>{all<V>(kReset), fma(ak, state_of<V>(p.H_0, r.s, p.D, ch), bk)};
                     } else {
                         run.b = fma(ak, run.b, bk);
                         run.a = mul(run.a, ak);   // -0 stays -0
                     }
                 }
             }
-            q.before = hand_over<LC, V, W>(sh, step, run);
+            q.before = hand_over<LC, V, W>(sh, step, col, run);
         };
         auto second_half = [&](Set& q, int step) {
             const int t0 = first_row(step);
             Vec<V> h;
-            if (!ok || !take_over<LC, V, W>(sh, step, q.before, h)) {
+            if (!ok || !take_over<LC, V, W>(sh, step, col, q.before, h)) {
                 ok = false;
                 return;
             }
             // the state that enters the rows
-            if (p.chunk_states && on && t0 >= 0 && t0 / kKeep * kKeep < p.T) {
+            if (p.chunk_states && t0 >= 0 && t0 / kKeep * kKeep < p.T) {
                 const long long at = (long long)(t0 / kKeep) * p.D + ch;
                 *reinterpret_cast<Vec<V>*>(p.chunk_states + at) = h;
             }
@@ -108,10 +107,10 @@ __global__ void __launch_bounds__(32 * (kWarpsF + 1), kPerSmF)
 #pragma unroll
                 for (int k = 0; k < R; ++k) {
                     h = fma(q.a[k], h, q.b[k]);
-                    if (on) __stcs(reinterpret_cast<uint32_t*>(y), Elem<BF>::put(h));
+                    __stcs(reinterpret_cast<uint32_t*>(y), Elem<BF>::put(h));
                     y += pitch;
                 }
-                bad |= on && wild<V>(h);   // inside a sequence a state that is not finite stays so
+                bad |= wild<V>(h);   // inside a sequence a state that is not finite stays so
             } else {
                 const uint8_t* in = input_of(step);
 #pragma unroll 1
@@ -120,11 +119,11 @@ __global__ void __launch_bounds__(32 * (kWarpsF + 1), kPerSmF)
                     if (r.s < 0) continue;
                     Vec<V> ak, bk;
                     load(in + k * pitch_in, ak, bk);
-                    if (r.start) h = state_of<V>(p.H_0, r.s, p.D, ch, on);
+                    if (r.start) h = state_of<V>(p.H_0, r.s, p.D, ch);
                     h = fma(ak, h, bk);
-                    bad |= on && wild<V>(h);
-                    if (on) __stcs(reinterpret_cast<uint32_t*>(y + k * pitch), Elem<BF>::put(h));
-                    if (r.end) put_state<V>(p.H_T, r.s, p.D, ch, on, h);
+                    bad |= wild<V>(h);
+                    __stcs(reinterpret_cast<uint32_t*>(y + k * pitch), Elem<BF>::put(h));
+                    if (r.end) put_state<V>(p.H_T, r.s, p.D, ch, h);
                 }
             }
         };

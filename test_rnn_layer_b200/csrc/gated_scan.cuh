@@ -16,6 +16,9 @@
 // is not finite would still reach through as 0 times it, so where a walk's result is not finite it is done again
 // with the runs' signs looked at.
 //
+// In a strip of fewer channels the lanes beyond them do the last one's work once more (the same values to the same
+// places), which spares a predicate on every access.
+//
 // Narrow strips (LC = 16 or 8) serve few channels, so that the grid is about one wave.  (Tiles that look back at
 // each other's states in global memory in place of the clusters were slower: 2.25 ms for 313,344 rows of 1,024
 // channels, the hand-over between tiles being the bound.)  Every wait is bounded.
@@ -210,11 +213,11 @@ __device__ __forceinline__ Row row_of(const SeqOffsets& c, Cursor& at, int t, in
     return {at.s, t == (reverse ? at.e - 1 : at.b), t == (reverse ? at.b : at.e - 1)};
 }
 
-// Sequence s's values of an fp32 array [n_seq, D] (null: zeros); `on`: the thread has channels.
+// Sequence s's values of an fp32 array [n_seq, D] (null: zeros).
 template <int V>
-__device__ __forceinline__ Vec<V> state_of(const float* p, int s, int D, int ch, bool on) {
+__device__ __forceinline__ Vec<V> state_of(const float* p, int s, int D, int ch) {
     Vec<V> r = all<V>(0.f);
-    if (p && on) {
+    if (p) {
         const long long at = (long long)s * D + ch;
 #pragma unroll
         for (int v = 0; v < V; ++v) r.set(v, p[at + v]);
@@ -222,8 +225,8 @@ __device__ __forceinline__ Vec<V> state_of(const float* p, int s, int D, int ch,
     return r;
 }
 template <int V>
-__device__ __forceinline__ void put_state(float* p, int s, int D, int ch, bool on, Vec<V> h) {
-    if (!p || !on) return;
+__device__ __forceinline__ void put_state(float* p, int s, int D, int ch, Vec<V> h) {
+    if (!p) return;
     const long long at = (long long)s * D + ch;
 #pragma unroll
     for (int v = 0; v < V; ++v) p[at + v] = h.get(v);
@@ -324,9 +327,9 @@ __device__ __forceinline__ void init_barriers(Shared<LC, V, W>& sh) {
 // A step's first half, by a walking warp: its groups' runs to the exchange.  Returns, for G > 1, the runs of the
 // warp's groups in front of this one.
 template <int LC, int V, int W>
-__device__ __forceinline__ Run<V> hand_over(Shared<LC, V, W>& sh, int step, Run<V> mine) {
+__device__ __forceinline__ Run<V> hand_over(Shared<LC, V, W>& sh, int step, int col, Run<V> mine) {
     constexpr int G = 32 / LC;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, col = lane % LC, group = lane / LC;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = lane / LC;
     Run<V> before = mine;
     if constexpr (G == 1) {
         sh.part[step & 1][warp][col] = mine;
@@ -348,9 +351,9 @@ __device__ __forceinline__ Run<V> hand_over(Shared<LC, V, W>& sh, int step, Run<
 }
 // Its second half: the state that enters this thread's rows.
 template <int LC, int V, int W>
-__device__ __forceinline__ bool take_over(Shared<LC, V, W>& sh, int step, Run<V> before, Vec<V>& h) {
+__device__ __forceinline__ bool take_over(Shared<LC, V, W>& sh, int step, int col, Run<V> before, Vec<V>& h) {
     if (!tc::mbar_wait(sh.entered + (step & 1), (step >> 1) & 1, &sh.abort)) return false;
-    const Vec<V> e = sh.enter[step & 1][threadIdx.x >> 5][threadIdx.x % LC];
+    const Vec<V> e = sh.enter[step & 1][threadIdx.x >> 5][col];
     h = e;
     if constexpr (LC < 32) {
         h = over<V>(before, e);
@@ -363,9 +366,9 @@ __device__ __forceinline__ bool take_over(Shared<LC, V, W>& sh, int step, Run<V>
 // walks the state over the runs of the CTAs and of the warps.  (Every warp doing this for itself took 40% of all
 // instructions; one of the walking warps doing it between two barriers left the others waiting 60% of the time.)
 template <int LC, int V, int W, class Issue>
-__device__ __forceinline__ bool exchange(Shared<LC, V, W>& sh, int steps, int cs, int rank, Issue issue) {
+__device__ __forceinline__ bool exchange(Shared<LC, V, W>& sh, int steps, int cs, int rank, int cols, Issue issue) {
     constexpr int G = 32 / LC;
-    const int lane = threadIdx.x & 31, col = lane % LC, group = lane / LC;
+    const int lane = threadIdx.x & 31, col = min(lane % LC, cols - 1), group = lane / LC;
     Vec<V> state = all<V>(0.f);
     if (lane == 0)
         for (int s = 0; s < 2; ++s) issue(s);

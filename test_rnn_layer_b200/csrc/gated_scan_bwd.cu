@@ -17,13 +17,13 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
     extern __shared__ __align__(128) uint8_t stages[];
     const SeqOffsets c{p.cu, p.n_seq, p.T};
     const int cs = cluster_size(), rank = tc::cluster_ctarank(), chunks = (p.T + TILE - 1) / TILE, steps = (chunks + cs - 1) / cs;
-    const int strip = blockIdx.x / cs * LC * V;
+    const int strip = blockIdx.x / cs * LC * V, cols = min(LC, (p.D - strip) / V);
     empty_sequences(c, p.D, p.dH_T, p.dH_0, p.status);
     init_barriers(sh);
     bool ok = true;
     if (threadIdx.x >= 32 * W) {
         // stage s: TILE rows of the strip of F, X and dY, then the kept states of the tile's segments
-        ok = exchange<LC, V, W>(sh, steps, cs, rank, [&](int step) {
+        ok = exchange<LC, V, W>(sh, steps, cs, rank, cols, [&](int step) {
             const int chunk = step * cs + rank, s = step % kStages;
             if (step >= steps || chunk >= chunks) return;
             const int row = (p.reverse ? chunk : chunks - 1 - chunk) * TILE;
@@ -37,8 +37,7 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
             tc::tma_load_2d(to + 3 * ARRAY, &m.h, strip, row / kKeep, sh.full + s);
         });
     } else {
-        const int col = threadIdx.x % LC, group = threadIdx.x / LC, dir = p.reverse ? 1 : -1, ch = strip + col * V;
-        const bool on = ch < p.D;
+        const int col = min((int)threadIdx.x % LC, cols - 1), group = threadIdx.x / LC, dir = p.reverse ? 1 : -1, ch = strip + col * V;
         using T = typename Elem<BF>::type;
         bool bad = false;
         int seq_b = 0, seq_e = 0;
@@ -94,19 +93,19 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
                     gates<V>(Elem<BF>::get(word(0, k)), ak, rest);
                     const Vec<V> g = Elem<BF>::get(word(2, k));
                     if (r.end) {   // lambda starts anew, with the final state's gradient
-                        run = Run<V>{all<V>(kReset), mul(ak, add(state_of<V>(p.dH_T, r.s, p.D, ch, on), g))};
+                        run = Run<V>{all<V>(kReset), mul(ak, add(state_of<V>(p.dH_T, r.s, p.D, ch), g))};
                     } else {
                         run.b = mul(ak, add(run.b, g));
                         run.a = mul(run.a, ak);   // -0 stays -0
                     }
                 }
             }
-            q.before = hand_over<LC, V, W>(sh, step, run);
+            q.before = hand_over<LC, V, W>(sh, step, col, run);
         };
         auto second_half = [&](Set& q, int step) {
             const int t0 = first_row(step);
             Vec<V> lam;
-            if (!ok || !take_over<LC, V, W>(sh, step, q.before, lam)) {
+            if (!ok || !take_over<LC, V, W>(sh, step, col, q.before, lam)) {
                 ok = false;
                 return;
             }
@@ -119,10 +118,8 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
                     const Vec<V> l = add(lam, Elem<BF>::get(q.dy[k])), d = mul(l, q.sl[k]);
                     seen = fma(all<V>(0.f), d, seen);
                     lam = mul(q.a[k], l);
-                    if (on) {
-                        __stcs(reinterpret_cast<uint32_t*>(df), Elem<BF>::put(d));
-                        __stcs(reinterpret_cast<uint32_t*>(dx), Elem<BF>::put(mul(l, q.sc[k])));
-                    }
+                    __stcs(reinterpret_cast<uint32_t*>(df), Elem<BF>::put(d));
+                    __stcs(reinterpret_cast<uint32_t*>(dx), Elem<BF>::put(mul(l, q.sc[k])));
                     df += pitch_f;
                     dx += pitch_x;
                 }
@@ -136,7 +133,7 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
                 for (int k = R - 1; k >= 0; --k) {
                     const Row r = row_of(c, at_row, t0 + dir * k, p.reverse);
                     if (r.s < 0) continue;
-                    if (r.start) h = state_of<V>(p.H_0, r.s, p.D, ch, on);
+                    if (r.start) h = state_of<V>(p.H_0, r.s, p.D, ch);
                     before[k] = h;
                     Vec<V> ak, rest;
                     gates<V>(Elem<BF>::get(word(0, k)), ak, rest);
@@ -149,19 +146,17 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
                     Vec<V> ak, rest, s, slope;
                     gates<V>(Elem<BF>::get(word(0, k)), ak, rest);
                     slopes<FORM, V>(ak, rest, before[k], Elem<BF>::get(word(1, k)), s, slope);
-                    if (r.end) lam = state_of<V>(p.dH_T, r.s, p.D, ch, on);
+                    if (r.end) lam = state_of<V>(p.dH_T, r.s, p.D, ch);
                     const Vec<V> l = add(lam, Elem<BF>::get(word(2, k))), d = mul(l, slope);
                     lam = mul(ak, l);
                     seen = fma(all<V>(0.f), d, seen);
                     seen = fma(all<V>(0.f), lam, seen);
-                    if (on) {
-                        *reinterpret_cast<uint32_t*>(df + k * pitch_f) = Elem<BF>::put(d);
-                        *reinterpret_cast<uint32_t*>(dx + k * pitch_x) = Elem<BF>::put(mul(l, s));
-                    }
-                    if (r.start) put_state<V>(p.dH_0, r.s, p.D, ch, on, lam);
+                    *reinterpret_cast<uint32_t*>(df + k * pitch_f) = Elem<BF>::put(d);
+                    *reinterpret_cast<uint32_t*>(dx + k * pitch_x) = Elem<BF>::put(mul(l, s));
+                    if (r.start) put_state<V>(p.dH_0, r.s, p.D, ch, lam);
                 }
             }
-            bad |= on && wild<V>(seen);
+            bad |= wild<V>(seen);
         };
         Set q0, q1;
         if (steps > 0) first_half(q0, 0);
