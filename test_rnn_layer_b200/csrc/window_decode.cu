@@ -3,7 +3,8 @@
 // Every visible key and value is read once: the bytes of the cache bound it.  A cluster of up to eight CTAs takes
 // one request and key head (and sixteen of the query heads that share it, padded to the matrix instruction's 16
 // rows); its warps take tiles of 32 visible keys in turn, each through a ring of its own (cp.async, 16 bytes a
-// lane, rows in a 128-byte swizzle; no barrier between warps).  S = Q K^T and O += P V run on mma.sync with the
+// lane, rows in a 128-byte swizzle; no barrier between warps; two stages, so that three CTAs share an SM: 64 requests
+// x 16,388 keys in 364 us, 5.9 TB/s, against 421 us with three stages and two CTAs).  S = Q K^T and O += P V run on mma.sync with the
 // softmax's statistics in registers: one token gives far too few rows for tcgen05's 128, and the tensor time is
 // a few percent of the loads'.  The warps' partial results join in shared memory, the CTAs' in the first CTA's
 // (distributed shared memory), in a fixed order: no workspace, no second launch.
@@ -20,7 +21,7 @@
 namespace ttt {
 namespace {
 
-constexpr int kWarps = 4, kTile = 32, kStages = 3, kHeads = 16, DH = 64, kMaxCluster = 8;
+constexpr int kWarps = 4, kTile = 32, kStages = 2, kHeads = 16, DH = 64, kMaxCluster = 8;
 constexpr int kStageBytes = 2 * kTile * DH * 2;   // K and V rows of a tile
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
@@ -258,8 +259,8 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t s) {
     const int G = a.Hq / a.Hk;
     const long long items = (long long)a.B * a.Hk * ((G + kHeads - 1) / kHeads);
     const long long keys = std::min<long long>(a.slots, (long long)a.left + 1 + a.sinks);   // at most, per request
-    // split the keys while the card has room (six waves of two CTAs per SM, for requests of unequal lengths) and
-    // every warp keeps a tile
+    // split the keys while the card has room (four waves of three CTAs per SM, for requests of unequal lengths: the
+    // 364 us above are 388 with half as many, 476 with a quarter) and every warp keeps a tile
     int cs = 1;
     while (cs < kMaxCluster && items * cs < 12LL * sms && keys > (long long)cs * kWarps * kTile) cs *= 2;
     if (items * cs > 0x7fffffffLL) return cudaErrorInvalidValue;
