@@ -6,7 +6,7 @@
 // 2^-31 turns; the rest is sinpi/cospi in fp32.  One angle serves every head
 // of a row, so a block first fills a table of cos and sin for its rows in
 // shared memory and then streams the heads past it, 16 bytes at a time and
-// four loads a thread under way while the table is made.  Bound by memory:
+// three units a thread under way while the table is made.  Bound by memory:
 // each element is read and written once.
 //
 // A unit is what one thread turns at once: two 16-byte pieces, the pairs'
@@ -18,7 +18,7 @@
 namespace ttt {
 namespace {
 
-constexpr int kThreads = 256, kMaxRows = 8, kBatch = 4;
+constexpr int kThreads = 128, kMaxRows = 8, kBatch = 3;   // 69 us for 32,768 x 48 heads; 256 x 4: 78, 128 x 6: 78
 
 __device__ __forceinline__ void fill_table(const RopeArgs& p, int t0, int rows, float2* cs) {
     const int pairs = p.rot / 2;
@@ -198,7 +198,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
     }
     const int turned = a.half ? a.rot / 2 / n : (a.rot / n + 1) / 2;
     const int copied = a.X == a.Y ? 0 : (a.d - a.rot) / n;
-    // rows of a block: enough for four loads a thread, fewer where blocks would be short of the SMs
+    // rows of a block: enough for three units a thread, fewer where blocks would be short of the SMs
     int rows = 1;
     while (rows < kMaxRows && (long long)rows * a.H * (turned + copied) < kBatch * kThreads && a.T / (2 * rows) >= 2 * sms) rows *= 2;
     const unsigned grid = (unsigned)((a.T + rows - 1) / rows);
