@@ -58,10 +58,10 @@ __device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
     return r;
 }
 
-// 2^x0, 2^x1 on the FMA pipe: fma_exp2.cuh's cubic (relative error 7.6e-5, 25 times below the bf16
-// rounding P gets) on a pair, with the packed f32x2 arithmetic.  x <= 8 here; below -125 it returns about
-// 2^-125, which next to a row maximum of at least 2^-8 is far below fp32 resolution.
-__device__ __forceinline__ void ex2_poly2(uint64_t x, float& p0, float& p1) {
+// 2^x0, 2^x1 on the FMA pipe: a cubic of fma_exp2.cuh's kind (coefficients c0 .. c3) on a pair, with the packed f32x2
+// arithmetic.  x <= 8 here; below -125 it returns about 2^-125, which next to a row maximum of at least 2^-8 is far
+// below fp32 resolution.
+__device__ __forceinline__ void ex2_cubic2(uint64_t x, float c0, float c1, float c2, float c3, float& p0, float& p1) {
     float x0, x1;
     f2_split(x, x0, x1);
     x = f2(max_nan(x0, -125.0f), max_nan(x1, -125.0f));   // as fexp::clamp_low; NaN stays NaN
@@ -69,9 +69,9 @@ __device__ __forceinline__ void ex2_poly2(uint64_t x, float& p0, float& p1) {
     const uint64_t shift = f2(kShift, kShift);
     const uint64_t t = f2_add(x, shift);
     const uint64_t f = f2_sub(x, f2_sub(t, shift));
-    uint64_t p = f2_fma(f2(kC3_3, kC3_3), f, f2(kC3_2, kC3_2));
-    p = f2_fma(p, f, f2(kC3_1, kC3_1));
-    p = f2_fma(p, f, f2(kC3_0, kC3_0));
+    uint64_t p = f2_fma(f2(c3, c3), f, f2(c2, c2));
+    p = f2_fma(p, f, f2(c1, c1));
+    p = f2_fma(p, f, f2(c0, c0));
     float t0, t1, q0, q1;
     f2_split(t, t0, t1);
     f2_split(p, q0, q1);

@@ -40,6 +40,7 @@
 #include <vector>
 
 #include "attn_prims.cuh"
+#include "fma_exp2.cuh"
 #include "internal.h"
 
 namespace ttt {
@@ -125,6 +126,12 @@ __device__ __forceinline__ void item_of(const AttnArgs& p, int w, int& gi, int& 
     const int r = w - p.g[gi].item0;
     h = r / p.g[gi].pairs;
     pr = r - h * p.g[gi].pairs;
+}
+
+// 2^x0, 2^x1 on the FMA pipe: fma_exp2.cuh's cubic (relative error 7.6e-5, 25 times below the bf16
+// rounding P gets) on a pair.
+__device__ __forceinline__ void ex2_poly2(uint64_t x, float& p0, float& p1) {
+    ex2_cubic2(x, fexp::kC3_0, fexp::kC3_1, fexp::kC3_2, fexp::kC3_3, p0, p1);
 }
 
 __global__ void __launch_bounds__(THREADS, 1) attn_seg_kernel(const __grid_constant__ AttnArgs p) {

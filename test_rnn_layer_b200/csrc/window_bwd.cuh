@@ -23,6 +23,12 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     return r;
 }
 
+// 2^x0, 2^x1 on the FMA pipe: fma_exp2.cuh's cubic (relative error 7.6e-5, 25 times below the bf16
+// rounding P and dS get) on a pair.
+__device__ __forceinline__ void ex2_poly2(uint64_t x, float& p0, float& p1) {
+    ex2_cubic2(x, fexp::kC3_0, fexp::kC3_1, fexp::kC3_2, fexp::kC3_3, p0, p1);
+}
+
 // Rows of a 128-row tile in shared memory that must not enter a product (not finite, or not the sequence's: a weight
 // of zero would not keep them out) are zeroed; bit `lane` of word g is row 32 g + lane.  A warp calls it.
 // Which rows of the inputs are not finite is found by the pass that computes delta: looking through every tile here
