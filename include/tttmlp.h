@@ -542,8 +542,14 @@ TTT_API ttt_status ttt_window_attention(const ttt_window_desc* desc, const int* 
  *             row of a sequence; keys that no query sees get zeros.  They must
  *             not overlap the inputs.
  * P and dS enter their products as bf16; every sum is fp32 in a fixed order
- * (no atomics; a key head's gradient sums its query heads one after the other).
- *   workspace ttt_window_attention_backward_workspace_size(desc) bytes.
+ * (no atomics; a key head's gradient sums its query heads one after the other,
+ * a sink's later queries in chunks of 2,048 that are added in order).
+ * A value of Q, K, V, Out or dOut that is not finite makes the gradients it
+ * takes part in NaN (dQ of rows that see it, dK and dV of the keys that those
+ * rows see) and is reported by the status; the others are not affected.
+ *   workspace ttt_window_attention_backward_workspace_size(desc) bytes (a
+ *             function of Tq, Tk, n_seq, Hq and Hk alone, and enough for the
+ *             forward pass too).
  */
 TTT_API size_t ttt_window_attention_backward_workspace_size(const ttt_window_desc* desc);
 TTT_API ttt_status ttt_window_attention_backward(const ttt_window_desc* desc, const int* cu_q, const int* cu_k,
@@ -607,8 +613,9 @@ TTT_API ttt_status ttt_window_attention_decode(const ttt_window_decode_desc* des
  *             overlap F or X.
  *   H_0, H_T  fp32 [n_seq, D], each may be NULL; H_T receives the state after
  *             each sequence's last row (H_0, or 0, for an empty sequence).
- *   chunk_states  NULL, or ttt_gated_scan_chunk_states_size(desc) bytes: what
- *             the backward pass needs besides the inputs.
+ *   chunk_states  NULL, or ttt_gated_scan_chunk_states_size(desc) bytes: the
+ *             fp32 state every 8 rows, what the backward pass needs besides the
+ *             inputs.
  *   workspace ttt_gated_scan_workspace_size(desc) bytes, 256-byte aligned;
  *             ttt_mlp_status reports non-finite outputs, bad offsets and
  *             expired waits.
@@ -620,6 +627,7 @@ TTT_API ttt_status ttt_window_attention_decode(const ttt_window_decode_desc* des
  *   dF_t = l_t (h_{t-1} a (1 - a) + x_t ds/df),  dX_t = l_t s(a_t),
  *   dH_0 = a l at the first row,
  * with h recomputed in fp32 from the chunk states.  The same workspace size.
+ * A value that is not finite stays with its sequence and channel.
  *
  * Step, for serving: one token of each of B rows: H_out = a H + s(a) x (fp32
  * [B, D] dense; H_out may be H), Y (may be NULL) = H_out rounded.
