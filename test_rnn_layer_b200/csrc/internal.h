@@ -198,6 +198,7 @@ struct WindowArgs {
     const __nv_bfloat16* dOut;
     __nv_bfloat16 *dQ, *dK, *dV;
     long long ld_do, ld_dq, ld_dk, ld_dv;
+    float grad_scale;            // scale, or 0 where no row can see two keys (one key's weight is 1 whatever its score)
     float* delta;                // [Hq, Tq] scratch: rowsum(dOut * Out)
     uint8_t* key_odd;            // [Hk, Tk] scratch: whether a key is not finite
     float* partial;              // scratch: partial sums of the sinks' dK and dV

@@ -247,6 +247,7 @@ extern "C" TTT_API ttt_status ttt_window_attention_backward(const ttt_window_des
     a.dK = static_cast<__nv_bfloat16*>(dK); a.ld_dk = ld_dk;
     a.dV = static_cast<__nv_bfloat16*>(dV); a.ld_dv = ld_dv;
     a.status = static_cast<int*>(workspace);
+    a.grad_scale = a.left == 0 && a.right == 0 && a.sinks == 0 ? 0.f : a.scale;
     char* space = static_cast<char*>(workspace) + kAlign;
     a.delta = reinterpret_cast<float*>(space);
     space += align_up((size_t)q.Hq * q.Tq * sizeof(float));

@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
             }
             if (mine) {
                 const long long t = it.q_lo + BT * X + r;
-                nonfinite |= store_row(p.w.dQ + t * p.w.ld_dq + it.h * DH + COLS * y, o, p.w.scale);
+                nonfinite |= store_row(p.w.dQ + t * p.w.ld_dq + it.h * DH + COLS * y, o, p.w.grad_scale);
             }
         }
         if (!ok && lane == 0) give_up();
@@ -378,9 +378,32 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
 // delta[h, t] = sum of dO Out over the head's columns, NaN where the row's q is not finite (so that delta is finite
 // only where q, dO and Out are), and key_odd[h, u]: whether the key is not finite.  Eight lanes a row of 64, 16
 // bytes each; a warp takes four consecutive rows of one head.  Also looks over the offsets.
+//
+// Out is rounded to bf16, and dP - delta of a row with few keys is small beside dP: with two keys the rounding put
+// dQ and dK off by 0.0055 in the norm (0.0025 with many).  So a row of at most FEW keys gets delta = sum_u P_u dP_u,
+// which is the same number, from the keys and values themselves.
+constexpr int FEW = 20;
+
+__device__ __forceinline__ float dot8(const uint4& x, const uint4& y) {
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+    float sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&xw[e]), b = *reinterpret_cast<const __nv_bfloat162*>(&yw[e]);
+        sum = fmaf(__low2float(a), __low2float(b), sum);
+        sum = fmaf(__high2float(a), __high2float(b), sum);
+    }
+    return sum;
+}
+__device__ __forceinline__ float sum8(float v) {   // over the eight lanes of a row
+#pragma unroll
+    for (int m = 1; m < 8; m *= 2) v += __shfl_xor_sync(0xffffffffu, v, m);
+    return v;
+}
+
 __global__ void __launch_bounds__(256) window_delta_kernel(const WindowArgs p, long long q_warps, long long warps) {
+    const SeqOffsets cq{p.cu_q, p.n_seq, p.Tq}, ck{p.cu_k, p.n_seq, p.Tk};
     if (blockIdx.x == 0) {
-        const SeqOffsets cq{p.cu_q, p.n_seq, p.Tq}, ck{p.cu_k, p.n_seq, p.Tk};
         for (int s = threadIdx.x; s <= p.n_seq; s += blockDim.x)
             if (cq.bad(s) || ck.bad(s)) atomicOr(p.status, kStatusBadOffsets);
     }
@@ -392,31 +415,54 @@ __global__ void __launch_bounds__(256) window_delta_kernel(const WindowArgs p, l
     const int heads = key ? p.Hk : p.Hq, h = (int)(w % heads), rows = key ? p.Tk : p.Tq;
     const long long t = w / heads * 4 + (lane >> 3);
     const int col = h * DH + (lane & 7) * 8;
-    float sum = 0.f;
-    bool odd = false;
-    if (t < rows) {
-        odd = odd_values(*reinterpret_cast<const uint4*>((key ? p.K + t * p.ld_k : p.Q + t * p.ld_q) + col));
+    const bool in = t < rows;
+    uint4 x = make_uint4(0, 0, 0, 0), g = x, o = x;
+    if (in) {
+        x = *reinterpret_cast<const uint4*>((key ? p.K + t * p.ld_k : p.Q + t * p.ld_q) + col);
         if (!key) {
-            const uint4 g = *reinterpret_cast<const uint4*>(p.dOut + t * p.ld_do + col);
-            const uint4 o = *reinterpret_cast<const uint4*>(p.Out + t * p.ld_out + col);
-            const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, ow[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&gw[e]), b = *reinterpret_cast<const __nv_bfloat162*>(&ow[e]);
-                sum = fmaf(__low2float(a), __low2float(b), sum);
-                sum = fmaf(__high2float(a), __high2float(b), sum);
-            }
-            if (odd) sum = NAN;
+            g = *reinterpret_cast<const uint4*>(p.dOut + t * p.ld_do + col);
+            o = *reinterpret_cast<const uint4*>(p.Out + t * p.ld_out + col);
         }
     }
+    const uint32_t odd = __ballot_sync(0xffffffffu, odd_values(x)) >> (lane & 24) & 0xffu;   // of the row's eight lanes
     if (key) {
-        const uint32_t any = __ballot_sync(0xffffffffu, odd);
-        if (t < rows && (lane & 7) == 0) p.key_odd[(long long)h * p.Tk + t] = (any >> lane) & 0xffu ? 1 : 0;
+        if (in && (lane & 7) == 0) p.key_odd[(long long)h * p.Tk + t] = odd ? 1 : 0;
         return;
     }
-#pragma unroll
-    for (int m = 1; m < 8; m *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    if (t < rows && (lane & 7) == 0) p.delta[(long long)h * p.Tq + t] = sum;
+    float delta = sum8(dot8(g, o));
+    // the keys that the row sees: the first `sk`, then [lo, lo + n)
+    int k0 = 0, lo = 0, sk = 0, n = 0;
+    if (in) {
+        const int s = cq.find((int)t), q0 = cq.begin(s), q1 = cq.begin(s + 1);
+        if (t >= q0 && t < q1) {
+            k0 = ck.begin(s);
+            const int nk = max(ck.begin(s + 1) - k0, 0), pos = nk - (q1 - q0) + (int)t - q0, end = min(pos + p.right + 1, nk);
+            lo = min(max(pos - p.left, 0), nk);
+            n = max(end - lo, 0);
+            sk = max(min(min(p.sinks, lo), end), 0);
+        }
+    }
+    const bool few = sk + n <= FEW && sk + n > 0 && isfinite(delta);
+    const int most = __reduce_max_sync(0xffffffffu, few ? sk + n : 0);
+    if (most > 0) {
+        const float lse = few ? p.Lse[(long long)h * p.Tq + t] : 0.f;
+        const int kcol = h / (p.Hq / p.Hk) * DH + (lane & 7) * 8;
+        float sum = 0.f;
+        for (int i = 0; i < most; ++i) {
+            uint4 k = make_uint4(0, 0, 0, 0), v = k;
+            const bool seen = few && i < sk + n;
+            if (seen) {
+                const long long u = k0 + (i < sk ? i : lo + i - sk);
+                k = *reinterpret_cast<const uint4*>(p.K + u * p.ld_k + kcol);
+                v = *reinterpret_cast<const uint4*>(p.V + u * p.ld_v + kcol);
+            }
+            const float score = sum8(dot8(x, k)), dp = sum8(dot8(g, v));
+            if (seen) sum = fmaf(ex2(fmaf(score, p.scale * kLog2e, -kLog2e * lse)), dp, sum);
+        }
+        if (few) delta = sum;
+    }
+    if (odd) delta = NAN;
+    if (in && (lane & 7) == 0) p.delta[(long long)h * p.Tq + t] = delta;
 }
 
 // after_dkv: the launch before is the one of dK and dV, whose end need not be waited for

@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(KV_THREADS, 1) window_dkv_kernel(const __grid_
                 for (int e = 0; e < COLS; ++e) o[e] = 0;
             }
             if (r < it.keys) {
-                const float f = X ? p.w.scale : 1.f;
+                const float f = X ? p.w.grad_scale : 1.f;
                 if (it.slot >= 0) {
                     float4* dst = reinterpret_cast<float4*>(p.w.partial + it.slot * SLOT + (X * BT + r) * DH + COLS * y);
 #pragma unroll

@@ -101,6 +101,39 @@ def test_window_log_sum_exp_of_few_keys(left):
     assert np.abs(_np(r["lse"]) - ref).max() < 2.0 ** -18 * 16 + 2.0 ** -18
 
 
+@pytest.mark.parametrize("left,right,sinks", [(0, 0, 1), (1, 0, 0), (2, 1, 1), (7, 0, 4), (0, 0, 16)])
+def test_window_gradients_of_few_keys_do_not_lean_on_the_rounded_output(left, right, sinks):
+    """dP - delta of a row with few keys is small beside dP, so delta must not come from Out's bf16 values there: the
+    bound has dS's own rounding (2^-8 in all with the exponential's 2^-10) and fp32's, and no part of Out's."""
+    T = 300
+    q, k, v, g = (_rand(50 + i, T, 1, 64, dtype=BF) for i in range(4))
+    r = L.window_attention(q, k, v, left=left, right=right, sinks=sinks, want_lse=True)
+    b = L.window_attention_backward(q, k, v, r["out"], r["lse"], g, left=left, right=right, sinks=sinks)
+    Q, K, V, G = (_np(t[:, 0]) for t in (q, k, v, g))
+    see = S.visible(T, T, left, right, sinks)
+    assert see.sum(1).max() <= 17
+    s = np.where(see, Q @ K.T / 8, -np.inf)
+    P = np.exp(s - s.max(1, keepdims=True))
+    P /= P.sum(1, keepdims=True)
+    dP = G @ V.T
+    dS = P * (dP - (P * dP).sum(1, keepdims=True))
+    # 2^-17: 64 products in fp32 (2^-18 of the sum of their sizes), in dP and in delta
+    off = (2.0 ** -8 + 2.0 ** -10) * abs(dS) + P * 2.0 ** -17 * (abs(G) @ abs(V).T).max(1, keepdims=True)
+    rows = see.sum(1) <= 16
+    for n, want, tol, at in (("dq", dS @ K / 8, off @ abs(K) / 8, rows), ("dk", dS.T @ Q / 8, off.T @ abs(Q) / 8, slice(sinks, None))):
+        _within(b[n][:, 0][torch.as_tensor(np.arange(T)[at], device="cuda")], want[at], (tol + 2.0 ** -8 * abs(want))[at], n)
+
+
+def test_window_of_one_key_has_no_gradient_but_the_values():
+    """A softmax of one score is constant."""
+    T = 500
+    q, k, v, g = (_rand(60 + i, T, 2, 64, dtype=BF) for i in range(4))
+    r = L.window_attention(q, k, v, left=0, want_lse=True)
+    b = L.window_attention_backward(q, k, v, r["out"], r["lse"], g, left=0)
+    assert torch.equal(r["out"], v) and torch.all(b["dq"] == 0) and torch.all(b["dk"] == 0)
+    _within(b["dv"], _np(g), 2.0 ** -8 * np.abs(_np(g)) * 1.25, "dv")
+
+
 @pytest.mark.parametrize("value", [NAN, math.inf])
 @pytest.mark.parametrize("which", ["q", "k", "v", "g"])
 def test_window_backward_keeps_non_finite_values_to_those_that_meet_them(which, value):
