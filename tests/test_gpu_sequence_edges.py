@@ -119,7 +119,7 @@ def test_window_gradients_of_few_keys_do_not_lean_on_the_rounded_output(left, ri
     dS = P * (dP - (P * dP).sum(1, keepdims=True))
     # 2^-17: 64 products in fp32 (2^-18 of the sum of their sizes), in dP and in delta
     off = (2.0 ** -8 + 2.0 ** -10) * abs(dS) + P * 2.0 ** -17 * (abs(G) @ abs(V).T).max(1, keepdims=True)
-    rows = see.sum(1) <= 16
+    rows = see.sum(1) <= 20
     for n, want, tol, at in (("dq", dS @ K / 8, off @ abs(K) / 8, rows), ("dk", dS.T @ Q / 8, off.T @ abs(Q) / 8, slice(sinks, None))):
         _within(b[n][:, 0][torch.as_tensor(np.arange(T)[at], device="cuda")], want[at], (tol + 2.0 ** -8 * abs(want))[at], n)
 
