@@ -24,6 +24,7 @@
 // channels, the hand-over between tiles being the bound.)  Every wait is bounded.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "attn_prims.cuh"
@@ -489,8 +490,10 @@ cudaError_t launch(Kernel kernel, const GatedScanArgs& a, bool backward, int cs,
     return cudaLaunchKernelEx(&cfg, kernel, a, m);
 }
 
-// The strip's width and the cluster's size: the widest strips (whole 128-byte lines) whose clusters of up to eight
-// CTAs fill more than half of the card, and no more CTAs than there are tiles of rows.
+// The strip's width and the cluster's size: those that have most rows under way at once, the wider strip (whole
+// 128-byte lines) where a narrower one has not a fifth more.  All clusters have to run at once, or the last ones
+// double the time: clusters of up to eight CTAs fill at least 86% of the card's places (120 of 148 with one CTA per
+// SM and eight, 264 of 296 with two).
 struct Shape {
     int lanes, cs;
 };
@@ -498,12 +501,20 @@ inline Shape shape_of(const GatedScanArgs& a, bool backward) {
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const int V = a.bf16 ? 2 : 1, room = sms * (backward ? kPerSmB : kPerSmF), rows = (backward ? kWarpsB : kWarpsF) * kRows;
-    auto strips = [&](int lanes) { return (a.D + lanes * V - 1) / (lanes * V); };
-    Shape q{32, 1};
-    while (q.lanes > 8 && strips(q.lanes / 2) > strips(q.lanes) && kMaxCluster * strips(q.lanes / 2) <= room) q.lanes /= 2;
-    while (q.cs < kMaxCluster && 2LL * q.cs * strips(q.lanes) <= room && (long long)q.cs * (32 / q.lanes) * rows < a.T) q.cs *= 2;
-    return q;
+    const int V = a.bf16 ? 2 : 1, room = sms * (backward ? kPerSmB : kPerSmF) * 865 / 1000, most = backward ? 6 : kMaxCluster;
+    Shape best{32, 1};
+    long long best_rows = 0;
+    for (int lanes = 32; lanes >= 8; lanes /= 2) {
+        const int strips = (a.D + lanes * V - 1) / (lanes * V), tile = 32 / lanes * (backward ? kWarpsB : kWarpsF) * kRows;
+        int cs = std::max(1, std::min(most, room / strips));
+        while (cs > 1 && (long long)(cs - 1) * tile >= a.T) --cs;
+        const long long rows = std::min<long long>((long long)cs * tile, a.T);
+        if (5 * rows > 6 * best_rows) {
+            best = Shape{lanes, cs};
+            best_rows = rows;
+        }
+    }
+    return best;
 }
 
 }  // namespace scan

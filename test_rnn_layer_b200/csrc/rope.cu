@@ -95,14 +95,15 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     bool made = false;
     for (int u0 = threadIdx.x; u0 - threadIdx.x < units; u0 += kBatch * kThreads) {
         uint4 a[kBatch], b[kBatch];
+        Unit q[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int u = u0 + i * kThreads;
             if (u < units) {
-                const Unit q = unit_of(u);
-                const char* x = X + (q.r * p.ld_x + q.col) * E;
+                q[i] = unit_of(u);
+                const char* x = X + (q[i].r * p.ld_x + q[i].col) * E;
                 a[i] = __ldcs(reinterpret_cast<const uint4*>(x));
-                if (q.second) b[i] = __ldcs(reinterpret_cast<const uint4*>(x + q.second * E));
+                if (q[i].second) b[i] = __ldcs(reinterpret_cast<const uint4*>(x + q[i].second * E));
             }
         }
         if (!made) {
@@ -114,13 +115,12 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         for (int i = 0; i < kBatch; ++i) {
             const int u = u0 + i * kThreads;
             if (u >= units) continue;
-            const Unit q = unit_of(u);
-            char* y = Y + (q.r * p.ld_y + q.col) * E;
-            if (q.pair >= 0) {
-                const float2* w = cs + q.r * pairs + q.pair;
+            char* y = Y + (q[i].r * p.ld_y + q[i].col) * E;
+            if (q[i].pair >= 0) {
+                const float2* w = cs + q[i].r * pairs + q[i].pair;
                 float v0[N], v1[N];
                 Piece<BF>::unpack(a[i], v0);
-                if (q.second) Piece<BF>::unpack(b[i], v1);
+                if (q[i].second) Piece<BF>::unpack(b[i], v1);
                 if constexpr (HALF) {
 #pragma unroll
                     for (int e = 0; e < N; ++e) {
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                         v0[e] = x0 * c.x - x1 * c.y;
                         v0[e + 1] = x0 * c.y + x1 * c.x;
                     }
-                    if (q.second) {
+                    if (q[i].second) {
 #pragma unroll
                         for (int e = 0; e < N; e += 2) {
                             const float x0 = v1[e], x1 = v1[e + 1];
@@ -147,10 +147,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                     }
                 }
                 a[i] = Piece<BF>::pack(v0);
-                if (q.second) b[i] = Piece<BF>::pack(v1);
+                if (q[i].second) b[i] = Piece<BF>::pack(v1);
             }
             __stcs(reinterpret_cast<uint4*>(y), a[i]);
-            if (q.second) __stcs(reinterpret_cast<uint4*>(y + q.second * E), b[i]);
+            if (q[i].second) __stcs(reinterpret_cast<uint4*>(y + q[i].second * E), b[i]);
         }
     }
 }

@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
 
 // delta[h, t] = sum of dO Out over the head's columns, NaN where the row's q is not finite (so that delta is finite
 // only where q, dO and Out are), and key_odd[h, u]: whether the key is not finite.  Eight lanes a row of 64, 16
-// bytes each; a warp takes four consecutive rows of one head.  Also looks over the offsets.
+// bytes each; a warp takes four consecutive rows of a few heads.  Also looks over the offsets.
 //
 // Out is rounded to bf16, and dP - delta of a row with few keys is small beside dP: with two keys the rounding put
 // dQ and dK off by 0.0055 in the norm (0.0025 with many).  So a row of at most FEW keys gets delta = sum_u P_u dP_u,
@@ -401,6 +401,8 @@ __device__ __forceinline__ float sum8(float v) {   // over the eight lanes of a 
     return v;
 }
 
+constexpr int DELTA_HEADS = 2;   // of a warp: all loads first, the rows' sequences are looked up once
+
 __global__ void __launch_bounds__(256) window_delta_kernel(const WindowArgs p, long long q_warps, long long warps) {
     const SeqOffsets cq{p.cu_q, p.n_seq, p.Tq}, ck{p.cu_k, p.n_seq, p.Tk};
     if (blockIdx.x == 0) {
@@ -412,24 +414,33 @@ __global__ void __launch_bounds__(256) window_delta_kernel(const WindowArgs p, l
     if (w >= warps) return;
     const bool key = w >= q_warps;
     if (key) w -= q_warps;
-    const int heads = key ? p.Hk : p.Hq, h = (int)(w % heads), rows = key ? p.Tk : p.Tq;
-    const long long t = w / heads * 4 + (lane >> 3);
-    const int col = h * DH + (lane & 7) * 8;
+    const int heads = key ? p.Hk : p.Hq, parts = (heads + DELTA_HEADS - 1) / DELTA_HEADS, rows = key ? p.Tk : p.Tq;
+    const int h0 = (int)(w % parts) * DELTA_HEADS, h1 = min(h0 + DELTA_HEADS, heads);
+    const long long t = w / parts * 4 + (lane >> 3);
     const bool in = t < rows;
-    uint4 x = make_uint4(0, 0, 0, 0), g = x, o = x;
-    if (in) {
-        x = *reinterpret_cast<const uint4*>((key ? p.K + t * p.ld_k : p.Q + t * p.ld_q) + col);
-        if (!key) {
-            g = *reinterpret_cast<const uint4*>(p.dOut + t * p.ld_do + col);
-            o = *reinterpret_cast<const uint4*>(p.Out + t * p.ld_out + col);
-        }
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    // this lane's row and columns of head 0
+    const int col0 = (lane & 7) * 8;
+    uint4 xs[DELTA_HEADS], gs[DELTA_HEADS], os[DELTA_HEADS];
+#pragma unroll
+    for (int i = 0; i < DELTA_HEADS; ++i) {
+        const int col = (h0 + i) * DH + col0;
+        const bool here = in && h0 + i < h1;
+        xs[i] = here ? *reinterpret_cast<const uint4*>((key ? p.K + t * p.ld_k : p.Q + t * p.ld_q) + col) : none;
+        gs[i] = here && !key ? *reinterpret_cast<const uint4*>(p.dOut + t * p.ld_do + col) : none;
+        os[i] = here && !key ? *reinterpret_cast<const uint4*>(p.Out + t * p.ld_out + col) : none;
     }
-    const uint32_t odd = __ballot_sync(0xffffffffu, odd_values(x)) >> (lane & 24) & 0xffu;   // of the row's eight lanes
     if (key) {
-        if (in && (lane & 7) == 0) p.key_odd[(long long)h * p.Tk + t] = odd ? 1 : 0;
+#pragma unroll
+        for (int i = 0; i < DELTA_HEADS; ++i) {
+            const int h = h0 + i;
+            if (h >= h1) break;
+            const uint4 x = xs[i];
+            const uint32_t odd = __ballot_sync(0xffffffffu, odd_values(x)) >> (lane & 24) & 0xffu;   // of the row's eight lanes
+            if (in && (lane & 7) == 0) p.key_odd[(long long)h * p.Tk + t] = odd ? 1 : 0;
+        }
         return;
     }
-    float delta = sum8(dot8(g, o));
     // the keys that the row sees: the first `sk`, then [lo, lo + n)
     int k0 = 0, lo = 0, sk = 0, n = 0;
     if (in) {
@@ -442,27 +453,35 @@ __global__ void __launch_bounds__(256) window_delta_kernel(const WindowArgs p, l
             sk = max(min(min(p.sinks, lo), end), 0);
         }
     }
-    const bool few = sk + n <= FEW && sk + n > 0 && isfinite(delta);
-    const int most = __reduce_max_sync(0xffffffffu, few ? sk + n : 0);
-    if (most > 0) {
-        const float lse = few ? p.Lse[(long long)h * p.Tq + t] : 0.f;
-        const int kcol = h / (p.Hq / p.Hk) * DH + (lane & 7) * 8;
-        float sum = 0.f;
-        for (int i = 0; i < most; ++i) {
-            uint4 k = make_uint4(0, 0, 0, 0), v = k;
-            const bool seen = few && i < sk + n;
-            if (seen) {
-                const long long u = k0 + (i < sk ? i : lo + i - sk);
-                k = *reinterpret_cast<const uint4*>(p.K + u * p.ld_k + kcol);
-                v = *reinterpret_cast<const uint4*>(p.V + u * p.ld_v + kcol);
+    const int most = __reduce_max_sync(0xffffffffu, sk + n <= FEW ? sk + n : 0);
+#pragma unroll
+    for (int e = 0; e < DELTA_HEADS; ++e) {
+        const int h = h0 + e;
+        if (h >= h1) break;
+        const uint4 x = xs[e], g = gs[e], o = os[e];
+        const uint32_t odd = __ballot_sync(0xffffffffu, odd_values(x)) >> (lane & 24) & 0xffu;
+        float delta = sum8(dot8(g, o));
+        if (most > 0) {
+            const bool few = sk + n <= FEW && sk + n > 0 && isfinite(delta);
+            const float lse = few ? p.Lse[(long long)h * p.Tq + t] : 0.f;
+            const int kcol = h / (p.Hq / p.Hk) * DH + col0;
+            float sum = 0.f;
+            for (int i = 0; i < most; ++i) {
+                uint4 k = none, v = none;
+                const bool seen = few && i < sk + n;
+                if (seen) {
+                    const long long u = k0 + (i < sk ? i : lo + i - sk);
+                    k = *reinterpret_cast<const uint4*>(p.K + u * p.ld_k + kcol);
+                    v = *reinterpret_cast<const uint4*>(p.V + u * p.ld_v + kcol);
+                }
+                const float score = sum8(dot8(x, k)), dp = sum8(dot8(g, v));
+                if (seen) sum = fmaf(ex2(fmaf(score, p.scale * kLog2e, -kLog2e * lse)), dp, sum);
             }
-            const float score = sum8(dot8(x, k)), dp = sum8(dot8(g, v));
-            if (seen) sum = fmaf(ex2(fmaf(score, p.scale * kLog2e, -kLog2e * lse)), dp, sum);
+            if (few) delta = sum;
         }
-        if (few) delta = sum;
+        if (odd) delta = NAN;
+        if (in && (lane & 7) == 0) p.delta[(long long)h * p.Tq + t] = delta;
     }
-    if (odd) delta = NAN;
-    if (in && (lane & 7) == 0) p.delta[(long long)h * p.Tq + t] = delta;
 }
 
 // after_dkv: the launch before is the one of dK and dV, whose end need not be waited for
@@ -500,7 +519,8 @@ cudaError_t launch_window_attention_backward(const WindowArgs& a, cudaStream_t s
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     {
         LaunchScope scope("window_delta", s);
-        const long long q = ((long long)a.Tq + 3) / 4 * a.Hq, warps = q + ((long long)a.Tk + 3) / 4 * a.Hk;
+        const auto parts = [](int heads) { return (heads + DELTA_HEADS - 1) / DELTA_HEADS; };
+        const long long q = ((long long)a.Tq + 3) / 4 * parts(a.Hq), warps = q + ((long long)a.Tk + 3) / 4 * parts(a.Hk);
         window_delta_kernel<<<(unsigned)((warps + 7) / 8 ? (warps + 7) / 8 : 1), 256, 0, s>>>(a, q, warps);
     }
     cudaError_t e = cudaGetLastError();
