@@ -7,6 +7,7 @@ library is missing or fails to load, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -530,28 +531,32 @@ def ttt_gated_scan_step(B, D, form, x_dtype, F, ld_f, X, ld_x, H, H_out, Y, ld_y
                                          _stream(stream)))
 
 
-class _Place:
-    """Runs a call with the tensors' device current and, if one is given, on `stream`
-    (new tensors then belong to that stream)."""
+class _Elsewhere:
+    """The tensors' device current and, if one is given, `stream` (new tensors then belong to it)."""
 
     __slots__ = ("stack",)
 
-    def __init__(self, tensor, stream):
-        self.stack = None
-        if stream is None and tensor.get_device() == torch.cuda.current_device():
-            return
-        self.stack = [torch.cuda.device(tensor.device)]
+    def __init__(self, device, stream):
+        self.stack = [torch.cuda.device(device)]
         if isinstance(stream, torch.cuda.Stream):
             self.stack.append(torch.cuda.stream(stream))
 
     def __enter__(self):
-        for c in self.stack or ():
+        for c in self.stack:
             c.__enter__()
 
     def __exit__(self, *exc):
-        for c in reversed(self.stack or ()):
+        for c in reversed(self.stack):
             c.__exit__(*exc)
         return False
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _place(device, stream):
+    """What a call on tensors of `device` runs within."""
+    return _HERE if stream is None and device == torch.cuda.current_device() else _Elsewhere(device, stream)
 
 
 # The checks run on every call of a few microseconds: messages are put together only for a refusal.
@@ -567,14 +572,21 @@ def _rows(x, shape, dtype, device, name) -> int:
     if x.shape != shape:
         raise ValueError(f"{name}: shape {tuple(x.shape)}, wanted {tuple(shape)}")
     strides = x.stride()
-    width = 1
-    for k in range(len(shape) - 1, 0, -1):
-        if strides[k] != width and shape[k] > 1:
-            raise ValueError(f"{name}: the columns of a row must be dense, strides {strides}")
-        width *= shape[k]
-    ld = strides[0] if shape[0] > 1 else -(-width // 8) * 8
-    if ld >= 2 ** 31:
-        raise ValueError(f"{name}: row stride {ld}")
+    ld = strides[0]
+    if len(strides) == 3:
+        dense = strides[2] == 1 and strides[1] == shape[2]
+    else:
+        dense = len(strides) == 2 and strides[1] == 1
+    if not dense or shape[0] < 2 or ld >= 2 ** 31:     # an axis of one element may have any stride
+        width = 1
+        for k in range(len(shape) - 1, 0, -1):
+            if strides[k] != width and shape[k] > 1:
+                raise ValueError(f"{name}: the columns of a row must be dense, strides {strides}")
+            width *= shape[k]
+        if shape[0] < 2:
+            ld = -(-width // 8) * 8
+        if ld >= 2 ** 31:
+            raise ValueError(f"{name}: row stride {ld}")
     return ld
 
 
@@ -641,7 +653,7 @@ def rope(x, positions=None, *, pos0: int = 0, rot: int | None = None, layout: st
                       sc.get("low", 0.0), sc.get("high", 0.0), sc.get("amplitude", 1.0))
     if positions is not None:
         _dense(positions, (T,), torch.int32, dev, "positions")
-    with _Place(x, stream):
+    with _place(dev, stream):
         if out is None:
             out = torch.empty(shape, dtype=x.dtype, device=dev)
         check(lib().ttt_rope(desc.ref, x.data_ptr(), _rows(x, shape, x.dtype, dev, "x"), out.data_ptr(),
@@ -673,7 +685,7 @@ def window_attention(q, k, v, *, left: int, right: int = 0, sinks: int = 0, cu_q
          "cu_q and cu_k: both or neither, of the same length")
     desc = _window_desc(q, k, n_seq, left, right, sinks, scale)
     lds = [_rows(q, q.shape, bf, dev, "q"), _rows(k, k.shape, bf, dev, "k"), _rows(v, k.shape, bf, dev, "v")]
-    with _Place(q, stream):
+    with _place(dev, stream):
         ws = _space(workspace, lambda: ttt_window_attention_workspace_size(desc), dev)
         if out is None:   # rows outside the sequences are not written: they start as zeros
             out = (torch.empty if cu_q is None else torch.zeros)(q.shape, dtype=bf, device=dev)
@@ -702,7 +714,7 @@ def window_attention_backward(q, k, v, out, lse, dout, *, left: int, right: int 
          "cu_q and cu_k: both or neither, of the same length")
     desc = _window_desc(q, k, n_seq, left, right, sinks, scale)
     _dense(lse, (q.shape[1], q.shape[0]), torch.float32, dev, "lse")
-    with _Place(q, stream):
+    with _place(dev, stream):
         ws = _space(workspace, lambda: ttt_window_attention_backward_workspace_size(desc), dev)
         new = torch.empty if cu_q is None else torch.zeros
         dq = new(q.shape, dtype=bf, device=dev) if dq is None else dq
@@ -754,7 +766,7 @@ def window_attention_decode(q, cache_k, cache_v, lens, *, left: int, sinks: int 
         shape = (q.shape[0], cache_k.shape[2], q.shape[2])
         ld_new = _rows(k_new, shape, bf, dev, "k_new")
         _ask(_rows(v_new, shape, bf, dev, "v_new") == ld_new, "k_new and v_new need the same row stride")
-    with _Place(q, stream):
+    with _place(dev, stream):
         if workspace is None:
             workspace = _space(None, lambda: ttt_window_attention_decode_workspace_size(desc), dev).zero_()
         if out is None:
@@ -791,7 +803,7 @@ def gated_scan(f, x, *, form: str = "convex", dirs: str = "fwd", cu=None, h0=Non
     state = (n_seq, x.shape[1])
     if h0 is not None:
         _dense(h0, state, torch.float32, dev, "h0")
-    with _Place(x, stream):
+    with _place(dev, stream):
         ws = _space(workspace, lambda: ttt_gated_scan_workspace_size(desc), dev)
         if y is None:
             y = (torch.empty if cu is None else torch.zeros)(x.shape, dtype=x.dtype, device=dev)
@@ -823,7 +835,7 @@ def gated_scan_backward(f, x, dy, chunk_states, *, form: str = "convex", dirs: s
     for t, name in ((h0, "h0"), (dh_T, "dh_T")):
         if t is not None:
             _dense(t, state, torch.float32, dev, name)
-    with _Place(x, stream):
+    with _place(dev, stream):
         ws = _space(workspace, lambda: ttt_gated_scan_workspace_size(desc), dev)
         new = torch.empty if cu is None else torch.zeros
         df = new(x.shape, dtype=x.dtype, device=dev) if df is None else df
@@ -848,7 +860,7 @@ def gated_scan_step(f, x, h, *, form: str = "convex", y=None, h_out=None, stream
     dev, code = x.get_device(), _dtype_code(x, "x")
     B, D = x.shape
     _dense(h, (B, D), torch.float32, dev, "h")
-    with _Place(x, stream):
+    with _place(dev, stream):
         y = torch.empty((B, D), dtype=x.dtype, device=dev) if y is None else y
         h_out = torch.empty_like(h) if h_out is None else _dense(h_out, (B, D), torch.float32, dev, "h_out")
         check(lib().ttt_gated_scan_step(
