@@ -304,3 +304,79 @@ def test_operators_refuse_tensors_of_the_wrong_place_or_size():
     with pytest.raises(L.TTTError):     # a workspace of the forward pass is too small for the backward pass
         f = L.window_attention(q, q.clone(), q.clone(), left=3, want_lse=True)
         L.window_attention_backward(q, q.clone(), q.clone(), f["out"], f["lse"], q.clone(), left=3, workspace=f["workspace"])
+
+
+def test_row_strides_past_32_bits():
+    """Rows 2^30 elements apart: every offset of the last rows needs 64 bits."""
+    T, ld = 3, 2 ** 30
+    big = torch.empty((T - 1) * ld + 4096, dtype=BF, device="cuda")
+
+    def far(col, *shape):       # [T, *shape] at columns col...
+        n = math.prod(shape)
+        t = big.as_strided((T, *shape), (ld, 64, 1) if len(shape) == 2 else (ld, 1), col)
+        return t.copy_(_rand(col + n, T, *shape, dtype=BF))
+
+    q, k, v, g = (far(512 * i, 2, 64) for i in range(4))
+    near = [t.contiguous() for t in (q, k, v, g)]
+    out, dq, dk, dv = (far(512 * i, 2, 64) for i in range(4, 8))
+    r = L.window_attention(q, k, v, left=5, want_lse=True, out=out)
+    b = L.window_attention_backward(q, k, v, out, r["lse"], g, left=5, dq=dq, dk=dk, dv=dv)
+    r1 = L.window_attention(*near[:3], left=5, want_lse=True)
+    b1 = L.window_attention_backward(*near[:3], r1["out"], r1["lse"], near[3], left=5)
+    assert torch.equal(out, r1["out"]) and torch.equal(r["lse"], r1["lse"])
+    assert all(torch.equal(b[n], b1[n]) for n in ("dq", "dk", "dv"))
+    assert torch.equal(L.rope(q, out=out), L.rope(near[0]))
+    f, x, dy = (far(512 * i, 128) for i in range(3))
+    near = [t.contiguous() for t in (f, x, dy)]
+    y, df, dx = (far(512 * i, 128) for i in range(3, 6))
+    s = L.gated_scan(f, x, y=y, want_chunk_states=True)
+    c = L.gated_scan_backward(f, x, dy, s["chunk_states"], df=df, dx=dx)
+    s1 = L.gated_scan(*near[:2], want_chunk_states=True)
+    c1 = L.gated_scan_backward(*near, s1["chunk_states"])
+    assert torch.equal(y, s1["y"]) and torch.equal(df, c1["df"]) and torch.equal(dx, c1["dx"])
+    h = _rand(9, T, 128)
+    y1, h1 = L.gated_scan_step(f, x, h, y=y)
+    y2, h2 = L.gated_scan_step(*near[:2], h)
+    assert torch.equal(y1, y2) and torch.equal(h1, h2)
+
+
+def test_a_training_block_in_one_graph():
+    """rotary positions, attention and recurrence, forward and backward, captured together and replayed on new inputs."""
+    T, Hq, Hk = 900, 4, 2
+    W = Hq * 64
+    cu = _ints([0, 400, 401, 850])
+    ins = [_rand(1, T, Hq + 2 * Hk, 64, dtype=BF), _rand(2, T, W, dtype=BF), _rand(3, T, W, dtype=BF)]
+    mask = dict(left=100, sinks=2, cu_q=cu, cu_k=cu, check_status=False)
+    like = torch.zeros(T, Hq + Hk, 64, dtype=BF, device="cuda")
+    ws = L.window_attention_workspace(like[:, :Hq], like[:, Hq:], 3, backward=True)
+    sw = L.gated_scan_workspace(ins[1], 3)
+
+    def step():
+        qkv, f, dy = ins
+        turned = L.rope(qkv[:, :Hq + Hk])
+        q, k, v = turned[:, :Hq], turned[:, Hq:], qkv[:, Hq + Hk:]
+        a = L.window_attention(q, k, v, want_lse=True, workspace=ws, **mask)
+        x = a["out"].view(T, W)
+        s = L.gated_scan(f, x, cu=cu, want_chunk_states=True, workspace=sw, check_status=False)
+        sb = L.gated_scan_backward(f, x, dy, s["chunk_states"], cu=cu, workspace=sw, check_status=False)
+        ab = L.window_attention_backward(q, k, v, a["out"], a["lse"], sb["dx"].view(T, Hq, 64), workspace=ws, **mask)
+        back = L.rope(torch.cat([ab["dq"], ab["dk"]], 1), inverse=True)
+        return [a["out"], a["lse"], s["y"], sb["df"], sb["dx"], ab["dv"], back]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            out = step()
+    s.synchronize()
+    for i, t in enumerate(ins):
+        t.copy_(_rand(20 + i, *t.shape, dtype=BF))
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in out]
+    for a, b in zip(got, step()):
+        assert torch.equal(a, b)
+    assert L.ttt_mlp_status(ws) == L.TTT_OK and L.ttt_mlp_status(sw) == L.TTT_OK
