@@ -580,7 +580,8 @@ TTT_API ttt_status ttt_window_attention_backward(const ttt_window_desc* desc, co
  *   lens      int [B] in device memory, the tokens so far, this one included.
  *             0: an idle request: Out = 0, nothing is stored.  Negative
  *             lengths count as 0 and set the status (TTT_ERR_INVALID_ARG).
- *   Q, Out    bf16 [B, ld].  No two requests may share cache slots.
+ *   Q, Out    bf16 [B, ld]; Out must not overlap Q, K_new or V_new.  No two
+ *             requests may store into the same cache slots.
  *   workspace ttt_window_attention_decode_workspace_size(desc) bytes, 256-byte
  *             aligned.  The caller zeroes it once after allocating it; the
  *             call does not clear the status word (one launch less), which
@@ -630,7 +631,8 @@ TTT_API ttt_status ttt_window_attention_decode(const ttt_window_decode_desc* des
  * A value that is not finite stays with its sequence and channel.
  *
  * Step, for serving: one token of each of B rows: H_out = a H + s(a) x (fp32
- * [B, D] dense; H_out may be H), Y (may be NULL) = H_out rounded.
+ * [B, D] dense; H_out may be H), Y (may be NULL) = H_out rounded.  The outputs
+ * overlap nothing else.
  */
 typedef enum { TTT_GATE_SUM = 0, TTT_GATE_CONVEX = 1, TTT_GATE_UNIT = 2 } ttt_gate_form;
 

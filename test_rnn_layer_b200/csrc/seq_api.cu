@@ -195,6 +195,8 @@ extern "C" TTT_API ttt_status ttt_window_attention(const ttt_window_desc* desc, 
     if (overlap(Out, q.Tq, ld_out, wq, 2, Q, q.Tq, ld_q, wq, 2) || overlap(Out, q.Tq, ld_out, wq, 2, K, q.Tk, ld_k, wk, 2) ||
         overlap(Out, q.Tq, ld_out, wq, 2, V, q.Tk, ld_v, wk, 2))
         return set_error(TTT_ERR_INVALID_ARG, "Out overlaps Q, K or V");
+    if (Xres != Out && overlap(Out, q.Tq, ld_out, wq, 2, Xres, q.Tq, ld_out, wq, 2))
+        return set_error(TTT_ERR_INVALID_ARG, "Xres overlaps Out and is not Out itself");
     a.Xres = static_cast<const __nv_bfloat16*>(Xres);
     a.Out = static_cast<__nv_bfloat16*>(Out);
     a.ld_out = ld_out;
@@ -295,8 +297,11 @@ extern "C" TTT_API ttt_status ttt_window_attention_decode(const ttt_window_decod
         SEQ_NEED(need_rows(K_new, ld_new, (long long)q.Hk * q.d, "K_new"));
         SEQ_NEED(need_rows(V_new, ld_new, (long long)q.Hk * q.d, "V_new"));
     }
-    if (overlap(Out, q.B, ld_out, (long long)q.Hq * q.d, 2, Q, q.B, ld_q, (long long)q.Hq * q.d, 2))
-        return set_error(TTT_ERR_INVALID_ARG, "Out overlaps Q");
+    const long long wq = (long long)q.Hq * q.d, wk = (long long)q.Hk * q.d;
+    if (overlap(Out, q.B, ld_out, wq, 2, Q, q.B, ld_q, wq, 2) || overlap(Out, q.B, ld_out, wq, 2, K_new, q.B, ld_new, wk, 2) ||
+        overlap(Out, q.B, ld_out, wq, 2, V_new, q.B, ld_new, wk, 2))
+        return set_error(TTT_ERR_INVALID_ARG, "Out overlaps Q, K_new or V_new");
+    if (q.ld_request == 0 && q.B > 1 && K_new) return set_error(TTT_ERR_INVALID_ARG, "the requests store into the same cache slots");
     WindowDecodeArgs a{};
     a.B = q.B; a.Hq = q.Hq; a.Hk = q.Hk; a.slots = q.slots; a.left = q.left; a.sinks = q.sinks; a.scale = q.scale;
     a.ld_request = q.ld_request; a.ld_slot = q.ld_slot; a.ld_head = q.ld_head;
@@ -427,6 +432,9 @@ extern "C" TTT_API ttt_status ttt_gated_scan_step(int B, int D, ttt_gate_form fo
         return set_error(TTT_ERR_INVALID_ARG, "H_out overlaps H and is not H itself");
     if (Y && (overlap(Y, B, ld_y, D, e, F, B, ld_f, D, e) || overlap(Y, B, ld_y, D, e, X, B, ld_x, D, e)))
         return set_error(TTT_ERR_INVALID_ARG, "Y overlaps F or X");
+    if (overlap(H_out, B, D, D, 4, F, B, ld_f, D, e) || overlap(H_out, B, D, D, 4, X, B, ld_x, D, e) ||
+        overlap(Y, B, ld_y, D, e, H, B, D, D, 4) || overlap(Y, B, ld_y, D, e, H_out, B, D, D, 4))
+        return set_error(TTT_ERR_INVALID_ARG, "H_out overlaps F or X, or Y overlaps a state");
     SEQ_TRY(launch_gated_scan_step(B, D, (int)form, x_dtype == TTT_BF16, F, ld_f, X, ld_x, H, H_out, Y, ld_y,
                                    reinterpret_cast<cudaStream_t>(stream)));
     return TTT_OK;

@@ -690,7 +690,7 @@ def window_attention(q, k, v, *, left: int, right: int = 0, sinks: int = 0, cu_q
         if out is None:   # rows outside the sequences are not written: they start as zeros
             out = (torch.empty if cu_q is None else torch.zeros)(q.shape, dtype=bf, device=dev)
         if lse is None and want_lse:
-            lse = (torch.empty if cu_q is None else torch.zeros)((q.shape[1], q.shape[0]), device=dev)
+            lse = (torch.empty if cu_q is None else torch.zeros)((q.shape[1], q.shape[0]), dtype=torch.float32, device=dev)
         if lse is not None:
             _dense(lse, (q.shape[1], q.shape[0]), torch.float32, dev, "lse")
         ld_out = _rows(out, q.shape, bf, dev, "out")
@@ -739,7 +739,7 @@ def _decode_desc(q, cache, left, sinks, scale):
     B, slots, Hk, d = cache.shape
     s0, s1, s2, _ = cache.stride()
     return _decode_sizes(B, q.shape[1], Hk, d, slots, left, sinks, d ** -0.5 if scale is None else scale,
-                         s0, s1 if slots > 1 else d, s2)
+                         s0 if B > 1 else 0, s1 if slots > 1 else d, s2 if Hk > 1 else 0)   # (axes of one: any stride)
 
 
 def window_attention_decode_workspace(q, cache) -> torch.Tensor:
@@ -808,13 +808,13 @@ def gated_scan(f, x, *, form: str = "convex", dirs: str = "fwd", cu=None, h0=Non
         if y is None:
             y = (torch.empty if cu is None else torch.zeros)(x.shape, dtype=x.dtype, device=dev)
         if h_T is None and want_state:
-            h_T = torch.empty(state, device=dev)
+            h_T = torch.empty(state, dtype=torch.float32, device=dev)
         if h_T is not None:
             _dense(h_T, state, torch.float32, dev, "h_T")
         if chunk_states is not None:
             _dense(chunk_states, (ttt_gated_scan_chunk_states_size(desc) // 4,), torch.float32, dev, "chunk_states")
         elif want_chunk_states:
-            chunk_states = torch.empty(ttt_gated_scan_chunk_states_size(desc) // 4, device=dev)
+            chunk_states = torch.empty(ttt_gated_scan_chunk_states_size(desc) // 4, dtype=torch.float32, device=dev)
         check(lib().ttt_gated_scan(desc.ref, _at(cu), f.data_ptr(), ld_f, x.data_ptr(), ld_x, _at(h0), y.data_ptr(),
                                    _rows(y, x.shape, x.dtype, dev, "y"), _at(h_T), _at(chunk_states), ws.data_ptr(),
                                    ws.numel(), _stream(stream)), "ttt_gated_scan")
@@ -841,7 +841,7 @@ def gated_scan_backward(f, x, dy, chunk_states, *, form: str = "convex", dirs: s
         df = new(x.shape, dtype=x.dtype, device=dev) if df is None else df
         dx = new(x.shape, dtype=x.dtype, device=dev) if dx is None else dx
         if dh0 is None and want_dh0:
-            dh0 = torch.empty(state, device=dev)
+            dh0 = torch.empty(state, dtype=torch.float32, device=dev)
         if dh0 is not None:
             _dense(dh0, state, torch.float32, dev, "dh0")
         dt, sx = x.dtype, x.shape

@@ -380,3 +380,31 @@ def test_a_training_block_in_one_graph():
     for a, b in zip(got, step()):
         assert torch.equal(a, b)
     assert L.ttt_mlp_status(ws) == L.TTT_OK and L.ttt_mlp_status(sw) == L.TTT_OK
+
+
+@pytest.mark.parametrize("default", [torch.bfloat16, torch.float64])
+def test_buffers_keep_their_type_under_another_default(default):
+    """What the wrappers allocate is fp32 where the kernels write fp32, whatever torch's default type."""
+    f, x, dy = (_rand(i, 40, 64, dtype=BF) for i in range(3))
+    q, k, v, g = (_rand(9 + i, 40, 2, 64, dtype=BF) for i in range(4))
+    cache = torch.stack([k[:8], v[:8]])
+
+    def run():
+        s = L.gated_scan(f, x, want_state=True, want_chunk_states=True)
+        b = L.gated_scan_backward(f, x, dy, s["chunk_states"], want_dh0=True)
+        r = L.window_attention(q, k, v, left=7, want_lse=True)
+        w = L.window_attention_backward(q, k, v, r["out"], r["lse"], g, left=7)
+        d = L.window_attention_decode(q[:1], cache[:1], cache[1:], _ints([5]), left=7)
+        y, h = L.gated_scan_step(f[:1], x[:1], s["h_T"])
+        return [s["y"], s["h_T"], s["chunk_states"], b["df"], b["dx"], b["dh0"], r["out"], r["lse"], w["dq"], w["dk"],
+                w["dv"], d["out"], y, h, L.rope(q)]
+
+    want = run()
+    before = torch.get_default_dtype()
+    try:
+        torch.set_default_dtype(default)
+        got = run()
+    finally:
+        torch.set_default_dtype(before)
+    for a, b in zip(got, want):
+        assert a.dtype is b.dtype and torch.equal(a, b)

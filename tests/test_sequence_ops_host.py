@@ -219,6 +219,17 @@ def test_step_refusals(no_gpu, bad):
     assert L.ttt_gated_scan_step(*c.values(), 0) == L.TTT_ERR_INVALID_ARG and L.ttt_last_error()
 
 
+def test_outputs_that_overlap_other_arrays_are_refused(no_gpu):
+    bad = L.TTT_ERR_INVALID_ARG
+    assert _window(Xres=P[3] + 512) == bad            # a residual one row off in Out
+    assert _window(Xres=P[3] - 16) == bad
+    assert _decode(Out=P[1]) == bad and _decode(Out=P[2] - 256) == bad
+    assert _decode(ld_request=0) == bad               # every request would store into the same slots
+    c = dict(B=4, D=64, form=0, dt=L.TTT_BF16, F=P[0], ld_f=64, X=P[1], ld_x=64, H=P[2], H_out=P[3], Y=P[4], ld_y=64)
+    for kw in (dict(Y=P[2]), dict(Y=P[3] + 512), dict(H_out=P[0]), dict(H_out=P[1])):
+        assert L.ttt_gated_scan_step(*{**c, **kw}.values(), 0) == bad, kw
+
+
 def test_struct_layouts_match_the_header():
     """Sizes of the descriptors as a C compiler lays them out (natural alignment, no packing)."""
     assert ctypes.sizeof(L.ttt_rope_desc) == 7 * 4 + 4 + 6 * 8
