@@ -40,7 +40,8 @@ constexpr int OFF_Q = 0;                          // Q_A, Q_B
 constexpr int OFF_KV = 2 * TILE;                  // stage s: K at OFF_KV + 2 s TILE, V after it
 constexpr int OFF_BAR = OFF_KV + NST * 2 * TILE;
 constexpr int OFF_ML = OFF_BAR + 512;             // [2][2][128] float2: a row's maximum and sum in each half
-constexpr int SMEM_BYTES = OFF_ML + 4096 + 1024;
+constexpr int OFF_ORDER = OFF_ML + 4096;          // [kOrder] bytes
+constexpr int SMEM_BYTES = OFF_ORDER + win::kOrder + 1024;
 constexpr uint32_t TM_X = 256, TM_O = 128;        // tile X's S at TM_X X + 64 y, its O at TM_X X + TM_O + 64 y
 constexpr float kLazy = 8.0f;                     // log2 of the largest unscaled exponential
 constexpr int EMU = 1;                            // pairs of every 8 whose 2^x runs on the FMA pipe
@@ -70,6 +71,7 @@ struct FwdArgs {
     CUtensorMap mapQ, mapK, mapV;   // bf16 [rows x heads*64 columns], 64 x 128 boxes
     WindowArgs w;
     long long n_items;
+    int sorted;                     // few blocks of unequal work: drawn by it
     float c;                        // scale * log2(e)
 };
 
@@ -196,6 +198,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
         tc::tma_prefetch_desc(&p.mapK);
         tc::tma_prefetch_desc(&p.mapV);
     }
+    uint8_t* order = sm + OFF_ORDER;
+    long long n_items = p.n_items;
+    if (warp == SOFT && p.sorted)   // (a tile of one row block costs three fifths of one of both)
+        n_items = (long long)p.w.Hq * win::order_blocks(order, (int)p.n_items / p.w.Hq, [&](int b) {
+            Item q;
+            return q.load(p.w, (long long)b * p.w.Hq) ? q.nt * (q.rows > BQ ? 5 : 3) : -1;
+        });
     if (warp == SOFT + 1) {
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
@@ -221,12 +230,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
         if (tc::elect_one()) {
             int gkv = 0, n = 0;
             bool ok = true;
-            for (int w = blockIdx.x, next, k = 0; ok && !*abort_flag; w = next) {
-                if (w >= p.n_items) {
+            for (int ticket = blockIdx.x, next, k = 0; ok && !*abort_flag; ticket = next) {
+                if (ticket >= n_items) {
                     ok = items.put(k, -1);
                     break;
                 }
                 next = gridDim.x + atomicAdd(p.w.status + kTicket, 1);
+                const int w = p.sorted ? order[ticket / p.w.Hq] * p.w.Hq + ticket % p.w.Hq : ticket;
                 if (!it.load(p.w, w)) continue;
                 if (!items.put(k++, w)) { ok = false; break; }
                 if (n > 0 && !tc::mbar_wait(bars + B_QE, (n - 1) & 1, abort_flag, win::kItemWait)) { ok = false; break; }
@@ -532,6 +542,7 @@ cudaError_t launch_window_attention(const WindowArgs& a, cudaStream_t s) {
     int dev = 0, sms = 148;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    p.sorted = win::ordered(a, p.n_items / a.Hq, sms);
     cudaError_t e = cudaFuncSetAttribute(window_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
     LaunchScope scope("window_attn", s);

@@ -20,7 +20,8 @@ constexpr int ROWS = 2 * BT, NST = 4;
 constexpr int OFF_Q = 0;                          // Q_A, Q_B, dO_A, dO_B
 constexpr int OFF_KV = 4 * TILE;                  // stage s: K at OFF_KV + 2 s TILE, V after it
 constexpr int OFF_BAR = OFF_KV + NST * 2 * TILE;
-constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
+constexpr int OFF_ORDER = OFF_BAR + 512;          // [kOrder] bytes
+constexpr int SMEM_BYTES = OFF_ORDER + win::kOrder + 1024;
 constexpr uint32_t TM_X = 256, TM_S = 0, TM_DP = 64, TM_DQ = 128, TM_DS = 192;
 
 enum : int {
@@ -47,6 +48,7 @@ struct QArgs {
     CUtensorMap mapQ, mapK, mapV, mapDO;
     WindowArgs w;
     long long n_items;
+    int sorted;                     // few blocks of unequal work: drawn by it
     float c;
 };
 
@@ -117,6 +119,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
         tc::tma_prefetch_desc(&p.mapV);
         tc::tma_prefetch_desc(&p.mapDO);
     }
+    uint8_t* order = sm + OFF_ORDER;
+    long long n_items = p.n_items;
+    if (warp == SOFT && p.sorted)
+        n_items = (long long)p.w.Hq * win::order_blocks(order, (int)p.n_items / p.w.Hq, [&](int b) {
+            Item q;
+            return q.load(p.w, (long long)b * p.w.Hq) ? q.nt * (q.rows > BT ? 5 : 3) : -1;
+        });
     if (warp == SOFT + 1) {
         tc::tmem_alloc(tmem_slot, 512);
         tc::tmem_relinquish();
@@ -142,12 +151,13 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
         if (tc::elect_one()) {
             int g = 0, n = 0;
             bool ok = true;
-            for (int w = blockIdx.x, next, k = 0; ok && !*abort_flag; w = next) {
-                if (w >= p.n_items) {
+            for (int ticket = blockIdx.x, next, k = 0; ok && !*abort_flag; ticket = next) {
+                if (ticket >= n_items) {
                     ok = items.put(k, -1);
                     break;
                 }
                 next = gridDim.x + atomicAdd(p.w.status + kTicket, 1);
+                const int w = p.sorted ? order[ticket / p.w.Hq] * p.w.Hq + ticket % p.w.Hq : ticket;
                 if (!it.load(p.w, w)) continue;
                 if (!items.put(k++, w)) { ok = false; break; }
                 if (n > 0 && !tc::mbar_wait(bars + B_QE, (n - 1) & 1, abort_flag, win::kItemWait)) { ok = false; break; }
@@ -495,6 +505,7 @@ cudaError_t launch_dq(const WindowArgs& a, int sms, bool after_dkv, cudaStream_t
         return cudaErrorInvalidValue;
     p.c = a.scale * kLog2e;
     p.n_items = win::block_numbers<ROWS>(a.Tq, a.n_seq) * a.Hq;
+    p.sorted = win::ordered(a, p.n_items / a.Hq, sms);
     cudaError_t e = cudaFuncSetAttribute(window_dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};

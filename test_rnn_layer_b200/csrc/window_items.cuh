@@ -89,6 +89,45 @@ struct ItemQueue {
         return w;
     }
 };
+// The order in which few blocks of unequal work are drawn: the longest first, so that the CTAs end together (forward
+// pass of 13 requests of up to 1,725 rows, 12 heads, window 1,024: 60 -> 49 us).  Ranking them takes 2 to 3 us of a
+// launch, so it is left out where blocks differ little: one sequence (16,384 rows, forward and backward: 580 us, 584
+// with it), a narrow window (5 sequences, 256 keys to both sides: 148 us, 152 with it), and where every CTA has one item.
+// A warp ranks up to kOrder blocks; with more, an item is a small part of a CTA's work.
+constexpr int kOrder = 128;
+inline bool ordered(const WindowArgs& p, long long n_blocks, int ctas) {
+    return n_blocks <= kOrder && n_blocks * p.Hq > ctas && p.n_seq > 1 && (long long)p.left + p.right >= 768;
+}
+// By a warp: block numbers by falling work(b) (-1: unused) into order[]; returns how many are used.
+template <class Work>
+__device__ __forceinline__ int order_blocks(uint8_t* order, int n, Work work) {
+    const int lane = threadIdx.x & 31;
+    int mine[kOrder / 32], rank[kOrder / 32], used = 0;
+#pragma unroll
+    for (int i = 0; i < kOrder / 32; ++i) {
+        mine[i] = 32 * i + lane < n ? work(32 * i + lane) : -1;
+        rank[i] = 0;
+        used += __popc(__ballot_sync(0xffffffffu, mine[i] >= 0));
+    }
+#pragma unroll
+    for (int k = 0; k < kOrder / 32; ++k) {
+        if (32 * k >= n) break;
+#pragma unroll 4
+        for (int l = 0; l < min(32, n - 32 * k); ++l) {
+            const int other = __shfl_sync(0xffffffffu, mine[k], l), b = 32 * k + l;
+#pragma unroll
+            for (int i = 0; i < kOrder / 32; ++i) {
+                if (32 * i >= n) break;
+                rank[i] += other >= mine[i] + (b >= 32 * i + lane);   // equal work: by number
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kOrder / 32; ++i)
+        if (mine[i] >= 0) order[rank[i]] = (uint8_t)(32 * i + lane);
+    __syncwarp();
+    return used;
+}
 // most items of a launch: the counter and its overshoot stay inside an int
 constexpr long long kMaxItems = (1LL << 31) - (1 << 20);
 

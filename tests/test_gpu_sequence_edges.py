@@ -408,3 +408,27 @@ def test_buffers_keep_their_type_under_another_default(default):
         torch.set_default_dtype(before)
     for a, b in zip(got, want):
         assert a.dtype is b.dtype and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("left,right,sinks", [(1023, 0, 4), (500, 400, 0), (5000, 0, 130)])
+def test_few_blocks_are_drawn_by_their_work(left, right, sinks):
+    """Sequences of unequal lengths, more items than CTAs: every row's result, and none behind the last one's, whatever
+    the order in which the blocks are drawn (a sequence alone gives the same bits)."""
+    Hq, Hk = 12, 4
+    nq, nk = [700, 0, 1, 129, 256, 257, 900], [1500, 300, 800, 100, 256, 1300, 900]
+    cq, ck = np.cumsum([0] + nq).tolist(), np.cumsum([0] + nk).tolist()
+    Tq, Tk = cq[-1] + 9, ck[-1] + 5
+    q, k, v, g = (_rand(60 + i, T, H, 64, dtype=BF) for i, (T, H) in enumerate([(Tq, Hq), (Tk, Hk), (Tk, Hk), (Tq, Hq)]))
+    mask = dict(left=left, right=right, sinks=sinks)
+    both = dict(mask, cu_q=_ints(cq), cu_k=_ints(ck))
+    r = L.window_attention(q, k, v, want_lse=True, **both)
+    b = L.window_attention_backward(q, k, v, r["out"], r["lse"], g, **both)
+    assert not r["out"][cq[-1]:].any() and not b["dq"][cq[-1]:].any()
+    for s in range(len(nq)):
+        if not nq[s]:
+            continue
+        i, u = slice(cq[s], cq[s + 1]), slice(ck[s], ck[s + 1])
+        r1 = L.window_attention(q[i], k[u], v[u], want_lse=True, **mask)
+        b1 = L.window_attention_backward(q[i], k[u], v[u], r1["out"], r1["lse"], g[i], **mask)
+        assert torch.equal(r["out"][i], r1["out"]) and torch.equal(r["lse"][:, i], r1["lse"])
+        assert torch.equal(b["dq"][i], b1["dq"])
