@@ -18,7 +18,7 @@
 namespace ttt {
 namespace {
 
-constexpr int kThreads = 128, kMaxRows = 8, kBatch = 3;   // 69 us for 32,768 x 48 heads; 256 x 4: 78, 128 x 6: 78
+constexpr int kThreads = 128, kMaxRows = 8, kBatch = 3;   // 72 us for 32,768 x 48 heads; 256 x 4 and 128 x 6: 78
 
 __device__ __forceinline__ void fill_table(const RopeArgs& p, int t0, int rows, float2* cs) {
     const int pairs = p.rot / 2;
