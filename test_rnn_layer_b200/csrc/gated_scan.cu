@@ -36,7 +36,6 @@ __global__ void __launch_bounds__(32 * (kWarpsF + 1), kPerSmF)
         using T = typename Elem<BF>::type;
         bool bad = false;
         int seq_b = 0, seq_e = 0;
-        Cursor at_row;
         const int pitch_in = dir * LC * 4;
         const long long pitch = dir * p.ld_y;
         // the group's first row in walking order; past the last chunk outside [0, T)
@@ -57,34 +56,36 @@ __global__ void __launch_bounds__(32 * (kWarpsF + 1), kPerSmF)
         struct Set {
             Vec<V> a[R], b[R];
             Run<V> before;
-            bool plain;
+            uint32_t marks;
         };
         auto first_half = [&](Set& q, int step) {
             const int t0 = first_row(step);
-            q.plain = plain_rows<R>(c, t0, dir, seq_b, seq_e);
+            q.marks = plain_rows<R>(c, t0, dir, seq_b, seq_e) ? 0 : marks_of(c, t0, dir, p.reverse);
             if (step * cs + rank < chunks) ok = ok && tc::mbar_wait(sh.full + step % kStages, (step / kStages) & 1, &sh.abort);
             const uint8_t* in = input_of(step);
             Run<V> run{all<V>(1.f), all<V>(0.f)};
-            if (q.plain) {
+#pragma unroll
+            for (int k = 0; k < R; ++k) {
+                load(in, q.a[k], q.b[k]);
+                in += pitch_in;
+                run.b = fma(q.a[k], run.b, q.b[k]);
+                run.a = mul(run.a, q.a[k]);
+            }
+            if (q.marks) {   // rows that begin a sequence take its first state, rows of none leave the state as it is
+                Vec<V> h0[R];
+                states_at<V>(h0, q.marks >> 8 & 0xffu, c, t0, dir, p.H_0, p.D, ch);
+                run = Run<V>{all<V>(1.f), all<V>(0.f)};
 #pragma unroll
                 for (int k = 0; k < R; ++k) {
-                    load(in, q.a[k], q.b[k]);
-                    in += pitch_in;
-                    run.b = fma(q.a[k], run.b, q.b[k]);
-                    run.a = mul(run.a, q.a[k]);
-                }
-            } else {
-#pragma unroll 1
-                for (int k = 0; k < R; ++k) {
-                    const Row r = row_of(c, at_row, t0 + dir * k, p.reverse);
-                    if (r.s < 0) continue;
-                    Vec<V> ak, bk;
-                    load(in + k * pitch_in, ak, bk);
-                    if (r.start) {
-                        run = Run<V>{all<V>(kReset), fma(ak, state_of<V>(p.H_0, r.s, p.D, ch), bk)};
+                    if (first_of(q.marks, k)) {
+                        q.b[k] = fma(q.a[k], h0[k], q.b[k]);
+                        run = Run<V>{all<V>(kReset), q.b[k]};
+                    } else if (in_sequence(q.marks, k)) {
+                        run.b = fma(q.a[k], run.b, q.b[k]);
+                        run.a = mul(run.a, q.a[k]);   // -0 stays -0
                     } else {
-                        run.b = fma(ak, run.b, bk);
-                        run.a = mul(run.a, ak);   // -0 stays -0
+                        q.a[k] = all<V>(1.f);
+                        q.b[k] = all<V>(0.f);
                     }
                 }
             }
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(32 * (kWarpsF + 1), kPerSmF)
                 *reinterpret_cast<Vec<V>*>(p.chunk_states + at) = h;
             }
             T* y = static_cast<T*>(p.Y) + (long long)t0 * p.ld_y + ch;
-            if (q.plain) {
+            if (!q.marks) {
 #pragma unroll
                 for (int k = 0; k < R; ++k) {
                     h = fma(q.a[k], h, q.b[k]);
@@ -112,19 +113,22 @@ __global__ void __launch_bounds__(32 * (kWarpsF + 1), kPerSmF)
                 }
                 bad |= wild<V>(h);   // inside a sequence a state that is not finite stays so
             } else {
-                const uint8_t* in = input_of(step);
-#pragma unroll 1
+                Vec<V> at[R];
+#pragma unroll
                 for (int k = 0; k < R; ++k) {
-                    const Row r = row_of(c, at_row, t0 + dir * k, p.reverse);
-                    if (r.s < 0) continue;
-                    Vec<V> ak, bk;
-                    load(in + k * pitch_in, ak, bk);
-                    if (r.start) h = state_of<V>(p.H_0, r.s, p.D, ch);
-                    h = fma(ak, h, bk);
-                    bad |= wild<V>(h);
-                    __stcs(reinterpret_cast<uint32_t*>(y + k * pitch), Elem<BF>::put(h));
-                    if (r.end) put_state<V>(p.H_T, r.s, p.D, ch, h);
+                    h = first_of(q.marks, k) ? q.b[k] : fma(q.a[k], h, q.b[k]);
+                    at[k] = h;
+                    if (in_sequence(q.marks, k)) {
+                        bad |= wild<V>(h);
+                        __stcs(reinterpret_cast<uint32_t*>(y), Elem<BF>::put(h));
+                    }
+                    y += pitch;
                 }
+                if (p.H_T)
+                    for (uint32_t bits = q.marks >> 16 & 0xffu; bits; bits &= bits - 1) {
+                        const int k = __ffs(bits) - 1;
+                        put_state<V>(p.H_T, c.find(t0 + dir * k), p.D, ch, at[k]);
+                    }
             }
         };
         Set q0, q1;

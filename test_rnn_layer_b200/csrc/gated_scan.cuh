@@ -182,8 +182,7 @@ struct Elem {
 
 // ------------------------------------------------------------------ rows
 // Whether R rows lie inside one sequence and none is its first or last one ([b, e): the sequence that the last
-// look-up found).  Where they do not, the rows are walked one by one from shared memory, in rolled loops: the
-// code of the common case stays small enough for the instruction cache.
+// look-up found).  Where they do not, each row's marks say what it is.
 template <int R>
 __device__ __forceinline__ bool plain_rows(const SeqOffsets& c, int first, int dir, int& b, int& e) {
     const int lo = dir > 0 ? first : first - (R - 1), hi = lo + R - 1;
@@ -194,25 +193,37 @@ __device__ __forceinline__ bool plain_rows(const SeqOffsets& c, int first, int d
     }
     return __all_sync(0xffffffffu, lo > b && hi < e - 1);
 }
-// One row: its sequence (-1: none), and whether it is the first and the last one in walking order.  The cursor
-// holds the sequence of the row before.
-struct Row {
-    int s;
-    bool start, end;
-};
-struct Cursor {
-    int s = 0, b = 0, e = 0;
-};
-__device__ __forceinline__ Row row_of(const SeqOffsets& c, Cursor& at, int t, int reverse) {
-    if (t < 0 || t >= c.rows) return {-1, false, false};
-    if (t < at.b || t >= at.e) {
-        at.s = c.find(t);
-        at.b = c.begin(at.s);
-        at.e = c.begin(at.s + 1);
-        if (t < at.b || t >= at.e) return {-1, false, false};
+// Marks of eight rows: bit k for row t0 + dir k in a sequence, bit 8 + k for the first one of a sequence in walking
+// order, bit 16 + k for the last one.  kBorder is set for rows that are not all plain ones.
+constexpr uint32_t kBorder = 1u << 31;
+__device__ __forceinline__ uint32_t marks_of(const SeqOffsets& c, int t0, int dir, int reverse) {
+    const int lo = dir > 0 ? t0 : t0 - (kRows - 1), stop = min(lo + kRows, c.rows);
+    uint32_t in = 0, low = 0, high = 0;   // bit r for row lo + r
+    for (int t = max(lo, 0); t < stop;) {
+        const int s = c.find(t), b = c.begin(s), e = c.begin(s + 1);
+        if (t < b || t >= e) {   // behind the last sequence (or between offsets that fall)
+            if (t >= c.begin(c.n)) break;
+            ++t;
+            continue;
+        }
+        const int u = min(e, stop);
+        in |= (1u << (u - lo)) - (1u << (t - lo));
+        if (t == b) low |= 1u << (t - lo);
+        if (u == e) high |= 1u << (u - 1 - lo);
+        t = u;
     }
-    return {at.s, t == (reverse ? at.e - 1 : at.b), t == (reverse ? at.b : at.e - 1)};
+    uint32_t first = reverse ? high : low, last = reverse ? low : high;
+    if (dir < 0) {
+        in = __brev(in) >> 24;
+        first = __brev(first) >> 24;
+        last = __brev(last) >> 24;
+    }
+    return kBorder | in | first << 8 | last << 16;
 }
+__device__ __forceinline__ bool in_sequence(uint32_t marks, int k) { return marks >> k & 1; }
+__device__ __forceinline__ bool first_of(uint32_t marks, int k) { return marks >> (8 + k) & 1; }
+__device__ __forceinline__ bool last_of(uint32_t marks, int k) { return marks >> (16 + k) & 1; }
+static_assert(kRows == 8, "marks");
 
 // Sequence s's values of an fp32 array [n_seq, D] (null: zeros).
 template <int V>
@@ -224,6 +235,14 @@ __device__ __forceinline__ Vec<V> state_of(const float* p, int s, int D, int ch)
         for (int v = 0; v < V; ++v) r.set(v, p[at + v]);
     }
     return r;
+}
+// The same for the rows whose bits are set (the others' places are left).
+template <int V>
+__device__ __forceinline__ void states_at(Vec<V>* to, uint32_t bits, const SeqOffsets& c, int t0, int dir, const float* p, int D, int ch) {
+    for (; bits; bits &= bits - 1) {
+        const int k = __ffs(bits) - 1;
+        to[k] = p ? state_of<V>(p, c.find(t0 + dir * k), D, ch) : all<V>(0.f);
+    }
 }
 template <int V>
 __device__ __forceinline__ void put_state(float* p, int s, int D, int ch, Vec<V> h) {

@@ -41,7 +41,6 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
         using T = typename Elem<BF>::type;
         bool bad = false;
         int seq_b = 0, seq_e = 0;
-        Cursor at_row;
         const int seg = p.reverse ? group : GROUPS - 1 - group;   // in the tile
         const int pitch_in = dir * LC * 4;
         const long long pitch_f = dir * p.ld_df, pitch_x = dir * p.ld_dx;
@@ -59,16 +58,16 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
             Vec<V> a[R], sc[R], sl[R];
             uint32_t dy[R];
             Run<V> before;
-            bool plain;
+            uint32_t marks;
         };
         auto first_half = [&](Set& q, int step) {
             const int t0 = first_row(step);
-            q.plain = plain_rows<R>(c, t0, dir, seq_b, seq_e);
+            q.marks = plain_rows<R>(c, t0, dir, seq_b, seq_e) ? 0 : marks_of(c, t0, dir, p.reverse);
             if (step * cs + rank < chunks) ok = ok && tc::mbar_wait(sh.full + step % kStages, (step / kStages) & 1, &sh.abort);
             const uint8_t* in = input_of(step);
             auto word = [&](int array, int k) { return *reinterpret_cast<const uint32_t*>(in + array * ARRAY + k * pitch_in); };
             Run<V> run{all<V>(1.f), all<V>(0.f)};
-            if (q.plain) {
+            if (!q.marks) {
                 Vec<V> h = kept_of(step);
 #pragma unroll
                 for (int k = R - 1; k >= 0; --k) {
@@ -85,18 +84,31 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
                     run.a = mul(run.a, q.a[k]);
                 }
             } else {
-#pragma unroll 1
+                Vec<V> anew[R];   // the states that sequences begin with, then the gradients of their final ones
+                states_at<V>(anew, q.marks >> 8 & 0xffu, c, t0, dir, p.H_0, p.D, ch);
+                Vec<V> h = kept_of(step);
+#pragma unroll
+                for (int k = R - 1; k >= 0; --k) {
+                    const Vec<V> x = Elem<BF>::get(word(1, k));
+                    Vec<V> rest;
+                    gates<V>(Elem<BF>::get(word(0, k)), q.a[k], rest);
+                    if (first_of(q.marks, k)) h = anew[k];
+                    slopes<FORM, V>(q.a[k], rest, h, x, q.sc[k], q.sl[k]);
+                    h = fma(q.a[k], h, mul(q.sc[k], x));
+                }
+                states_at<V>(anew, q.marks >> 16 & 0xffu, c, t0, dir, p.dH_T, p.D, ch);
+#pragma unroll
                 for (int k = 0; k < R; ++k) {
-                    const Row r = row_of(c, at_row, t0 + dir * k, p.reverse);
-                    if (r.s < 0) continue;
-                    Vec<V> ak, rest;
-                    gates<V>(Elem<BF>::get(word(0, k)), ak, rest);
-                    const Vec<V> g = Elem<BF>::get(word(2, k));
-                    if (r.end) {   // lambda starts anew, with the final state's gradient
-                        run = Run<V>{all<V>(kReset), mul(ak, add(state_of<V>(p.dH_T, r.s, p.D, ch), g))};
-                    } else {
-                        run.b = mul(ak, add(run.b, g));
-                        run.a = mul(run.a, ak);   // -0 stays -0
+                    q.dy[k] = word(2, k);
+                    const Vec<V> g = Elem<BF>::get(q.dy[k]);
+                    if (last_of(q.marks, k)) {   // lambda starts anew
+                        run = Run<V>{all<V>(kReset), mul(q.a[k], add(anew[k], g))};
+                    } else if (in_sequence(q.marks, k)) {
+                        run.b = mul(q.a[k], add(run.b, g));
+                        run.a = mul(run.a, q.a[k]);   // -0 stays -0
+                    } else {   // a row of no sequence leaves lambda as it is
+                        q.a[k] = all<V>(1.f);
+                        q.dy[k] = 0;
                     }
                 }
             }
@@ -112,7 +124,7 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
             T* df = static_cast<T*>(p.dF) + (long long)t0 * p.ld_df + ch;
             T* dx = static_cast<T*>(p.dX) + (long long)t0 * p.ld_dx + ch;
             Vec<V> seen = all<V>(0.f);   // 0 times what is stored: NaN where it is not finite
-            if (q.plain) {
+            if (!q.marks) {
 #pragma unroll
                 for (int k = 0; k < R; ++k) {
                     const Vec<V> l = add(lam, Elem<BF>::get(q.dy[k])), d = mul(l, q.sl[k]);
@@ -125,36 +137,28 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
                 }
                 seen = fma(all<V>(0.f), lam, seen);   // inside a sequence what is not finite stays so
             } else {
-                const uint8_t* in = input_of(step);
-                auto word = [&](int array, int k) { return *reinterpret_cast<const uint32_t*>(in + array * ARRAY + k * pitch_in); };
-                Vec<V> before[R];   // h before each row (a short array in local memory)
-                Vec<V> h = kept_of(step);
-#pragma unroll 1
-                for (int k = R - 1; k >= 0; --k) {
-                    const Row r = row_of(c, at_row, t0 + dir * k, p.reverse);
-                    if (r.s < 0) continue;
-                    if (r.start) h = state_of<V>(p.H_0, r.s, p.D, ch);
-                    before[k] = h;
-                    Vec<V> ak, rest;
-                    gates<V>(Elem<BF>::get(word(0, k)), ak, rest);
-                    h = fma(ak, h, input<FORM, V>(ak, rest, Elem<BF>::get(word(1, k))));
-                }
-#pragma unroll 1
+                Vec<V> anew[R], at[R];
+                states_at<V>(anew, q.marks >> 16 & 0xffu, c, t0, dir, p.dH_T, p.D, ch);
+#pragma unroll
                 for (int k = 0; k < R; ++k) {
-                    const Row r = row_of(c, at_row, t0 + dir * k, p.reverse);
-                    if (r.s < 0) continue;
-                    Vec<V> ak, rest, s, slope;
-                    gates<V>(Elem<BF>::get(word(0, k)), ak, rest);
-                    slopes<FORM, V>(ak, rest, before[k], Elem<BF>::get(word(1, k)), s, slope);
-                    if (r.end) lam = state_of<V>(p.dH_T, r.s, p.D, ch);
-                    const Vec<V> l = add(lam, Elem<BF>::get(word(2, k))), d = mul(l, slope);
-                    lam = mul(ak, l);
-                    seen = fma(all<V>(0.f), d, seen);
-                    seen = fma(all<V>(0.f), lam, seen);
-                    *reinterpret_cast<uint32_t*>(df + k * pitch_f) = Elem<BF>::put(d);
-                    *reinterpret_cast<uint32_t*>(dx + k * pitch_x) = Elem<BF>::put(mul(l, s));
-                    if (r.start) put_state<V>(p.dH_0, r.s, p.D, ch, lam);
+                    if (last_of(q.marks, k)) lam = anew[k];
+                    const Vec<V> l = add(lam, Elem<BF>::get(q.dy[k])), d = mul(l, q.sl[k]);
+                    lam = mul(q.a[k], l);
+                    at[k] = lam;
+                    if (in_sequence(q.marks, k)) {
+                        seen = fma(all<V>(0.f), d, seen);
+                        seen = fma(all<V>(0.f), lam, seen);
+                        __stcs(reinterpret_cast<uint32_t*>(df), Elem<BF>::put(d));
+                        __stcs(reinterpret_cast<uint32_t*>(dx), Elem<BF>::put(mul(l, q.sc[k])));
+                    }
+                    df += pitch_f;
+                    dx += pitch_x;
                 }
+                if (p.dH_0)
+                    for (uint32_t bits = q.marks >> 8 & 0xffu; bits; bits &= bits - 1) {
+                        const int k = __ffs(bits) - 1;
+                        put_state<V>(p.dH_0, c.find(t0 + dir * k), p.D, ch, at[k]);
+                    }
             }
             bad |= wild<V>(seen);
         };
