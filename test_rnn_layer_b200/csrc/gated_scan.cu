@@ -56,27 +56,31 @@ __global__ void __launch_bounds__(32 * (kWarpsF + 1), kPerSmF)
         struct Set {
             Vec<V> a[R], b[R];
             Run<V> before;
-            uint32_t marks;
+            bool plain;
+            uint32_t marks;   // where not plain
         };
         auto first_half = [&](Set& q, int step) {
             const int t0 = first_row(step);
-            q.marks = plain_rows<R>(c, t0, dir, seq_b, seq_e) ? 0 : marks_of(c, t0, dir, p.reverse);
+            q.plain = plain_rows<R>(c, t0, dir, seq_b, seq_e);
             if (step * cs + rank < chunks) ok = ok && tc::mbar_wait(sh.full + step % kStages, (step / kStages) & 1, &sh.abort);
             const uint8_t* in = input_of(step);
             Run<V> run{all<V>(1.f), all<V>(0.f)};
-#pragma unroll
-            for (int k = 0; k < R; ++k) {
-                load(in, q.a[k], q.b[k]);
-                in += pitch_in;
-                run.b = fma(q.a[k], run.b, q.b[k]);
-                run.a = mul(run.a, q.a[k]);
-            }
-            if (q.marks) {   // rows that begin a sequence take its first state, rows of none leave the state as it is
-                Vec<V> h0[R];
-                states_at<V>(h0, q.marks >> 8 & 0xffu, c, t0, dir, p.H_0, p.D, ch);
-                run = Run<V>{all<V>(1.f), all<V>(0.f)};
+            if (q.plain) {
 #pragma unroll
                 for (int k = 0; k < R; ++k) {
+                    load(in, q.a[k], q.b[k]);
+                    in += pitch_in;
+                    run.b = fma(q.a[k], run.b, q.b[k]);
+                    run.a = mul(run.a, q.a[k]);
+                }
+            } else {   // rows that begin a sequence take its first state, rows of none leave the state as it is
+                q.marks = marks_of(c, t0, dir, p.reverse);
+                Vec<V> h0[R];
+                states_at<V>(h0, q.marks >> 8 & 0xffu, c, t0, dir, p.H_0, p.D, ch);
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    load(in, q.a[k], q.b[k]);
+                    in += pitch_in;
                     if (first_of(q.marks, k)) {
                         q.b[k] = fma(q.a[k], h0[k], q.b[k]);
                         run = Run<V>{all<V>(kReset), q.b[k]};
@@ -104,7 +108,7 @@ __global__ void __launch_bounds__(32 * (kWarpsF + 1), kPerSmF)
                 *reinterpret_cast<Vec<V>*>(p.chunk_states + at) = h;
             }
             T* y = static_cast<T*>(p.Y) + (long long)t0 * p.ld_y + ch;
-            if (!q.marks) {
+            if (q.plain) {
 #pragma unroll
                 for (int k = 0; k < R; ++k) {
                     h = fma(q.a[k], h, q.b[k]);

@@ -182,7 +182,10 @@ struct Elem {
 
 // ------------------------------------------------------------------ rows
 // Whether R rows lie inside one sequence and none is its first or last one ([b, e): the sequence that the last
-// look-up found).  Where they do not, each row's marks say what it is.
+// look-up found).  Where they do not, each row's marks say what it is
+// and the rows stay in registers like the others.  (Walking them one by one from shared memory, in rolled loops, held
+// the cluster up for 3 us a border: 9,001 rows in 7 sequences, fp32, both passes 115 us against 92, in 40
+// sequences 163 against 129; one sequence of 313,344 rows takes 525 us with the larger code, 517 with the smaller.)
 template <int R>
 __device__ __forceinline__ bool plain_rows(const SeqOffsets& c, int first, int dir, int& b, int& e) {
     const int lo = dir > 0 ? first : first - (R - 1), hi = lo + R - 1;

@@ -58,16 +58,17 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
             Vec<V> a[R], sc[R], sl[R];
             uint32_t dy[R];
             Run<V> before;
-            uint32_t marks;
+            bool plain;
+            uint32_t marks;   // where not plain
         };
         auto first_half = [&](Set& q, int step) {
             const int t0 = first_row(step);
-            q.marks = plain_rows<R>(c, t0, dir, seq_b, seq_e) ? 0 : marks_of(c, t0, dir, p.reverse);
+            q.plain = plain_rows<R>(c, t0, dir, seq_b, seq_e);
             if (step * cs + rank < chunks) ok = ok && tc::mbar_wait(sh.full + step % kStages, (step / kStages) & 1, &sh.abort);
             const uint8_t* in = input_of(step);
             auto word = [&](int array, int k) { return *reinterpret_cast<const uint32_t*>(in + array * ARRAY + k * pitch_in); };
             Run<V> run{all<V>(1.f), all<V>(0.f)};
-            if (!q.marks) {
+            if (q.plain) {
                 Vec<V> h = kept_of(step);
 #pragma unroll
                 for (int k = R - 1; k >= 0; --k) {
@@ -84,6 +85,7 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
                     run.a = mul(run.a, q.a[k]);
                 }
             } else {
+                q.marks = marks_of(c, t0, dir, p.reverse);
                 Vec<V> anew[R];   // the states that sequences begin with, then the gradients of their final ones
                 states_at<V>(anew, q.marks >> 8 & 0xffu, c, t0, dir, p.H_0, p.D, ch);
                 Vec<V> h = kept_of(step);
@@ -124,7 +126,7 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
             T* df = static_cast<T*>(p.dF) + (long long)t0 * p.ld_df + ch;
             T* dx = static_cast<T*>(p.dX) + (long long)t0 * p.ld_dx + ch;
             Vec<V> seen = all<V>(0.f);   // 0 times what is stored: NaN where it is not finite
-            if (!q.marks) {
+            if (q.plain) {
 #pragma unroll
                 for (int k = 0; k < R; ++k) {
                     const Vec<V> l = add(lam, Elem<BF>::get(q.dy[k])), d = mul(l, q.sl[k]);
