@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(32 * (kWarpsF + 1), kPerSmF)
                 }
             } else {   // rows that begin a sequence take its first state, rows of none leave the state as it is
                 q.marks = marks_of(c, t0, dir, p.reverse);
+                in = apart(in);
                 Vec<V> h0[R];
                 states_at<V>(h0, q.marks >> 8 & 0xffu, c, t0, dir, p.H_0, p.D, ch);
 #pragma unroll
@@ -117,6 +118,7 @@ __global__ void __launch_bounds__(32 * (kWarpsF + 1), kPerSmF)
                 }
                 bad |= wild<V>(h);   // inside a sequence a state that is not finite stays so
             } else {
+                y = apart(y);
                 Vec<V> at[R];
 #pragma unroll
                 for (int k = 0; k < R; ++k) {

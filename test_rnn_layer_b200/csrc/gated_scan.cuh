@@ -184,8 +184,8 @@ struct Elem {
 // Whether R rows lie inside one sequence and none is its first or last one ([b, e): the sequence that the last
 // look-up found).  Where they do not, each row's marks say what it is
 // and the rows stay in registers like the others.  (Walking them one by one from shared memory, in rolled loops, held
-// the cluster up for 3 us a border: 9,001 rows in 7 sequences, fp32, both passes 115 us against 92, in 40
-// sequences 163 against 129; one sequence of 313,344 rows takes 525 us with the larger code, 517 with the smaller.)
+// the cluster up for 3 us a border: 9,001 rows in 7 sequences, fp32, both passes 115 us against 91, in 40
+// sequences 163 against 129; one sequence of 313,344 rows takes 523 us with the larger code, 517 with the smaller.)
 template <int R>
 __device__ __forceinline__ bool plain_rows(const SeqOffsets& c, int first, int dir, int& b, int& e) {
     const int lo = dir > 0 ? first : first - (R - 1), hi = lo + R - 1;
@@ -227,6 +227,12 @@ __device__ __forceinline__ bool in_sequence(uint32_t marks, int k) { return mark
 __device__ __forceinline__ bool first_of(uint32_t marks, int k) { return marks >> (8 + k) & 1; }
 __device__ __forceinline__ bool last_of(uint32_t marks, int k) { return marks >> (16 + k) & 1; }
 static_assert(kRows == 8, "marks");
+// Keeps the compiler from computing a border's addresses in front of the branch, where plain rows would pay for them.
+template <class T>
+__device__ __forceinline__ T* apart(T* p) {
+    asm volatile("" : "+l"(p));
+    return p;
+}
 
 // Sequence s's values of an fp32 array [n_seq, D] (null: zeros).
 template <int V>

@@ -86,6 +86,7 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
                 }
             } else {
                 q.marks = marks_of(c, t0, dir, p.reverse);
+                in = apart(in);
                 Vec<V> anew[R];   // the states that sequences begin with, then the gradients of their final ones
                 states_at<V>(anew, q.marks >> 8 & 0xffu, c, t0, dir, p.H_0, p.D, ch);
                 Vec<V> h = kept_of(step);
@@ -139,6 +140,8 @@ __global__ void __launch_bounds__(32 * (kWarpsB + 1), kPerSmB)
                 }
                 seen = fma(all<V>(0.f), lam, seen);   // inside a sequence what is not finite stays so
             } else {
+                df = apart(df);
+                dx = apart(dx);
                 Vec<V> anew[R], at[R];
                 states_at<V>(anew, q.marks >> 16 & 0xffu, c, t0, dir, p.dH_T, p.D, ch);
 #pragma unroll
