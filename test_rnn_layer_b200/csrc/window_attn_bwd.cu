@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
 #pragma unroll
                 for (int e = 0; e < COLS; ++e) o[e] = 0;
             }
-            if (mine) {
+            if (mine && !RowKeys(p.w, it.pos0 + BT * X + r, it.nk).few()) {
                 const long long t = it.q_lo + BT * X + r;
                 nonfinite |= store_row(p.w.dQ + t * p.w.ld_dq + it.h * DH + COLS * y, o, p.w.grad_scale);
             }
@@ -391,8 +391,8 @@ __global__ void __launch_bounds__(THREADS, 1) window_dq_kernel(const __grid_cons
 //
 // Out is rounded to bf16, and dP - delta of a row with few keys is small beside dP: with two keys the rounding put
 // dQ and dK off by 0.0055 in the norm (0.0025 with many).  So a row of at most FEW keys gets delta = sum_u P_u dP_u,
-// which is the same number, from the keys and values themselves.
-constexpr int FEW = 20;
+// which is the same number, from the keys and values themselves, and its dQ here in fp32: scale (sum_u P_u dP_u k_u -
+// delta sum_u P_u k_u).  (With the rounded dS, dQ of rows of five keys was off by 0.0026, more than the 0.0024 of long ones.)
 
 __device__ __forceinline__ float dot8(const uint4& x, const uint4& y) {
     const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
@@ -451,16 +451,16 @@ __global__ void __launch_bounds__(256) window_delta_kernel(const WindowArgs p, l
         }
         return;
     }
-    // the keys that the row sees: the first `sk`, then [lo, lo + n)
     int k0 = 0, lo = 0, sk = 0, n = 0;
     if (in) {
         const int s = cq.find((int)t), q0 = cq.begin(s), q1 = cq.begin(s + 1);
         if (t >= q0 && t < q1) {
             k0 = ck.begin(s);
-            const int nk = max(ck.begin(s + 1) - k0, 0), pos = nk - (q1 - q0) + (int)t - q0, end = min(pos + p.right + 1, nk);
-            lo = min(max(pos - p.left, 0), nk);
-            n = max(end - lo, 0);
-            sk = max(min(min(p.sinks, lo), end), 0);
+            const int nk = max(ck.begin(s + 1) - k0, 0);
+            const RowKeys r(p, nk - (q1 - q0) + (int)t - q0, nk);
+            lo = r.lo;
+            n = r.n;
+            sk = r.sk;
         }
     }
     const int most = __reduce_max_sync(0xffffffffu, sk + n <= FEW ? sk + n : 0);
@@ -472,10 +472,11 @@ __global__ void __launch_bounds__(256) window_delta_kernel(const WindowArgs p, l
         const uint32_t odd = __ballot_sync(0xffffffffu, odd_values(x)) >> (lane & 24) & 0xffu;
         float delta = sum8(dot8(g, o));
         if (most > 0) {
-            const bool few = sk + n <= FEW && sk + n > 0 && isfinite(delta);
+            const bool few = sk + n <= FEW && sk + n > 0;
             const float lse = few ? p.Lse[(long long)h * p.Tq + t] : 0.f;
             const int kcol = h / (p.Hq / p.Hk) * DH + col0;
-            float sum = 0.f;
+            const float whole = delta;
+            float sum = 0.f, pk[8] = {}, pdk[8] = {};
             for (int i = 0; i < most; ++i) {
                 uint4 k = none, v = none;
                 const bool seen = few && i < sk + n;
@@ -485,9 +486,32 @@ __global__ void __launch_bounds__(256) window_delta_kernel(const WindowArgs p, l
                     v = *reinterpret_cast<const uint4*>(p.V + u * p.ld_v + kcol);
                 }
                 const float score = sum8(dot8(x, k)), dp = sum8(dot8(g, v));
-                if (seen) sum = fmaf(ex2(fmaf(score, p.scale * kLog2e, -kLog2e * lse)), dp, sum);
+                if (!seen) continue;
+                const float w = ex2(fmaf(score, p.scale * kLog2e, -kLog2e * lse)), wd = w * dp;
+                sum += wd;
+                const uint32_t kw[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float kc = __uint_as_float(c % 2 ? kw[c / 2] & 0xffff0000u : kw[c / 2] << 16);
+                    pk[c] = fmaf(w, kc, pk[c]);
+                    pdk[c] = fmaf(wd, kc, pdk[c]);
+                }
             }
-            if (few) delta = sum;
+            if (few) {
+                // a product of dO and Out that is not finite spoils the row; one key's weight is 1 whatever its score
+                if (isfinite(whole)) delta = sum;
+                const float scale = sk + n == 1 ? 0.f : p.grad_scale;
+                float d[8];
+                bool fine = true;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    d[c] = odd || !isfinite(whole) ? NAN : scale * fmaf(-delta, pk[c], pdk[c]);
+                    fine &= isfinite(d[c]);
+                }
+                if (!fine) atomicOr(p.status, kStatusNonFinite);
+                *reinterpret_cast<uint4*>(p.dQ + t * p.ld_dq + h * DH + col0) =
+                    make_uint4(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]), pack_bf16(d[4], d[5]), pack_bf16(d[6], d[7]));
+            }
         }
         if (odd) delta = NAN;
         if (in && (lane & 7) == 0) p.delta[(long long)h * p.Tq + t] = delta;

@@ -121,6 +121,21 @@ __device__ __forceinline__ bool store_row(__nv_bfloat16* dst, const uint32_t (&o
 // go to slots of the workspace in fp32 and are added in a fixed order.
 constexpr int CHUNK = 16 * BT;              // query rows of a chunk
 constexpr int SINK_BLOCKS = 2;              // key blocks (of 128) that are cut up like this; with more sinks none
+// Rows of at most FEW keys get their dQ from the delta pass (there in fp32), not from the dQ kernel.
+constexpr int FEW = 20;
+// The keys that a row at position pos sees: the first `sk`, then [lo, lo + n)
+struct RowKeys {
+    int sk, lo, n;
+    __device__ __forceinline__ RowKeys(const WindowArgs& p, int pos, int nk) {
+        const int end = min(pos + p.right + 1, nk);
+        lo = min(max(pos - p.left, 0), nk);
+        n = max(end - lo, 0);
+        sk = max(min(min(p.sinks, lo), end), 0);
+    }
+    __device__ __forceinline__ int all() const { return sk + n; }
+    __device__ __forceinline__ bool few() const { return all() > 0 && all() <= FEW; }
+};
+
 constexpr long long SLOT = 2LL * BT * DH;   // floats: dK and dV of one block
 constexpr long long MAX_SLOTS = 4096;       // 256 MB; calls with more sequences and heads leave the lists whole
 

@@ -432,3 +432,29 @@ def test_few_blocks_are_drawn_by_their_work(left, right, sinks):
         b1 = L.window_attention_backward(q[i], k[u], v[u], r1["out"], r1["lse"], g[i], **mask)
         assert torch.equal(r["out"][i], r1["out"]) and torch.equal(r["lse"][:, i], r1["lse"])
         assert torch.equal(b["dq"][i], b1["dq"])
+
+
+def test_query_gradients_of_rows_with_few_keys():
+    """Rows of 1 to 30 keys: dQ is one rounding from the formula's where the delta pass makes it (up to 20 keys), and a row
+    whose upstream gradient is not finite is NaN while the others keep their bits."""
+    T, Hq, Hk = 400, 4, 2
+    q, k, v, g = (_rand(80 + i, T, H, 64, dtype=BF) for i, H in enumerate([Hq, Hk, Hk, Hq]))
+    cu = list(range(0, 400, 30)) + [400]
+    both = dict(left=200, sinks=1, cu_q=_ints(cu), cu_k=_ints(cu))
+    r = L.window_attention(q, k, v, want_lse=True, **both)
+    b = L.window_attention_backward(q, k, v, r["out"], r["lse"], g, **both)
+    want = S.window_attention(*map(_np, (q, k, v)), 200, 0, 1, cu, cu, grad_out=_np(g))["dq"]
+    few = np.concatenate([np.arange(a, min(a + 20, e)) for a, e in zip(cu, cu[1:])])
+    got = _np(b["dq"])
+    # a rounding of bf16 is off by at most 2^-8 of the value; 2^-12 of the row's largest value covers fp32 and the log-sum-exp
+    tol = 2.0 ** -8 * np.abs(want) + 2.0 ** -12 * np.abs(want).max(axis=(1, 2), keepdims=True)
+    single = np.isin(np.arange(T), cu[:-1])
+    assert not got[single].any()
+    assert (np.abs(got - want) <= tol)[few][~single[few]].all()
+    g2 = g.clone()
+    g2[7, 1, 3] = NAN
+    b2 = L.window_attention_backward(q, k, v, r["out"], r["lse"], g2, check_status=False, **both)
+    assert b2["dq"][7, 1].isnan().all() and L.ttt_mlp_status(b2["workspace"]) == L.TTT_ERR_NUMERIC
+    keep = torch.ones(T, Hq, dtype=torch.bool, device="cuda")
+    keep[7, 1] = False
+    assert torch.equal(b2["dq"][keep], b["dq"][keep])
