@@ -58,6 +58,12 @@ __device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
     return r;
 }
 
+// Where the exponentials on the FMA pipe hold x: there the polynomial is just above 1 and the exponent field reaches
+// zero, so what comes out is below 2^-139 and becomes +0 as bf16.  A weight has to: at the clamp of -125 a masked
+// score (-infinity) got 2^-125, which is nothing beside a row's sum but 8 times a value of 3e38.  Between -126 and
+// here the result falls to that without a jump, off by less than 2^-126.
+constexpr float kLowest = -126.99985f;
+
 // 2^x0, 2^x1 on the FMA pipe: a cubic of fma_exp2.cuh's kind (coefficients c0 .. c3) on a pair, with the packed f32x2
 // arithmetic.  x <= 8 here; below -125 it returns about 2^-125, which next to a row maximum of at least 2^-8 is far
 // below fp32 resolution.
@@ -79,11 +85,11 @@ __device__ __forceinline__ void ex2_cubic2(uint64_t x, float c0, float c1, float
     p1 = scale_by_rint(q1, t1);
 }
 
-// The same with fma_exp2.cuh's quartic (relative error 2.7e-6), for sums that are kept in fp32.
+// The same with fma_exp2.cuh's quartic (relative error 2.7e-6), for sums that are kept in fp32; +0 as bf16 from kLowest on.
 __device__ __forceinline__ void ex2_poly2_fine(uint64_t x, float& p0, float& p1) {
     float x0, x1;
     f2_split(x, x0, x1);
-    x = f2(max_nan(x0, -125.0f), max_nan(x1, -125.0f));
+    x = f2(max_nan(x0, kLowest), max_nan(x1, kLowest));
     using namespace fexp;
     const uint64_t shift = f2(kShift, kShift);
     const uint64_t t = f2_add(x, shift);

@@ -140,8 +140,7 @@ __device__ __forceinline__ float softmax_tile(uint32_t (&s)[NC], float c, RowSta
         st.m = mt;
         st.l *= f;
     }
-    // nothing seen so far: any finite reference serves, as every weight is zero (or 2^-125 on the FMA pipe,
-    // which the factor 0 of the first raise removes)
+    // nothing seen so far: any finite reference serves, as every weight is zero
     const float ref = st.m == -INFINITY ? 0.f : st.m;
     const uint64_t c2 = f2(c, c), nm2 = f2(-ref, -ref);
     uint64_t ls[4] = {0, 0, 0, 0};

@@ -1,0 +1,77 @@
+"""What the sequence operators promise beyond their formulas: unseen places may hold anything, values that are not finite
+are reported where they take part, numbers and streams are taken as they are at the call."""
+import math
+
+import pytest
+import torch
+
+from test_rnn_layer_b200 import tttmlp as L
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+NAN, INF = float("nan"), math.inf
+
+
+def _rand(seed, *shape, dtype=torch.float32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda").to(dtype)
+
+
+def _ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+# ---------------------------------------------------------------- unseen places
+def _garbage(kind, like):
+    """Finite values of about 3e38 of both signs, or any 16 bits (NaN and infinities among them)."""
+    g = torch.Generator(device="cuda").manual_seed(17)
+    if kind == "huge":
+        return torch.where(torch.rand(like.shape, generator=g, device="cuda") < 0.5, -3e38, 3e38).to(BF)
+    return torch.randint(-2 ** 15, 2 ** 15, like.shape, generator=g, device="cuda", dtype=torch.int32).to(torch.int16).view(BF)
+
+
+LENGTHS = list(range(1, 49)) + [127, 128, 129, 200]     # ends at every place of sixteen keys, and about a tile's end
+
+
+@pytest.mark.parametrize("kind", ["huge", "bits"])
+@pytest.mark.parametrize("left,right,sinks", [(1000, 0, 0), (20, 0, 3), (9, 9, 0)])
+@pytest.mark.parametrize("place", ["padding", "neighbour"])
+def test_other_sequences_and_padding_change_no_bit(place, left, right, sinks, kind):
+    """A sequence's results do not depend on what lies behind the last one, nor on its neighbours."""
+    lens = LENGTHS if place == "neighbour" else [70, 45]
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    T = cu[-1] + 150
+    q, k, v, g = (_rand(i, T, H, 64, dtype=BF) for i, H in enumerate((4, 2, 2, 4)))
+    mask = dict(left=left, right=right, sinks=sinks, cu_q=_ints(cu), cu_k=_ints(cu), check_status=False)
+
+    def run():
+        r = L.window_attention(q, k, v, want_lse=True, **mask)
+        b = L.window_attention_backward(q, k, v, r["out"], r["lse"], g, **mask)
+        return [r["out"], r["lse"].t(), b["dq"], b["dk"], b["dv"]], r["workspace"]
+
+    want, _ = run()
+    mine = torch.zeros(T, dtype=torch.bool, device="cuda")
+    for s in range(0, len(lens), 2 if place == "neighbour" else 1):
+        mine[cu[s]:cu[s + 1]] = True
+    for t in (q, k, v, g):
+        t[~mine] = _garbage(kind, t)[~mine]
+    got, ws = run()
+    for n, a, b in zip(("out", "lse", "dq", "dk", "dv"), got, want):
+        assert torch.equal(a[mine], b[mine]), n
+    if place == "padding":
+        assert L.ttt_mlp_status(ws) == L.TTT_OK
+
+
+@pytest.mark.parametrize("kind", ["huge", "bits"])
+@pytest.mark.parametrize("at", range(130, 146))
+def test_a_value_changes_only_the_rows_that_see_it(at, kind):
+    T, left, sinks = 300, 20, 3
+    q, k, v = (_rand(i, T, 2, 64, dtype=BF) for i in range(3))
+    want = L.window_attention(q, k, v, left=left, sinks=sinks, want_lse=True)
+    k[at], v[at] = _garbage(kind, k)[at], _garbage(kind, v)[at]
+    got = L.window_attention(q, k, v, left=left, sinks=sinks, want_lse=True, check_status=False)
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[at:at + left + 1] = False
+    assert torch.equal(got["out"][rest], want["out"][rest]) and torch.equal(got["lse"][:, rest], want["lse"][:, rest])
