@@ -65,12 +65,11 @@ __device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
 constexpr float kLowest = -126.99985f;
 
 // 2^x0, 2^x1 on the FMA pipe: a cubic of fma_exp2.cuh's kind (coefficients c0 .. c3) on a pair, with the packed f32x2
-// arithmetic.  x <= 8 here; below -125 it returns about 2^-125, which next to a row maximum of at least 2^-8 is far
-// below fp32 resolution.
+// arithmetic.  x <= 8 here; +0 as bf16 from kLowest on.
 __device__ __forceinline__ void ex2_cubic2(uint64_t x, float c0, float c1, float c2, float c3, float& p0, float& p1) {
     float x0, x1;
     f2_split(x, x0, x1);
-    x = f2(max_nan(x0, -125.0f), max_nan(x1, -125.0f));   // as fexp::clamp_low; NaN stays NaN
+    x = f2(max_nan(x0, kLowest), max_nan(x1, kLowest));
     using namespace fexp;
     const uint64_t shift = f2(kShift, kShift);
     const uint64_t t = f2_add(x, shift);

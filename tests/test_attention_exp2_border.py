@@ -9,7 +9,7 @@ import pytest
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "test_rnn_layer_b200", "csrc")
 POLY = open(os.path.join(CSRC, "fma_exp2.cuh")).read()
 PRIMS = open(os.path.join(CSRC, "attn_prims.cuh")).read()
-BORDERS = {"kC4": "ex2_poly2_fine"}     # the polynomial and the function that holds x
+BORDERS = {"kC4": "ex2_poly2_fine", "kC3": "ex2_cubic2"}     # the polynomial and the function that holds x
 
 
 def _lowest(name):

@@ -75,3 +75,23 @@ def test_a_value_changes_only_the_rows_that_see_it(at, kind):
     rest = torch.ones(T, dtype=torch.bool, device="cuda")
     rest[at:at + left + 1] = False
     assert torch.equal(got["out"][rest], want["out"][rest]) and torch.equal(got["lse"][:, rest], want["lse"][:, rest])
+
+
+@pytest.mark.parametrize("seg", [9, 16, 100, 130, 143])
+def test_segment_attention_takes_no_part_of_the_next_segment(seg):
+    T, H = 3 * seg, 2
+    q, k, v = (_rand(i, T, H * 64, dtype=BF) for i in range(3))
+
+    def run():
+        out = torch.empty(T, H * 64, dtype=BF, device="cuda")
+        ws = torch.empty(L.ttt_seg_attention_workspace_size(), dtype=torch.uint8, device="cuda")
+        L.check(L.ttt_seg_attention(T, H, 64, seg, q, k, v, H * 64, None, out, H * 64, 0, T, ws, ws.numel()), "ttt_seg_attention")
+        torch.cuda.synchronize()
+        return out
+
+    want = run()
+    v[seg:2 * seg] = _garbage("huge", v)[seg:2 * seg]
+    got = run()
+    rest = torch.ones(T, dtype=torch.bool, device="cuda")
+    rest[seg:2 * seg] = False
+    assert torch.equal(got[rest], want[rest])
