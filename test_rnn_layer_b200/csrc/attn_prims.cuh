@@ -62,6 +62,8 @@ __device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
 // zero, so what comes out is below 2^-139 and becomes +0 as bf16.  A weight has to: at the clamp of -125 a masked
 // score (-infinity) got 2^-125, which is nothing beside a row's sum but 8 times a value of 3e38.  Between -126 and
 // here the result falls to that without a jump, off by less than 2^-126.
+// A NaN comes out as 2^128 - 2^104 (the bits 0x7fffffff that the arithmetic makes of any NaN, plus themselves shifted
+// left by 23), an infinity once it is bf16: the callers look for NaN in their rows' maxima, statistics or inputs.
 constexpr float kLowest = -126.99985f;
 
 // 2^x0, 2^x1 on the FMA pipe: a cubic of fma_exp2.cuh's kind (coefficients c0 .. c3) on a pair, with the packed f32x2

@@ -7,8 +7,10 @@
 // equal relative error (Lawson's iteration); then 2^n is added to the exponent
 // field: the bits of x + 1.5 * 2^23 shifted left by 23 are n << 23 (the shift
 // drops the bits of 1.5 * 2^23).  Inputs below -125 give 2^-125 (times the
-// polynomial's value at 0); NaN stays NaN.  Maximum relative error in fp32
-// over [-125, 8]: cubic 7.6e-5, quartic 2.7e-6 (tests/test_attention_exp2_poly.py).
+// polynomial's value at 0).  A NaN whose low mantissa bits are zero stays NaN;
+// 0x7fffffff, which CUDA's arithmetic makes of any NaN, becomes 0x7f7fffff, the
+// largest finite number.  Maximum relative error in fp32 over [-125, 8]: cubic
+// 7.6e-5, quartic 2.7e-6 (tests/test_attention_exp2_poly.py).
 #pragma once
 
 #include <stdint.h>
@@ -23,7 +25,7 @@ constexpr float kC3_0 = 0.9999281764030457f, kC3_1 = 0.6932609677314758f, kC3_2 
 constexpr float kC4_0 = 0.9999992847442627f, kC4_1 = 0.6931218504905701f, kC4_2 = 0.240247443318367f,
                 kC4_3 = 0.05591771379113197f, kC4_4 = 0.009570036083459854f;
 
-__device__ __forceinline__ float clamp_low(float x) { return x < -125.0f ? -125.0f : x; }   // NaN stays NaN
+__device__ __forceinline__ float clamp_low(float x) { return x < -125.0f ? -125.0f : x; }   // (NaN stays NaN here)
 
 __device__ __forceinline__ float scale_by_rint(float p, float t) {
     return __int_as_float(__float_as_int(p) + (__float_as_int(t) << 23));

@@ -140,6 +140,7 @@ __device__ __forceinline__ float softmax_tile(uint32_t (&s)[NC], float c, RowSta
         st.m = mt;
         st.l *= f;
     }
+    if (mt != mt) st.l = NAN;   // (the FMA pipe's exponential of a NaN may be finite)
     // nothing seen so far: any finite reference serves, as every weight is zero
     const float ref = st.m == -INFINITY ? 0.f : st.m;
     const uint64_t c2 = f2(c, c), nm2 = f2(-ref, -ref);

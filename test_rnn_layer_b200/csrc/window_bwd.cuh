@@ -62,7 +62,7 @@ __device__ __forceinline__ void grad_scores(uint32_t (&s)[COLS], uint32_t (&dp)[
     if (bad) {
 #pragma unroll
         for (int k = 0; k < COLS; ++k)
-            if ((bad >> k) & 1u) s[k] = 0x7fffffffu;
+            if ((bad >> k) & 1u) s[k] = dp[k] = 0x7fffffffu;   // (both: the FMA pipe's exponential of a NaN may be finite)
     }
     const uint64_t c2 = f2(c, c);
 #pragma unroll

@@ -52,3 +52,11 @@ def test_the_way_there_has_no_jump(poly):
     want = np.exp2(x.astype(np.float64))
     assert np.all(got >= 0) and np.all(np.abs(got - want) < 2.0 ** -126)
     assert np.all(np.diff(got) <= 2.0 ** -126 * 1e-4)      # falls with x (to the polynomial's error)
+
+
+def test_a_nan_comes_out_finite():
+    """CUDA's arithmetic makes 0x7fffffff of any NaN.  Shifted left by 23 and added to itself it is the largest finite
+    number, which is why the kernels look for NaN in their rows' maxima and inputs."""
+    bits = 0x7fffffff
+    got = np.array([(bits + (bits << 23)) & 0xFFFFFFFF], dtype=np.uint32).view(np.float32)
+    assert np.isnan(np.array([bits], dtype=np.uint32).view(np.float32)[0]) and got[0] == np.finfo(np.float32).max

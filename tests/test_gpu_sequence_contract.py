@@ -95,3 +95,35 @@ def test_segment_attention_takes_no_part_of_the_next_segment(seg):
     rest = torch.ones(T, dtype=torch.bool, device="cuda")
     rest[seg:2 * seg] = False
     assert torch.equal(got[rest], want[rest])
+
+
+# ---------------------------------------------------------------- values that are not finite
+@pytest.mark.parametrize("at", range(64, 81))
+@pytest.mark.parametrize("left", [0, 3])
+def test_a_key_that_is_nan_makes_its_rows_nan_at_every_place_of_a_tile(left, at):
+    T = 150
+    q, k, v = (_rand(i, T, 1, 64, dtype=BF) for i in range(3))
+    want = L.window_attention(q, k, v, left=left, want_lse=True)
+    k[at, 0, 5] = NAN
+    got = L.window_attention(q, k, v, left=left, want_lse=True, check_status=False)
+    assert L.ttt_mlp_status(got["workspace"]) == L.TTT_ERR_NONFINITE
+    rows = torch.zeros(T, dtype=torch.bool, device="cuda")
+    rows[at:at + left + 1] = True
+    assert got["out"][rows].isnan().all() and got["lse"][:, rows].isnan().all()
+    assert torch.equal(got["out"][~rows], want["out"][~rows]) and torch.equal(got["lse"][:, ~rows], want["lse"][:, ~rows])
+
+
+@pytest.mark.parametrize("at", range(128, 144))
+def test_query_gradients_of_rows_that_see_an_infinite_key_are_nan(at):
+    """Also where its score is -infinity (a weight of zero: 0 times infinity), at every place of a tile."""
+    T, left = 400, 60
+    q, k, v, g = (_rand(i, T, 1, 64, dtype=BF) for i in range(4))
+    q[:, 0, 9] = -q[:, 0, 9].abs() - 0.125
+    g *= 2.0 ** -10
+    k[at, 0, 9] = INF
+    r = L.window_attention(q, k, v, left=left, want_lse=True, check_status=False)
+    b = L.window_attention_backward(q, k, v, r["out"], r["lse"], g, left=left, check_status=False)
+    assert L.ttt_mlp_status(b["workspace"]) == L.TTT_ERR_NONFINITE
+    rows = torch.zeros(T, dtype=torch.bool, device="cuda")
+    rows[at:at + left + 1] = True
+    assert b["dq"][rows].isnan().all() and torch.isfinite(b["dq"][~rows]).all()
