@@ -507,8 +507,11 @@ TTT_API ttt_status ttt_rope(const ttt_rope_desc* desc, const void* X, int ld_x, 
  * Arithmetic as in ttt_seg_attention: bf16 operands, products accumulated in
  * fp32, softmax statistics in fp32, the weights rounded to bf16 for the
  * product with V, one rounding of the result.
- * A non-finite key, value or query makes the rows that see it (its own row)
- * NaN and is reported by the status; rows that do not see it are not affected.
+ * A non-finite value makes the rows that see it NaN, a query its own row (if it
+ * sees a key), and so does a key's score of NaN or +infinity; the status reports
+ * it.  A score of -infinity is a weight of zero, as in the formula; a row that
+ * has no other score is NaN and reported.  Rows that do not see the value or
+ * key are not affected.
  *
  *   desc      Tq, Tk rows of the query and key arrays (0 to 2^28), d = 64,
  *             Hq a multiple of Hk, left, right, sinks >= 0, scale > 0.
@@ -546,7 +549,9 @@ TTT_API ttt_status ttt_window_attention(const ttt_window_desc* desc, const int* 
  * a sink's later queries in chunks of 2,048 that are added in order).
  * A value of Q, K, V, Out or dOut that is not finite makes the gradients it
  * takes part in NaN (dQ of rows that see it, dK and dV of the keys that those
- * rows see) and is reported by the status; the others are not affected.
+ * rows see) and is reported by the status; the others are not affected.  (Where
+ * an infinite key has a score of -infinity its weight is zero: only the row's
+ * dQ is NaN, 0 times infinity.)
  *   workspace ttt_window_attention_backward_workspace_size(desc) bytes (a
  *             function of Tq, Tk, n_seq, Hq and Hk alone, and enough for the
  *             forward pass too).
@@ -580,6 +585,7 @@ TTT_API ttt_status ttt_window_attention_backward(const ttt_window_desc* desc, co
  *   lens      int [B] in device memory, the tokens so far, this one included.
  *             0: an idle request: Out = 0, nothing is stored.  Negative
  *             lengths count as 0 and set the status (TTT_ERR_INVALID_ARG).
+ *             What is not finite acts as in ttt_window_attention.
  *   Q, Out    bf16 [B, ld]; Out must not overlap Q, K_new or V_new.  No two
  *             requests may store into the same cache slots.
  *   workspace ttt_window_attention_decode_workspace_size(desc) bytes, 256-byte

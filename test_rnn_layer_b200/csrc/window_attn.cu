@@ -465,9 +465,12 @@ __global__ void __launch_bounds__(THREADS, 1) window_fwd_kernel(const __grid_con
             if (!has[0]) ml0.y = 0.f;
             if (!has[1]) ml1.y = 0.f;
             const float m = fmaxf(ml0.x, ml1.x), ref = m == -INFINITY ? 0.f : m;
-            const float f0 = ex2(ml0.x - ref), f1 = ex2(ml1.x - ref), l = ml0.y * f0 + ml1.y * f1;
+            // a row without keys; one whose scores are all -infinity has keys, and is NaN as in the formula
+            const int end = min(pos + p.w.right + 1, it.nk);
+            const bool empty = end <= max(pos - p.w.left, 0) && min(p.w.sinks, end) <= 0;
             // NaN sums stay (a half whose maximum is -infinity has factor 0 and, unless it saw a NaN, a finite sum)
-            const bool empty = m == -INFINITY && ml0.y == ml0.y && ml1.y == ml1.y;
+            const float f0 = ex2(ml0.x - ref), f1 = ex2(ml1.x - ref);
+            const float l = m == -INFINITY ? NAN : ml0.y * f0 + ml1.y * f1;
             const float inv = 1.0f / l, g0 = f0 * inv, g1 = f1 * inv;
             uint32_t o0[32], o1[32];
             tc::tmem_ld_32x32b_x32(tX + TM_O + 32 * y, o0);

@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(32 * kWarps) window_decode_kernel(const Window
     bool bad = false;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        v[e] = lj > 0.f ? oj[e] / lj : lj;   // an idle request is 0, a NaN sum stays
+        // an idle request is 0; a sum that is NaN, or 0 because every score is -infinity, makes NaN as in the formula
+        v[e] = total == 0 ? 0.f : lj > 0.f ? oj[e] / lj : NAN;
         bad |= !isfinite(v[e]);
     }
     if (bad) atomicOr(p.status, kStatusNonFinite);

@@ -127,3 +127,62 @@ def test_query_gradients_of_rows_that_see_an_infinite_key_are_nan(at):
     rows = torch.zeros(T, dtype=torch.bool, device="cuda")
     rows[at:at + left + 1] = True
     assert b["dq"][rows].isnan().all() and torch.isfinite(b["dq"][~rows]).all()
+
+
+@pytest.mark.parametrize("at", [8, 78, 79])
+@pytest.mark.parametrize("which", ["q", "k"])
+@pytest.mark.parametrize("residual", [False, True])
+def test_rows_whose_only_scores_are_minus_infinity_are_nan(which, at, residual):
+    """Such a row sees keys: it is not an empty one."""
+    T = 150
+    q, k, v, x = (_rand(i, T, 1, 64, dtype=BF) for i in range(4))
+    q[at, 0, 9], k[at, 0, 9] = -1.5, 1.5
+    how = dict(left=0, want_lse=True, residual=x if residual else None)
+    want = L.window_attention(q, k, v, **how)
+    (q if which == "q" else k)[at, 0, 9] *= INF
+    got = L.window_attention(q, k, v, check_status=False, **how)
+    assert L.ttt_mlp_status(got["workspace"]) == L.TTT_ERR_NONFINITE
+    rest = torch.arange(T, device="cuda") != at
+    assert got["out"][at].isnan().all() and got["lse"][0, at].isnan()
+    assert torch.equal(got["out"][rest], want["out"][rest]) and torch.equal(got["lse"][:, rest], want["lse"][:, rest])
+
+
+@pytest.mark.parametrize("left", [0, 40])
+def test_rows_that_see_no_key_stay_empty(left):
+    """More queries than keys: rows in front of the first key, with queries that are not finite among them."""
+    Tq, Tk = 300, 100
+    q, k, v = _rand(0, Tq, 2, 64, dtype=BF), _rand(1, Tk, 1, 64, dtype=BF), _rand(2, Tk, 1, 64, dtype=BF)
+    q[7, 1, 3], q[150, 0, 0] = NAN, -INF
+    r = L.window_attention(q, k, v, left=left, want_lse=True)
+    assert not r["out"][:200].any() and (r["lse"][:, :200] == -INF).all() and torch.isfinite(r["lse"][:, 200:]).all()
+
+
+@pytest.mark.parametrize("at", [1, 14, 15, 33])
+def test_a_score_of_minus_infinity_beside_others_is_a_weight_of_zero(at):
+    """As in the formula: the same bits as a score that is very low."""
+    T = 60
+    q, k, v = (_rand(i, T, 1, 64, dtype=BF) for i in range(3))
+    q[:, 0, 9] = -q[:, 0, 9].abs() - 0.125
+    how = dict(left=100, want_lse=True)
+    k[at, 0, 9] = 1e30
+    want = L.window_attention(q, k, v, **how)
+    k[at, 0, 9] = INF
+    got = L.window_attention(q, k, v, check_status=False, **how)
+    assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+
+
+@pytest.mark.parametrize("which", ["q", "k"])
+def test_decode_of_scores_of_minus_infinity(which):
+    """One visible key: NaN and reported, beside an idle request; among others: a weight of zero."""
+    B, slots, Hq = 4, 40, 2
+    q, ck, cv = _rand(0, B, Hq, 64, dtype=BF), _rand(1, B, slots, 1, 64, dtype=BF), _rand(2, B, slots, 1, 64, dtype=BF)
+    lens = _ints([0, 1, 30, 40])
+    q[:, 0, 9], ck[:, 0, 0, 9] = -1.5, 1.5
+    ck[2, 0, 0, 9] = 1e30
+    want = L.window_attention_decode(q, ck, cv, lens, left=100)
+    (q[1, 0] if which == "q" else ck[1, 0, 0])[9] *= INF
+    ck[2, 0, 0, 9] = INF if which == "k" else 1e30
+    got = L.window_attention_decode(q, ck, cv, lens, left=100, check_status=False)
+    assert L.ttt_mlp_status(got["workspace"]) == L.TTT_ERR_NONFINITE
+    assert got["out"][1, 0].isnan().all() and not got["out"][0].any()
+    assert torch.equal(got["out"][2, 0], want["out"][2, 0]) and torch.equal(got["out"][3], want["out"][3])
