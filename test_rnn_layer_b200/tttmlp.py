@@ -532,13 +532,16 @@ def ttt_gated_scan_step(B, D, form, x_dtype, F, ld_f, X, ld_x, H, H_out, Y, ld_y
 
 
 class _Elsewhere:
-    """The tensors' device current and, if one is given, `stream` (new tensors then belong to it)."""
+    """The tensors' device current and, if one is given, `stream` (new tensors then belong to it and are filled on it)."""
 
     __slots__ = ("stack",)
 
     def __init__(self, device, stream):
         self.stack = [torch.cuda.device(device)]
-        if isinstance(stream, torch.cuda.Stream):
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):   # a handle; 0 and 1 name the default stream
+                handle = int(stream)
+                stream = torch.cuda.ExternalStream(handle, device) if handle > 1 else torch.cuda.default_stream(device)
             self.stack.append(torch.cuda.stream(stream))
 
     def __enter__(self):

@@ -186,3 +186,45 @@ def test_decode_of_scores_of_minus_infinity(which):
     assert L.ttt_mlp_status(got["workspace"]) == L.TTT_ERR_NONFINITE
     assert got["out"][1, 0].isnan().all() and not got["out"][0].any()
     assert torch.equal(got["out"][2, 0], want["out"][2, 0]) and torch.equal(got["out"][3], want["out"][3])
+
+
+# ---------------------------------------------------------------- streams and numbers
+def test_a_raw_stream_handle_orders_every_fill():
+    """Buffers that the functions make and fill themselves are filled on the stream that the kernels run on."""
+    T, D = 500, 64
+    cu = _ints([0, 200, 450])
+    q, k, v, g = (_rand(i, T, 2, 64, dtype=BF) for i in range(4))
+    f, x, dy = (_rand(9 + i, T, D, dtype=BF) for i in range(3))
+    mask = dict(left=60, cu_q=cu, cu_k=cu)
+    cache = torch.stack([k[:8], v[:8]])
+    lens = _ints([5])
+    w0 = L.window_attention(q, k, v, want_lse=True, **mask)
+    s0 = L.gated_scan(f, x, cu=cu, want_chunk_states=True)
+
+    def run(stream):
+        how = dict(check_status=False, stream=stream)
+        w = L.window_attention(q, k, v, want_lse=True, **mask, **how)
+        b = L.window_attention_backward(q, k, v, w0["out"], w0["lse"], g, **mask, **how)
+        s = L.gated_scan(f, x, cu=cu, **how)
+        t = L.gated_scan_backward(f, x, dy, s0["chunk_states"], cu=cu, **how)
+        d = L.window_attention_decode(q[:1], cache[:1], cache[1:], lens, left=9, **how)
+        return [w["out"], w["lse"], b["dq"], b["dk"], b["dv"], s["y"], t["df"], t["dx"], d["out"]]
+
+    want = run(None)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(400_000_000)      # a fifth of a second on the current stream
+    got = run(side.cuda_stream)
+    assert not torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(zip(got, want)):
+        assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("handle", [0, 1, 2])   # the default stream's two names, this thread's
+def test_streams_by_their_fixed_handles(handle):
+    q = _rand(0, 40, 1, 64, dtype=BF)
+    cu = _ints([0, 30])
+    a, b = (L.window_attention(q, q, q, left=3, cu_q=cu, cu_k=cu, stream=s)["out"] for s in (handle, None))
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
