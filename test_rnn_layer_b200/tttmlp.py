@@ -11,6 +11,7 @@ import contextlib
 import ctypes
 import functools
 import os
+from operator import index
 
 import torch
 
@@ -626,7 +627,8 @@ def _dtype_code(x, name) -> int:
 
 
 _ROPE_KEYS = {"kind", "factor", "length", "low", "high", "amplitude"}
-# Descriptors by their sizes, with a reference for the call: building one costs as much as a launch.
+# Descriptors by their sizes, with a reference for the call: building one costs as much as a launch.  They are looked up
+# by Python's own numbers, which do not change: a tensor of one element would be found again whatever it holds by then.
 def _descriptor(_type, *args):
     desc = _type(*args)
     desc.ref = ctypes.byref(desc)
@@ -651,9 +653,10 @@ def rope(x, positions=None, *, pos0: int = 0, rot: int | None = None, layout: st
     sc = scaling or {}
     if not (_ROPE_KEYS >= sc.keys() and sc.get("kind", "none") in TTT_ROPE_SCALINGS):
         raise ValueError(f"scaling {scaling}")
-    desc = _rope_desc(T, H, d, d if rot is None else rot, TTT_ROPE_LAYOUTS[layout], code,
-                      TTT_ROPE_SCALINGS[sc.get("kind", "none")], base, sc.get("factor", 1.0), sc.get("length", 0.0),
-                      sc.get("low", 0.0), sc.get("high", 0.0), sc.get("amplitude", 1.0))
+    desc = _rope_desc(T, H, d, d if rot is None else index(rot), TTT_ROPE_LAYOUTS[layout], code,
+                      TTT_ROPE_SCALINGS[sc.get("kind", "none")], float(base), float(sc.get("factor", 1.0)),
+                      float(sc.get("length", 0.0)), float(sc.get("low", 0.0)), float(sc.get("high", 0.0)),
+                      float(sc.get("amplitude", 1.0)))
     if positions is not None:
         _dense(positions, (T,), torch.int32, dev, "positions")
     with _place(dev, stream):
@@ -668,7 +671,8 @@ def rope(x, positions=None, *, pos0: int = 0, rot: int | None = None, layout: st
 def _window_desc(q, k, n_seq, left, right, sinks, scale):
     _ask(q.is_cuda and q.dim() == 3 and k.dim() == 3, "q and k: [T, H, 64] on a GPU")
     (Tq, Hq, d), (Tk, Hk, _) = q.shape, k.shape
-    return _window_sizes(Tq, Tk, n_seq, Hq, Hk, d, left, right, sinks, d ** -0.5 if scale is None else scale)
+    return _window_sizes(Tq, Tk, index(n_seq), Hq, Hk, d, index(left), index(right), index(sinks),
+                         d ** -0.5 if scale is None else float(scale))
 
 
 def window_attention_workspace(q, k, n_seq: int = 1, backward: bool = False) -> torch.Tensor:
@@ -741,7 +745,7 @@ def _decode_desc(q, cache, left, sinks, scale):
     _ask(cache.stride(3) == 1, "the cache's last axis must be dense")
     B, slots, Hk, d = cache.shape
     s0, s1, s2, _ = cache.stride()
-    return _decode_sizes(B, q.shape[1], Hk, d, slots, left, sinks, d ** -0.5 if scale is None else scale,
+    return _decode_sizes(B, q.shape[1], Hk, d, slots, index(left), index(sinks), d ** -0.5 if scale is None else float(scale),
                          s0 if B > 1 else 0, s1 if slots > 1 else d, s2 if Hk > 1 else 0)   # (axes of one: any stride)
 
 
@@ -786,7 +790,7 @@ def window_attention_decode(q, cache_k, cache_v, lens, *, left: int, sinks: int 
 def _gated_desc(x, n_seq, form, dirs):
     _ask(x.dim() == 2, "x: [T, D]")
     T, D = x.shape
-    return _gated_sizes(T, D, n_seq, TTT_GATE_FORMS[form], DIRS[dirs], _dtype_code(x, "x"))
+    return _gated_sizes(T, D, index(n_seq), TTT_GATE_FORMS[form], DIRS[dirs], _dtype_code(x, "x"))
 
 
 def gated_scan_workspace(x, n_seq: int = 1) -> torch.Tensor:

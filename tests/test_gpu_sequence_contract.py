@@ -228,3 +228,20 @@ def test_streams_by_their_fixed_handles(handle):
     a, b = (L.window_attention(q, q, q, left=3, cu_q=cu, cu_k=cu, stream=s)["out"] for s in (handle, None))
     torch.cuda.synchronize()
     assert torch.equal(a, b)
+
+
+def test_numbers_are_taken_at_the_call():
+    """A number given as a tensor of one element that changes between calls."""
+    q, k, v = (_rand(i, 50, 2, 64, dtype=BF) for i in range(3))
+    cache, lens = torch.stack([k[:8], v[:8]]), _ints([6])
+    scale, base, factor, left = torch.tensor(0.125), torch.tensor(100.0), torch.tensor(1.0), torch.tensor(5)
+
+    def run(scale, base, factor, left):
+        return [L.window_attention(q, k, v, left=left, scale=scale)["out"],
+                L.window_attention_decode(q[:1], cache[:1], cache[1:], lens, left=left, scale=scale)["out"],
+                L.rope(q, base=base, scaling={"kind": "linear", "factor": factor})]
+
+    for s, b, f, n in ((0.125, 100.0, 1.0, 5), (0.5, 1000.0, 4.0, 2)):
+        scale.fill_(s), base.fill_(b), factor.fill_(f), left.fill_(n)
+        for x, y in zip(run(scale, base, factor, left), run(s, b, f, n)):
+            assert torch.equal(x, y), (s, b, f, n)

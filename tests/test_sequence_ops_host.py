@@ -236,3 +236,30 @@ def test_struct_layouts_match_the_header():
     assert ctypes.sizeof(L.ttt_window_desc) == 10 * 4
     assert ctypes.sizeof(L.ttt_window_decode_desc) == 8 * 4 + 3 * 8
     assert ctypes.sizeof(L.ttt_gated_scan_desc) == 6 * 4
+
+
+# ---------------------------------------------------------------- tensor-level functions
+class _Like:
+    """What the checks look at of a tensor on a GPU."""
+    is_cuda = True
+
+    def __init__(self, *shape):
+        self.shape = shape
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, k=None):
+        s = tuple(int(np.prod(self.shape[i + 1:], dtype=np.int64)) for i in range(len(self.shape)))
+        return s if k is None else s[k]
+
+
+def test_descriptors_hold_the_numbers_of_the_call():
+    """A number given as a tensor of one element that changes between calls."""
+    import torch
+    q, k, cache = _Like(8, 4, 64), _Like(8, 2, 64), _Like(8, 16, 2, 64)
+    scale, left = torch.tensor(0.125), torch.tensor(5)
+    for s, n in ((0.125, 5), (0.5, 2)):
+        scale.fill_(s), left.fill_(n)
+        for d in (L._window_desc(q, k, 1, left, 0, 0, scale), L._decode_desc(q, cache, left, 0, scale)):
+            assert (d.scale, d.left) == (s, n)
