@@ -630,6 +630,8 @@ _ROPE_KEYS = {"kind", "factor", "length", "low", "high", "amplitude"}
 # Descriptors by their sizes, with a reference for the call: building one costs as much as a launch.  They are looked up
 # by Python's own numbers, which do not change: a tensor of one element would be found again whatever it holds by then.
 def _descriptor(_type, *args):
+    for (name, kind), n in zip(_type._fields_, args):
+        _ask(kind is not ctypes.c_int or -2 ** 31 <= n < 2 ** 31, f"{name}={n} does not fit 32 bits")   # ctypes cuts it
     desc = _type(*args)
     desc.ref = ctypes.byref(desc)
     return desc
@@ -657,6 +659,7 @@ def rope(x, positions=None, *, pos0: int = 0, rot: int | None = None, layout: st
                       TTT_ROPE_SCALINGS[sc.get("kind", "none")], float(base), float(sc.get("factor", 1.0)),
                       float(sc.get("length", 0.0)), float(sc.get("low", 0.0)), float(sc.get("high", 0.0)),
                       float(sc.get("amplitude", 1.0)))
+    _ask(-2 ** 31 <= pos0 < 2 ** 31, "pos0 does not fit 32 bits")
     if positions is not None:
         _dense(positions, (T,), torch.int32, dev, "positions")
     with _place(dev, stream):
@@ -866,6 +869,7 @@ def gated_scan_step(f, x, h, *, form: str = "convex", y=None, h_out=None, stream
     """One token of each row: returns (y, h_out) for f, x [B, D] and the state h fp32 [B, D] (h_out may be h)."""
     dev, code = x.get_device(), _dtype_code(x, "x")
     B, D = x.shape
+    _ask(B < 2 ** 31 and D < 2 ** 31, "f, x: too many rows or columns")
     _dense(h, (B, D), torch.float32, dev, "h")
     with _place(dev, stream):
         y = torch.empty((B, D), dtype=x.dtype, device=dev) if y is None else y

@@ -245,3 +245,16 @@ def test_numbers_are_taken_at_the_call():
         scale.fill_(s), base.fill_(b), factor.fill_(f), left.fill_(n)
         for x, y in zip(run(scale, base, factor, left), run(s, b, f, n)):
             assert torch.equal(x, y), (s, b, f, n)
+
+
+def test_numbers_past_32_bits_are_refused():
+    """The interface's integers have 32 bits: a larger number must not lose its upper ones."""
+    q = _rand(0, 30, 1, 64, dtype=BF)
+    cache, lens = q[:16][None], _ints([6])
+    for n in (2 ** 32, 2 ** 32 + 5, 2 ** 31, -2 ** 32 + 1):
+        for call in (lambda: L.window_attention(q, q, q, left=n), lambda: L.window_attention(q, q, q, left=3, right=n),
+                     lambda: L.window_attention(q, q, q, left=3, sinks=n), lambda: L.rope(q, pos0=n), lambda: L.rope(q, rot=n),
+                     lambda: L.window_attention_decode(q[:1], cache, cache, lens, left=n),
+                     lambda: L.window_attention_decode(q[:1], cache, cache, lens, left=3, sinks=n)):
+            with pytest.raises((ValueError, L.TTTError)):
+                call()

@@ -263,3 +263,14 @@ def test_descriptors_hold_the_numbers_of_the_call():
         scale.fill_(s), left.fill_(n)
         for d in (L._window_desc(q, k, 1, left, 0, 0, scale), L._decode_desc(q, cache, left, 0, scale)):
             assert (d.scale, d.left) == (s, n)
+
+
+def test_numbers_past_32_bits_are_refused():
+    """A descriptor's integers have 32 bits: neither sizes nor windows may lose their upper ones."""
+    q, k = _Like(8, 4, 64), _Like(8, 2, 64)
+    for n in (2 ** 31, 2 ** 32 + 5, -2 ** 31 - 1):
+        for call in (lambda: L._window_desc(q, k, 1, n, 0, 0, None), lambda: L._window_desc(q, k, 1, 3, n, 0, None),
+                     lambda: L._window_desc(q, _Like(n, 2, 64), 1, 3, 0, 0, None),
+                     lambda: L._decode_desc(q, _Like(8, n, 2, 64), 3, 0, None), lambda: L._gated_sizes(n, 8, 1, 0, 0, 0)):
+            with pytest.raises(ValueError):
+                call()
