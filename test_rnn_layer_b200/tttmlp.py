@@ -672,7 +672,7 @@ def rope(x, positions=None, *, pos0: int = 0, rot: int | None = None, layout: st
 
 
 def _window_desc(q, k, n_seq, left, right, sinks, scale):
-    _ask(q.is_cuda and q.dim() == 3 and k.dim() == 3, "q and k: [T, H, 64] on a GPU")
+    _ask(q.is_cuda and q.dim() == 3 and k.dim() == 3 and q.shape[2] == k.shape[2], "q and k: [T, H, 64] on a GPU")
     (Tq, Hq, d), (Tk, Hk, _) = q.shape, k.shape
     return _window_sizes(Tq, Tk, index(n_seq), Hq, Hk, d, index(left), index(right), index(sinks),
                          d ** -0.5 if scale is None else float(scale))

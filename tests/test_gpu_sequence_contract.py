@@ -258,3 +258,12 @@ def test_numbers_past_32_bits_are_refused():
                      lambda: L.window_attention_decode(q[:1], cache, cache, lens, left=3, sinks=n)):
             with pytest.raises((ValueError, L.TTTError)):
                 call()
+
+
+def test_keys_of_another_head_width_are_refused():
+    q, k = _rand(0, 30, 2, 64, dtype=BF), _rand(1, 30, 2, 128, dtype=BF)
+    r = L.window_attention(q, q, q, left=3, want_lse=True)
+    with pytest.raises(ValueError):
+        L.window_attention(q, k, k, left=3)
+    with pytest.raises(ValueError):
+        L.window_attention_backward(q, k, k, r["out"], r["lse"], q.clone(), left=3)

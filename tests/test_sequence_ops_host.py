@@ -274,3 +274,9 @@ def test_numbers_past_32_bits_are_refused():
                      lambda: L._decode_desc(q, _Like(8, n, 2, 64), 3, 0, None), lambda: L._gated_sizes(n, 8, 1, 0, 0, 0)):
             with pytest.raises(ValueError):
                 call()
+
+
+@pytest.mark.parametrize("d", [32, 128])
+def test_keys_of_another_head_width_are_refused(d):
+    with pytest.raises(ValueError):
+        L._window_desc(_Like(8, 4, 64), _Like(8, 2, d), 1, 3, 0, 0, None)
