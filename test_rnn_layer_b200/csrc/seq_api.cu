@@ -302,6 +302,14 @@ extern "C" TTT_API ttt_status ttt_window_attention_decode(const ttt_window_decod
         overlap(Out, q.B, ld_out, wq, 2, V_new, q.B, ld_new, wk, 2))
         return set_error(TTT_ERR_INVALID_ARG, "Out overlaps Q, K_new or V_new");
     if (q.ld_request == 0 && q.B > 1 && K_new) return set_error(TTT_ERR_INVALID_ARG, "the requests store into the same cache slots");
+    if (K_new) {
+        // a request's new key of one head must not land in another head's: heads lie within a slot or slots within a head
+        const bool within_slot = (q.Hk - 1) * q.ld_head + q.d <= q.ld_slot && q.ld_head >= q.d;
+        const bool within_head = (q.slots - 1) * q.ld_slot + q.d <= q.ld_head;
+        if (q.Hk > 1 && !within_slot && !within_head)
+            return set_error(TTT_ERR_INVALID_ARG, "ld_slot=%lld, ld_head=%lld: heads share cache slots", q.ld_slot, q.ld_head);
+        if (K_cache == V_cache) return set_error(TTT_ERR_INVALID_ARG, "keys and values are stored into the same cache");
+    }
     WindowDecodeArgs a{};
     a.B = q.B; a.Hq = q.Hq; a.Hk = q.Hk; a.slots = q.slots; a.left = q.left; a.sinks = q.sinks; a.scale = q.scale;
     a.ld_request = q.ld_request; a.ld_slot = q.ld_slot; a.ld_head = q.ld_head;

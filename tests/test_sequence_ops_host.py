@@ -280,3 +280,20 @@ def test_numbers_past_32_bits_are_refused():
 def test_keys_of_another_head_width_are_refused(d):
     with pytest.raises(ValueError):
         L._window_desc(_Like(8, 4, 64), _Like(8, 2, d), 1, 3, 0, 0, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(ld_head=0), dict(ld_head=32),                              # one place for both heads, half of one
+    dict(ld_slot=64, ld_head=64), dict(ld_slot=64, ld_head=128),    # a slot's second head is a later slot's first
+    dict(ld_slot=64, ld_head=64 * 31),                              # heads of 32 slots, one too near
+    dict(ld_slot=120), dict(V=P[3])])
+def test_decode_refuses_new_keys_that_overwrite_each_other(no_gpu, bad):
+    assert _decode(**bad) == L.TTT_ERR_INVALID_ARG and L.ttt_last_error()
+
+
+@pytest.mark.parametrize("good", [
+    dict(), dict(ld_slot=64, ld_head=64 * 32, ld_request=64 * 64), dict(Hk=1, Hq=4, ld_head=0, ld_slot=64),
+    dict(K_new=None, V_new=None, ld_head=0), dict(K_new=None, V_new=None, V=P[3]), dict(ld_slot=136, ld_head=72)])
+def test_decode_accepts_its_cache_layouts(no_gpu, good):
+    """Without a GPU the launch fails, behind the checks."""
+    assert _decode(**good) == L.TTT_ERR_CUDA
