@@ -1111,10 +1111,12 @@ ttt_status ttt_mlp_backward(const ttt_mlp_desc* desc, const void* X, const void*
 ttt_status ttt_mlp_status(void* workspace, ttt_stream_t stream_) {
     if (!workspace) return fail(TTT_ERR_INVALID_ARG, "workspace is NULL");
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
-    CUDA_TRY(cudaStreamSynchronize(s));
+    // on the caller's stream alone: the default stream may be busy with other work, and a memset there could still be on
+    // its way when the workspace has found another use
     int word = 0;
-    CUDA_TRY(cudaMemcpy(&word, workspace, sizeof(int), cudaMemcpyDeviceToHost));
-    CUDA_TRY(cudaMemset(workspace, 0, sizeof(int)));
+    CUDA_TRY(cudaMemcpyAsync(&word, workspace, sizeof(int), cudaMemcpyDeviceToHost, s));
+    CUDA_TRY(cudaMemsetAsync(workspace, 0, sizeof(int), s));
+    CUDA_TRY(cudaStreamSynchronize(s));
     if (word & kStatusTimeout) return fail(TTT_ERR_TIMEOUT, "a bounded wait inside a scan kernel expired");
     if (word & kStatusBadOffsets)
         return fail(TTT_ERR_INVALID_ARG, "sequence offsets or lengths in device memory fall or leave the arrays");

@@ -267,3 +267,16 @@ def test_keys_of_another_head_width_are_refused():
         L.window_attention(q, k, k, left=3)
     with pytest.raises(ValueError):
         L.window_attention_backward(q, k, k, r["out"], r["lse"], q.clone(), left=3)
+
+
+def test_status_waits_for_its_own_stream_only():
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    ws.view(torch.int32)[0] = 1
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)      # a fifth of a second on the default stream
+    assert L.ttt_mlp_status(ws, side) == L.TTT_ERR_NONFINITE
+    assert not torch.cuda.current_stream().query()
+    assert L.ttt_mlp_status(ws, side) == L.TTT_OK
+    torch.cuda.synchronize()
+    assert not ws.any()
