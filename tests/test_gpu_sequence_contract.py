@@ -280,3 +280,34 @@ def test_status_waits_for_its_own_stream_only():
     assert L.ttt_mlp_status(ws, side) == L.TTT_OK
     torch.cuda.synchronize()
     assert not ws.any()
+
+
+# ---------------------------------------------------------------- gated recurrence
+@pytest.mark.parametrize("dirs", ["fwd", "rev"])
+@pytest.mark.parametrize("form", ["sum", "convex", "unit"])
+@pytest.mark.parametrize("value", [INF, -INF])
+def test_scan_takes_infinite_logits_as_open_and_closed_gates(value, form, dirs):
+    """a = 1 or 0: every output stays finite, and what no such gate touches keeps its bits."""
+    cu, D, at = [0, 300, 700, 1500], 72, 500
+    T = cu[-1]
+    f, x, dy, h0 = _rand(1, T, D) + 2, _rand(2, T, D), _rand(3, T, D), _rand(4, 3, D)
+    how = dict(form=form, dirs=dirs, cu=_ints(cu))
+
+    def both():
+        r = L.gated_scan(f, x, h0=h0, want_state=True, want_chunk_states=True, **how)
+        b = L.gated_scan_backward(f, x, dy, r["chunk_states"], h0=h0, want_dh0=True, **how)
+        return [r["y"], b["df"], b["dx"]], [r["h_T"], b["dh0"]]
+
+    f[at, 5] = 200.0 if value > 0 else -200.0
+    rows0, states0 = both()
+    f[at, 5] = value
+    rows, states = both()           # (the status is looked at: nothing is reported)
+    for a, b in zip(rows + states, rows0 + states0):
+        assert torch.equal(a, b) and torch.isfinite(a).all()
+    y, df, dx = rows
+    prev = y[at - 1, 5] if dirs == "fwd" else y[at + 1, 5]
+    gain = {"sum": 1.0, "convex": 0.0, "unit": 0.0}[form] if value > 0 else 1.0
+    # gates: a and s(a) to 2^-20; the closed gate's a is below 2^-115
+    want = (prev if value > 0 else 0.0) + gain * x[at, 5]
+    assert abs(float(y[at, 5] - want)) <= 2.0 ** -20 * (abs(float(prev)) + abs(float(x[at, 5])))
+    assert abs(float(df[at, 5])) <= 2.0 ** -100
