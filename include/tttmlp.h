@@ -428,8 +428,8 @@ TTT_API ttt_status ttt_linear_forward_host(const ttt_mlp_desc* desc, const void*
  * Packed sequences.  Where a call takes `cu`, rows [cu[s], cu[s+1]) of its
  * arrays are sequence s (0 <= s < n_seq): n_seq + 1 ints in DEVICE memory,
  * cu[0] = 0, not falling, cu[n_seq] at most the number of rows.  Sequences may
- * be empty.  Rows from cu[n_seq] on are neither read nor written (they may
- * hold anything, NaN included).  cu = NULL is one sequence of every row
+ * be empty.  Rows from cu[n_seq] on take no part and are not written: they
+ * may hold anything, NaN included, and change no bit of a result.  cu = NULL is one sequence of every row
  * (n_seq must be 1).  The host cannot see the values: offsets that fall or
  * leave the array are cut to it, never followed out of bounds, the outputs are
  * then undefined, and ttt_mlp_status(workspace, stream) returns

@@ -2,8 +2,9 @@
 // for each pair of a head's first `rot` columns, u = position * frequency.
 //
 // The angle is taken in turns: position * turns[i] in 64 bits, less its whole
-// part, so that a far position (2^20 and more radians) keeps its angle to
-// 2^-31 turns; the rest is sinpi/cospi in fp32.  One angle serves every head
+// part, so that a far position (2^20 and more radians) keeps its angle: to
+// 2^-31 turns or better there, to 2^-26 once the rest, at most half a turn, is
+// cast to fp32 for sinpi/cospi.  One angle serves every head
 // of a row, so a block first fills a table of cos and sin for its rows in
 // shared memory and then streams the heads past it, 16 bytes at a time and
 // three units a thread under way while the table is made.  Bound by memory:

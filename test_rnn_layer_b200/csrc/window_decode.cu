@@ -4,7 +4,7 @@
 // one request and key head (and sixteen of the query heads that share it, padded to the matrix instruction's 16
 // rows); its warps take tiles of 32 visible keys in turn, each through a ring of its own (cp.async, 16 bytes a
 // lane, rows in a 128-byte swizzle; no barrier between warps; two stages, so that three CTAs share an SM: 64 requests
-// x 16,388 keys in 364 us, 5.9 TB/s, against 421 us with three stages and two CTAs).  S = Q K^T and O += P V run on mma.sync with the
+// x 16,388 keys in 377 us, 5.7 TB/s, against 427 us with three stages and two CTAs).  S = Q K^T and O += P V run on mma.sync with the
 // softmax's statistics in registers: one token gives far too few rows for tcgen05's 128, and the tensor time is
 // a few percent of the loads'.  The warps' partial results join in shared memory, the CTAs' in the first CTA's
 // (distributed shared memory), in a fixed order: no workspace, no second launch.
@@ -261,7 +261,7 @@ cudaError_t launch_window_decode(const WindowDecodeArgs& a, cudaStream_t s) {
     const long long items = (long long)a.B * a.Hk * ((G + kHeads - 1) / kHeads);
     const long long keys = std::min<long long>(a.slots, (long long)a.left + 1 + a.sinks);   // at most, per request
     // split the keys while the card has room (four waves of three CTAs per SM, for requests of unequal lengths: the
-    // 364 us above are 388 with half as many, 476 with a quarter) and every warp keeps a tile
+    // 377 us above are 405 with half as many, 491 with a quarter) and every warp keeps a tile
     int cs = 1;
     while (cs < kMaxCluster && items * cs < 12LL * sms && keys > (long long)cs * kWarps * kTile) cs *= 2;
     if (items * cs > 0x7fffffffLL) return cudaErrorInvalidValue;

@@ -90,10 +90,13 @@ struct ItemQueue {
     }
 };
 // The order in which few blocks of unequal work are drawn: the longest first, so that the CTAs end together (forward
-// pass of 13 requests of up to 1,725 rows, 12 heads, window 1,024: 60 -> 49 us).  Ranking them takes 2 to 3 us of a
+// pass of 13 requests of up to 1,725 rows, 12 heads, window 1,024: 60 -> 49 us).  Ranking them takes 2 to 4 us of a
 // launch, so it is left out where blocks differ little: one sequence (16,384 rows, forward and backward: 580 us, 584
 // with it), a narrow window (5 sequences, 256 keys to both sides: 148 us, 152 with it), and where every CTA has one item.
 // A warp ranks up to kOrder blocks; with more, an item is a small part of a CTA's work.
+// The window's width is a rough sign of unequal work.  On 13 requests of 20 to 760 rows behind up to 1,500 cached ones
+// the order is worth nothing at 256 keys, and 8 us at 512 to 768, where it is not used (53 -> 45, 57 -> 47); short
+// sequences under a wide window are all alike and pay for it (40 of 128 rows: forward 35 -> 39 us, backward 80 -> 84).
 constexpr int kOrder = 128;
 inline bool ordered(const WindowArgs& p, long long n_blocks, int ctas) {
     return n_blocks <= kOrder && n_blocks * p.Hq > ctas && p.n_seq > 1 && (long long)p.left + p.right >= 768;
@@ -128,8 +131,6 @@ __device__ __forceinline__ int order_blocks(uint8_t* order, int n, Work work) {
     __syncwarp();
     return used;
 }
-// most items of a launch: the counter and its overshoot stay inside an int
-constexpr long long kMaxItems = (1LL << 31) - (1 << 20);
 
 }  // namespace win
 }  // namespace ttt
