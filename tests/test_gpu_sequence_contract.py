@@ -230,6 +230,33 @@ def test_streams_by_their_fixed_handles(handle):
     assert torch.equal(a, b)
 
 
+def test_the_capturing_stream_by_its_handle():
+    """Inside a capture: fills and outputs belong to the graph, and a replay on new inputs gives what a call gives."""
+    q, k, v, g = (_rand(i, 300, 2, 64, dtype=BF) for i in range(4))
+    cu = _ints([0, 120, 290])
+    ws = L.window_attention_workspace(q, k, 2, backward=True)
+    mask = dict(left=50, cu_q=cu, cu_k=cu, check_status=False)
+
+    def run(ws, stream):
+        r = L.window_attention(q, k, v, want_lse=True, workspace=ws, stream=stream, **mask)
+        b = L.window_attention_backward(q, k, v, r["out"], r["lse"], g, workspace=ws, stream=stream, **mask)
+        return [r["out"], r["lse"], b["dq"], b["dk"], b["dv"]]
+
+    run(ws, None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(ws, torch.cuda.current_stream().cuda_stream)
+    for t in (q, k, v, g):
+        t.copy_(_rand(9, *t.shape, dtype=BF) * (1 + t.float().mean()))
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    got = [t.clone() for t in out]
+    for a, b in zip(got, run(None, None)):
+        assert torch.equal(a, b)
+
+
 def test_numbers_are_taken_at_the_call():
     """A number given as a tensor of one element that changes between calls."""
     q, k, v = (_rand(i, 50, 2, 64, dtype=BF) for i in range(3))
