@@ -588,7 +588,8 @@ TTT_API ttt_status ttt_window_attention_backward(const ttt_window_desc* desc, co
  *             What is not finite acts as in ttt_window_attention.
  *   Q, Out    bf16 [B, ld]; Out must not overlap Q, K_new, V_new or a cache.
  *             Where K_new is given, no two requests and no two heads may store
- *             into the same place, nor keys and values into the same cache.
+ *             into the same place, nor different keys and values into the same
+ *             cache.
  *   workspace ttt_window_attention_decode_workspace_size(desc) bytes, 256-byte
  *             aligned.  The caller zeroes it once after allocating it; the
  *             call does not clear the status word (one launch less), which

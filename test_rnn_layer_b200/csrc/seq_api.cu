@@ -308,7 +308,7 @@ extern "C" TTT_API ttt_status ttt_window_attention_decode(const ttt_window_decod
         const bool within_head = (q.slots - 1) * q.ld_slot + q.d <= q.ld_head;
         if (q.Hk > 1 && !within_slot && !within_head)
             return set_error(TTT_ERR_INVALID_ARG, "ld_slot=%lld, ld_head=%lld: heads share cache slots", q.ld_slot, q.ld_head);
-        if (K_cache == V_cache) return set_error(TTT_ERR_INVALID_ARG, "keys and values are stored into the same cache");
+        if (K_cache == V_cache && K_new != V_new) return set_error(TTT_ERR_INVALID_ARG, "keys and values are stored into the same cache");
     }
     WindowDecodeArgs a{};
     a.B = q.B; a.Hq = q.Hq; a.Hk = q.Hk; a.slots = q.slots; a.left = q.left; a.sinks = q.sinks; a.scale = q.scale;

@@ -293,7 +293,8 @@ def test_decode_refuses_new_keys_that_overwrite_each_other(no_gpu, bad):
 
 @pytest.mark.parametrize("good", [
     dict(), dict(ld_slot=64, ld_head=64 * 32, ld_request=64 * 64), dict(Hk=1, Hq=4, ld_head=0, ld_slot=64),
-    dict(K_new=None, V_new=None, ld_head=0), dict(K_new=None, V_new=None, V=P[3]), dict(ld_slot=136, ld_head=72)])
+    dict(K_new=None, V_new=None, ld_head=0), dict(K_new=None, V_new=None, V=P[3]), dict(ld_slot=136, ld_head=72),
+    dict(V=P[3], V_new=P[1])])
 def test_decode_accepts_its_cache_layouts(no_gpu, good):
     """Without a GPU the launch fails, behind the checks."""
     assert _decode(**good) == L.TTT_ERR_CUDA
