@@ -280,6 +280,9 @@ TTT_API ttt_status ttt_mlp_forward_heads(const ttt_mlp_desc* desc, int h0, int h
  *               the status word, cleared by the call; ttt_mlp_status(workspace,
  *               stream) reports non-finite outputs (TTT_ERR_NONFINITE) and
  *               expired waits (TTT_ERR_TIMEOUT).
+ * Finite values of one segment do not reach another's rows.  One that is not
+ * finite may make rows of its own segment non-finite, and of an earlier one
+ * whose last key tile (128 rows) reaches it; the status reports them.
  * All pointers are device pointers, 16-byte aligned.  Asynchronous on
  * `stream`; no allocation.  TTT_ERR_UNSUPPORTED for d != 64.
  */
@@ -428,12 +431,12 @@ TTT_API ttt_status ttt_linear_forward_host(const ttt_mlp_desc* desc, const void*
  * Packed sequences.  Where a call takes `cu`, rows [cu[s], cu[s+1]) of its
  * arrays are sequence s (0 <= s < n_seq): n_seq + 1 ints in DEVICE memory,
  * cu[0] = 0, not falling, cu[n_seq] at most the number of rows.  Sequences may
- * be empty.  Rows from cu[n_seq] on take no part and are not written: they
- * may hold anything, NaN included, and change no bit of a result.  cu = NULL is one sequence of every row
- * (n_seq must be 1).  The host cannot see the values: offsets that fall or
- * leave the array are cut to it, never followed out of bounds, the outputs are
- * then undefined, and ttt_mlp_status(workspace, stream) returns
- * TTT_ERR_INVALID_ARG.
+ * be empty.  Rows from cu[n_seq] on take no part and are not written: they may
+ * hold anything, NaN included, and change no bit of a result.  cu = NULL is
+ * one sequence of every row (n_seq must be 1).  The host cannot see the
+ * values: offsets that fall or leave the array are cut to it, never followed
+ * out of bounds, the outputs are then undefined, and ttt_mlp_status(workspace,
+ * stream) returns TTT_ERR_INVALID_ARG.
  *
  * All pointers are device pointers, 16-byte aligned, row strides (ld) count
  * elements and are multiples of 8.  The calls are asynchronous on `stream`,
